@@ -27,6 +27,16 @@
  *                      positioning"; its outputs are the arrangement the
  *                      unpermute's formulas invert (see its section below).
  *
+ * and the experts' own work between the two reorderings:
+ *
+ *   moe_quant_fp8   -- rows to e4m3 with an FP32 scale for each 128 elements.
+ *   moe_grouped_matmul_fp8 -- e4m3 rows times their expert's e4m3 weights (a scale for
+ *                      each 128 x 128 block), group by group of the batching's
+ *                      group_list or as one dense product; optionally with SwiGLU, and
+ *                      with SwiGLU and the quantising of its result.
+ *   moe_layer       -- the whole expert layer (both products, SwiGLU, the weighted sum
+ *                      over a token's experts) for at most 64 tokens.
+ *
  * Conventions shared by every entry point
  *   - All array pointers are DEVICE pointers owned by the caller.  The library
  *     never allocates, frees or synchronises; it only enqueues kernels on
@@ -78,6 +88,7 @@ extern "C" {
 #define FFNWB_DT_FP32 3 /* unpermute and permute */
 #define FFNWB_DT_INT32 4 /* moe_update_expert ids */
 #define FFNWB_DT_INT64 5 /* moe_update_expert ids */
+#define FFNWB_DT_FP8_E4M3 6 /* 1 sign, 4 exponent (bias 7), 3 mantissa bits; largest 448, no infinity, NaN 0x7f / 0xff */
 
 /* ------------------------------------------------------------------------------------------
  * FFN-worker batching (aclnnFfnWorkerBatching API page).
@@ -456,6 +467,165 @@ int moe_update_expert_workspace_size(const moe_update_expert_desc* d, size_t* ws
 /* Validates again, then enqueues the update on `stream` (one launch). */
 int moe_update_expert(const moe_update_expert_desc* d, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Rows to e4m3 with a scale for each 128 elements: the input of moe_grouped_matmul_fp8.
+ *
+ * For row i and block b (elements 128 b .. 128 b + 127 of the row, the last block shorter):
+ *   scale[i, b] = max(a / 448, 2^-126), a = the largest |x| of the block (FP32 division,
+ *                 rounded to nearest)
+ *   q[i, h]     = e4m3(x[i, h] / scale[i, b]): the FP32 quotient, then e4m3, both rounded to
+ *                 nearest, ties to even.
+ * A block holding a NaN gets scale NaN and NaN elements; one holding an infinity (and no NaN)
+ * gets scale inf, NaN for its infinities and 0 for the rest, so every value it stands for is
+ * NaN.  Rows i >= *actual_rows are not written.
+ * ------------------------------------------------------------------------------------------ */
+#define FFNWB_FP8_BLOCK 128
+
+typedef struct moe_quant_fp8_desc {
+  int32_t dtype;             /* of x: FFNWB_DT_FP16, _BF16 or _FP32 */
+  int32_t reserved0;         /* must be 0 */
+  int64_t num_rows;          /* R >= 0 */
+  int64_t hidden;            /* H in (0, 2^20]; R * ceil(H / 128) < 2^30 */
+  int64_t x_row_stride;      /* bytes, a multiple of the element size; 0 = H * element size */
+  int64_t q_row_stride;      /* bytes; 0 = H */
+  int64_t scale_row_stride;  /* elements; 0 = ceil(H / 128) */
+  const void* x;             /* [R, H] */
+  const int64_t* actual_rows;/* [1] rows to take (clamped to [0, R]), e.g. the batching's
+                                actual_token_num; NULL = R */
+  void* q;                   /* [R, H] e4m3 */
+  float* scale;              /* [R, ceil(H / 128)] */
+  /* Optional timing hooks (hipEvent_t) around the kernel, as in ffnwb_batching_desc. */
+  void* ev_quant_begin;
+  void* ev_quant_end;
+} moe_quant_fp8_desc;
+
+/* Validates *d and returns the workspace size (0) (host only).  Errors:
+   FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes, x, q or scale NULL), FFNWB_ERR_PARAM_INVALID (dtype,
+   sizes, a stride below its row or above 2^40, x not aligned to its element size, reserved0 != 0). */
+int moe_quant_fp8_workspace_size(const moe_quant_fp8_desc* d, size_t* ws_bytes);
+
+/* Validates again, then enqueues the quantising on `stream` (one launch). */
+int moe_quant_fp8(const moe_quant_fp8_desc* d, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The experts' products on e4m3 rows.
+ *
+ * Rows 0 .. R-1 of x lie group by group: the first group_list[0].count rows belong to expert
+ * group_list[0].key, and so on ({key, count} pairs as ffnwb_batching writes them).  For a row
+ * i of expert e, with block sums over the 128 columns of block b:
+ *   p[i, n] = sum_b x_scale[i, b] * w_scale[e, n / 128, b] * sum_{k in b} x[i, k] * w[e, n, k]
+ * FFNWB_EPI_NONE:   y[i, n] = p[i, n], n < N.
+ * FFNWB_EPI_SWIGLU: N = 2 F (gate rows of w, then up rows),
+ *   y[i, f] = g * sigmoid(g) * u, g = p[i, f], u = p[i, F + f], f < F.
+ * y is rounded once to out_dtype; with out_dtype FFNWB_DT_FP8_E4M3 (SwiGLU only) y and
+ * y_scale are the rows quantised as moe_quant_fp8 does.  Sums are held in FP32.
+ *
+ * Without a group_list (NULL, num_groups = 0, num_experts = 1) all R rows are one group: the
+ * plain product of x with w.  A pair with a count <= 0 has no rows; a pair whose key lies
+ * outside [0, E) has rows, and they are left unwritten; counts past R rows are cut.  Rows of
+ * no group are left unwritten.
+ * ------------------------------------------------------------------------------------------ */
+#define FFNWB_EPI_NONE   0
+#define FFNWB_EPI_SWIGLU 1
+
+typedef struct moe_grouped_matmul_fp8_desc {
+  int32_t epilogue;          /* FFNWB_EPI_NONE or FFNWB_EPI_SWIGLU */
+  int32_t out_dtype;         /* FFNWB_DT_FP16, _BF16, _FP32; _FP8_E4M3 with SwiGLU */
+  int64_t num_rows;          /* R in [0, 2^24] */
+  int64_t in_features;       /* K in (0, 2^18], a multiple of 16 */
+  int64_t out_features;      /* N in (0, 2^18], rows of one expert's w; SwiGLU: a multiple of 32 */
+  int64_t num_experts;       /* E in [1, 8192] */
+  int64_t num_groups;        /* pairs of group_list, in [1, 8192]; 0 without one */
+  int64_t x_row_stride;      /* bytes, a multiple of 16; 0 = K */
+  int64_t x_scale_stride;    /* elements between rows; 0 = ceil(K / 128) */
+  int64_t y_row_stride;      /* bytes, a multiple of the element size; 0 = dense */
+  int64_t y_scale_stride;    /* elements between rows; 0 = ceil(F / 128) */
+
+  /* Inputs. */
+  const void* x;             /* [R, K] e4m3, 16-byte aligned */
+  const float* x_scale;      /* [R, ceil(K / 128)] */
+  const void* w;             /* [E, N, K] e4m3, dense, 16-byte aligned */
+  const float* w_scale;      /* [E, ceil(N / 128), ceil(K / 128)], dense */
+  const int64_t* group_list; /* [num_groups, 2] or NULL */
+
+  /* Outputs. */
+  void* y;                   /* [R, N] (SwiGLU: [R, F]) of out_dtype */
+  float* y_scale;            /* [R, ceil(F / 128)] (FFNWB_DT_FP8_E4M3 only) */
+
+  /* Optional timing hooks (hipEvent_t) around the product's kernel, as in
+     ffnwb_batching_desc. */
+  void* ev_matmul_begin;
+  void* ev_matmul_end;
+} moe_grouped_matmul_fp8_desc;
+
+/* Validates *d and returns the workspace size in bytes (host only).  Errors:
+   FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes or a required array NULL), FFNWB_ERR_PARAM_INVALID
+   (a code, range, multiple or alignment above violated, a stride below its row or above
+   2^32, more than 2^24 tiles of output; group_list given without
+   num_groups or the other way round; num_experts != 1 without a group_list). */
+int moe_grouped_matmul_fp8_workspace_size(const moe_grouped_matmul_fp8_desc* d, size_t* ws_bytes);
+
+/* Validates again, then enqueues the product on `stream`. */
+int moe_grouped_matmul_fp8(const moe_grouped_matmul_fp8_desc* d, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * A whole expert layer for a few tokens, in two launches.
+ *
+ * T = num_tokens, K = slots of a token, H = hidden, F = inter_size, E = num_experts.
+ *   h(e, t) = silu(w13[e, 0:F] x[t]) * (w13[e, F:2F] x[t])          silu(g) = g * sigmoid(g)
+ *   y[t]    = sum over the experts e of token t of c(e, t) * (w2[e] h(e, t))
+ *   c(e, t) = sum of expert_scales[t, k] over the slots k with expert_ids[t, k] = e that
+ *             active_mask leaves active (1 each without expert_scales)
+ * Products with weights stand for the weight times its 128 x 128 block's scale.  Ids outside
+ * [0, E) (the -1 of moe_update_expert) and inactive slots take no part; a token without any
+ * gets a row of zeros.  Activations keep the 16-bit type of x, h is held to 16 significant
+ * bits, sums in FP32, and y is rounded once.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct moe_layer_desc {
+  int32_t dtype;             /* of x and y: FFNWB_DT_FP16 or _BF16 */
+  int32_t weight_dtype;      /* FFNWB_DT_FP8_E4M3, or FFNWB_DT_BF16 when dtype is BF16 */
+  int32_t id_dtype;          /* FFNWB_DT_INT32 or _INT64 */
+  int32_t scale_dtype;       /* of expert_scales: FFNWB_DT_FP16, _BF16 or _FP32; ignored without */
+  int64_t num_tokens;        /* T in [0, 64] */
+  int64_t slots;             /* K in (0, 64] */
+  int64_t hidden;            /* H in (0, 2^18], a multiple of 16 */
+  int64_t inter_size;        /* F in (0, 2^17], a multiple of 16 */
+  int64_t num_experts;       /* E in [1, 8192] */
+  int64_t x_row_stride;      /* bytes, a multiple of 16; 0 = dense */
+  int64_t y_row_stride;      /* bytes, a multiple of the element size; 0 = dense */
+  int64_t expert_ids_stride;    /* elements between tokens; 0 = K */
+  int64_t expert_scales_stride; /* elements between tokens; 0 = K */
+  int64_t active_mask_stride;   /* elements between tokens; 0 = K */
+
+  /* Inputs. */
+  const void* x;             /* [T, H], 16-byte aligned */
+  const void* expert_ids;    /* [T, K] of id_dtype */
+  const void* expert_scales; /* [T, K] of scale_dtype, or NULL */
+  const uint8_t* active_mask;/* [T, K] bool (moe_update_expert's balanced_active_mask), or NULL */
+  const void* w13;           /* [E, 2 F, H] of weight_dtype, dense, 16-byte aligned */
+  const float* w13_scale;    /* [E, ceil(2 F / 128), ceil(H / 128)]; NULL exactly with BF16 weights */
+  const void* w2;            /* [E, H, F] of weight_dtype, dense, 16-byte aligned */
+  const float* w2_scale;     /* [E, ceil(H / 128), ceil(F / 128)]; NULL exactly with BF16 weights */
+
+  /* Output. */
+  void* y;                   /* [T, H] of dtype */
+
+  /* Optional timing hooks (hipEvent_t): `begin` is recorded before the first kernel, `end`
+     takes the second kernel's completion.  NULL = not recorded. */
+  void* ev_layer_begin;
+  void* ev_layer_end;
+} moe_layer_desc;
+
+/* Validates *d and returns the workspace size in bytes (host only).  Errors:
+   FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes or a required array NULL), FFNWB_ERR_PARAM_INVALID
+   (a code, range, multiple or alignment above violated, a stride below its row or above
+   2^40, min(T K, E) * F / 16 of 2^24 - 1 or more; scales of weights given with
+   BF16 weights, or missing with e4m3 ones). */
+int moe_layer_workspace_size(const moe_layer_desc* d, size_t* ws_bytes);
+
+/* Validates again, then enqueues the layer on `stream`. */
+int moe_layer(const moe_layer_desc* d, void* workspace, size_t ws_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* ffnwb_status_string(int status);
 
@@ -468,6 +638,9 @@ size_t ffnwb_batching_ctx_desc_size(void);
 size_t moe_unpermute_desc_size(void);
 size_t moe_permute_desc_size(void);
 size_t moe_update_expert_desc_size(void);
+size_t moe_quant_fp8_desc_size(void);
+size_t moe_grouped_matmul_fp8_desc_size(void);
+size_t moe_layer_desc_size(void);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,8 @@ Parity status per function (see each module header for the pins):
   the W1 switch and the non-padded ``out_index``/``permute_token_id`` outputs
   are pinned only by properties (ranges, permutation, stability) --
   "parity unpinned" beyond those.
+* ``expert_ffn`` -- pinned (torch's CPU e4m3 conversion, plain dequantised products, a loop
+  over tokens and slots).
 * ``permute``   -- pinned (round trips through the unpermute oracle, a torch
   nonzero / cumsum construction, brute force of the capacity blocks).
 """

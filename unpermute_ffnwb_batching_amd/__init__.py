@@ -1,6 +1,7 @@
-"""Python binding of libffnwb (include/ffnwb.h): MoE token reordering on MI355X.
+"""Python binding of libffnwb (include/ffnwb.h): MoE token reordering and the experts'
+products on MI355X.
 
-Argument marshalling only -- every step of both operations runs in the library's HIP
+Argument marshalling only -- every step of every operation runs in the library's HIP
 kernels.  PyTorch provides device memory and the current HIP stream.
 
 The names mirror the C ABI:
@@ -10,12 +11,16 @@ The names mirror the C ABI:
 * ``moe_unpermute_workspace_size`` / ``moe_unpermute`` / ``moe_unpermute_noalloc``
 * ``moe_permute_workspace_size`` / ``moe_permute``
 * ``moe_update_expert_workspace_size`` / ``moe_update_expert``
+* ``moe_quant_fp8_workspace_size`` / ``moe_quant_fp8``
+* ``moe_grouped_matmul_fp8_workspace_size`` / ``moe_grouped_matmul_fp8``
+* ``moe_layer_workspace_size`` / ``moe_layer``
 * ``ffnwb_status_string``, ``ffnwb_abi_version``
 
-``ffnwb_batching``, ``moe_unpermute`` and ``moe_permute`` take torch tensors, allocate any
-output or workspace the caller did not pass, fill the C descriptor and enqueue the call
-on the current stream.  ``BatchingCall`` / ``UnpermuteCall`` / ``PermuteCall`` build the
-descriptor once for repeated launches (benchmarks, graph capture).
+``ffnwb_batching``, ``moe_unpermute`` and the other ``moe_`` calls take torch tensors,
+allocate any output or workspace the caller did not pass, fill the C descriptor and
+enqueue the call on the current stream.  ``BatchingCall`` / ``UnpermuteCall`` /
+``PermuteCall`` / ``QuantFp8Call`` / ``GroupedMatmulFp8Call`` / ``LayerCall`` build the
+descriptor once for repeated launches (serving loops, benchmarks, graph capture).
 
 The library must be built (``python -m unpermute_ffnwb_batching_amd.build``); importing
 works without it, but every call then raises ``RuntimeError``: there is no fallback.
@@ -34,7 +39,8 @@ from ._abi import (FFNWB_OK, FFNWB_ERR_PARAM_NULLPTR, FFNWB_ERR_PARAM_INVALID,  
                    FFNWB_DT_FP16, FFNWB_DT_BF16, FFNWB_DT_INT8, FFNWB_DT_FP32,
                    FFNWB_CTX_BYTES, FFNWB_CTX_SHAPE, FFNWB_CTX_POLLING, FFNWB_CTX_POINTER,
                    FFNWB_CTX_BUFFER, FFNWB_DT_INT32, FFNWB_DT_INT64, BatchingDesc, BatchingCtxDesc,
-                   UnpermuteDesc, PermuteDesc, UpdateExpertDesc)
+                   UnpermuteDesc, PermuteDesc, UpdateExpertDesc, FFNWB_DT_FP8_E4M3, FFNWB_FP8_BLOCK,
+                   FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libffnwb.so")
 _lib = None
@@ -66,6 +72,15 @@ def lib():
         L.moe_permute.argtypes = [ctypes.POINTER(PermuteDesc), vp, sz, vp]
         L.moe_update_expert_workspace_size.argtypes = [ctypes.POINTER(UpdateExpertDesc), ctypes.POINTER(sz)]
         L.moe_update_expert.argtypes = [ctypes.POINTER(UpdateExpertDesc), vp, sz, vp]
+        for name, desc in (("moe_quant_fp8", QuantFp8Desc), ("moe_grouped_matmul_fp8", GroupedMatmulFp8Desc),
+                           ("moe_layer", LayerDesc)):
+            getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
+            getattr(L, name + "_workspace_size").restype = ctypes.c_int
+            getattr(L, name).argtypes = [ctypes.POINTER(desc), vp, sz, vp]
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name + "_desc_size").restype = sz
+            if getattr(L, name + "_desc_size")() != ctypes.sizeof(desc):
+                raise RuntimeError("libffnwb descriptor layout does not match the Python binding")
         for f in ("ffnwb_batching_workspace_size", "ffnwb_batching", "ffnwb_batching_ctx_workspace_size",
                   "ffnwb_batching_ctx", "moe_unpermute_workspace_size",
                   "moe_unpermute", "moe_unpermute_noalloc", "moe_permute_workspace_size", "moe_permute", "moe_update_expert_workspace_size",
@@ -774,3 +789,255 @@ def moe_update_expert(expert_ids, eplb_table, *, stream=None, **kw):
     dict of output tensors, allocated on that stream."""
     with _on(stream):
         return UpdateExpertCall(expert_ids, eplb_table, **kw).run(stream)
+
+
+# ----------------------------------------------------------------------------- experts' products
+
+_FP8 = torch.float8_e4m3fn
+_OUT_CODE = {**_FLOAT_CODE, _FP8: FFNWB_DT_FP8_E4M3}
+
+
+def _blocks(n):
+    return -(-n // FFNWB_FP8_BLOCK)
+
+
+def _row_elems(t):
+    """A 2-D tensor's row stride in elements; 0 (dense) where a single row leaves torch's stride free."""
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _row_bytes(t):
+    return _row_elems(t) * t.element_size()
+
+
+class _Call:
+    """A descriptor with its outputs and workspace, launched on the tensors' own device."""
+
+    def _bind(self, name, desc, device, out, keep, workspace, ws_bytes):
+        if workspace is None and ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        elif workspace is not None:
+            _check_tensor(workspace, "workspace", device, (torch.uint8,))
+            _req(workspace.numel() >= ws_bytes, f"workspace has {workspace.numel()} bytes, the call needs {ws_bytes}")
+        self.desc, self.out, self.workspace, self.ws_bytes = desc, out, workspace, ws_bytes
+        self._name, self._device, self._keep = name, device, keep
+        self._alloc_stream = _alloc_stream(device)
+        self._args = (ctypes.byref(desc), _ptr(workspace), ctypes.c_size_t(ws_bytes))
+
+    def run(self, stream=None):
+        """Enqueue the call on ``stream`` (default: the current stream of the tensors' device)."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        else:
+            _req(stream.device == self._device, f"stream is on {stream.device}, the tensors on {self._device}")
+        if torch.cuda.current_device() == self._device.index:
+            st = getattr(lib(), self._name)(*self._args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self._device):
+                st = getattr(lib(), self._name)(*self._args, stream.cuda_stream)
+        if st != FFNWB_OK:
+            raise FfnwbError(st, self._name)
+        _record_on([self.workspace, *self._keep, *self.out.values()], stream, self._alloc_stream)
+        return self.out
+
+
+def _workspace_size(name, desc):
+    n = ctypes.c_size_t(0)
+    st = getattr(lib(), name + "_workspace_size")(ctypes.byref(desc), ctypes.byref(n))
+    if st != FFNWB_OK:
+        raise FfnwbError(st, name + "_workspace_size")
+    return n.value
+
+
+def moe_quant_fp8_workspace_size(desc):
+    return _workspace_size("moe_quant_fp8", desc)
+
+
+def moe_grouped_matmul_fp8_workspace_size(desc):
+    return _workspace_size("moe_grouped_matmul_fp8", desc)
+
+
+def moe_layer_workspace_size(desc):
+    return _workspace_size("moe_layer", desc)
+
+
+class QuantFp8Call(_Call):
+    """A prepared moe_quant_fp8 call.
+
+    ``x`` [R, H] (float16 / bfloat16 / float32; rows may be strided).  ``actual_rows``: an
+    int64 tensor of one element, the rows to take (the batching's ``actual_token_num``); the
+    rows behind them are left as they were.  Outputs ``q`` [R, H] float8_e4m3fn and ``scale``
+    [R, ceil(H / 128)] float32, allocated unless given in ``out`` (rows may be strided).
+    """
+
+    def __init__(self, x, *, actual_rows=None, out=None, ev_quant=None):
+        _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [R, H]")
+        dev = x.device
+        _check_rows(x, "x", dev, tuple(_FLOAT_CODE))
+        R, H = x.shape
+        _req(H > 0, "x must have at least one column")
+        if actual_rows is not None:
+            _check_numel(actual_rows, "actual_rows", dev, (torch.int64,), 1)
+        out = dict(out or {})
+        want = {"q": ((R, H), _FP8), "scale": ((R, _blocks(H)), torch.float32)}
+        for k, t in out.items():
+            _req(k in want, f"unknown output {k!r}")
+            _check_rows(t, f"out[{k!r}]", dev, (want[k][1],))
+            _req(tuple(t.shape) == want[k][0], f"out[{k!r}] must be {want[k][0]}")
+        for k, (shape, dtype) in want.items():
+            if k not in out:
+                out[k] = torch.empty(shape, dtype=dtype, device=dev)
+        d = QuantFp8Desc()
+        d.dtype = _FLOAT_CODE[x.dtype]
+        d.num_rows, d.hidden = R, H
+        d.x_row_stride, d.q_row_stride, d.scale_row_stride = _row_bytes(x), _row_bytes(out["q"]), _row_elems(out["scale"])
+        d.x, d.actual_rows, d.q, d.scale = _ptr(x), _ptr(actual_rows), _ptr(out["q"]), _ptr(out["scale"])
+        if ev_quant is not None:
+            d.ev_quant_begin, d.ev_quant_end = _event_handle(ev_quant[0]), _event_handle(ev_quant[1])
+        self._bind("moe_quant_fp8", d, dev, out, [x, actual_rows], None, moe_quant_fp8_workspace_size(d))
+
+
+def moe_quant_fp8(x, *, stream=None, **kw):
+    """Quantise rows to e4m3 with a scale for each 128 elements, once on ``stream`` (default:
+    the current stream); returns dict(q, scale), allocated on that stream."""
+    with _on(stream):
+        return QuantFp8Call(x, **kw).run(stream)
+
+
+class GroupedMatmulFp8Call(_Call):
+    """A prepared moe_grouped_matmul_fp8 call.
+
+    ``x`` [R, K] float8_e4m3fn with ``x_scale`` [R, ceil(K / 128)] (rows of both may be
+    strided), ``w`` [E, N, K] float8_e4m3fn with ``w_scale`` [E, ceil(N / 128), ceil(K / 128)].
+    ``group_list`` int64 [G, 2]: the {expert, row count} pairs of the batching, rows in that
+    order; None: one dense product (E = 1, ``w`` and ``w_scale`` may also be 2-D).
+    ``epilogue`` FFNWB_EPI_NONE or FFNWB_EPI_SWIGLU (N = 2 F, gate rows then up rows).
+    ``out_dtype`` float16 / bfloat16 / float32, or float8_e4m3fn with SwiGLU, which also
+    returns ``y_scale``.  K must be a multiple of 16, F too.
+    """
+
+    def __init__(self, x, x_scale, w, w_scale, *, group_list=None, epilogue=FFNWB_EPI_NONE, out_dtype=torch.bfloat16,
+                 out=None, workspace=None, ev_matmul=None):
+        _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [R, K]")
+        dev = x.device
+        _check_rows(x, "x", dev, (_FP8,))
+        R, K = x.shape
+        _check_rows(x_scale, "x_scale", dev, (torch.float32,))
+        _req(tuple(x_scale.shape) == (R, _blocks(K)), f"x_scale must be [{R}, {_blocks(K)}]")
+        _req(isinstance(w, torch.Tensor) and isinstance(w_scale, torch.Tensor), "w and w_scale must be tensors")
+        if group_list is None and w.dim() == 2 and w_scale.dim() == 2:
+            w, w_scale = w[None], w_scale[None]
+        _req(w.dim() == 3 and w.shape[2] == K, f"w must be [E, N, K={K}]")
+        E, N = w.shape[0], w.shape[1]
+        _check_tensor(w, "w", dev, (_FP8,))
+        _check_tensor(w_scale, "w_scale", dev, (torch.float32,), (E, _blocks(N), _blocks(K)))
+        if group_list is not None:
+            _req(isinstance(group_list, torch.Tensor) and group_list.dim() == 2 and group_list.shape[1] == 2,
+                 "group_list must be [G, 2]")
+            _check_tensor(group_list, "group_list", dev, (torch.int64,))
+        _req(out_dtype in _OUT_CODE, f"out_dtype {out_dtype} is not float16, bfloat16, float32 or float8_e4m3fn")
+        cols = N // 2 if epilogue == FFNWB_EPI_SWIGLU else N
+        out = dict(out or {})
+        want = {"y": ((R, cols), out_dtype)}
+        if out_dtype == _FP8:
+            want["y_scale"] = ((R, _blocks(cols)), torch.float32)
+        for k, t in out.items():
+            _req(k in want, f"unknown output {k!r}")
+            _check_rows(t, f"out[{k!r}]", dev, (want[k][1],))
+            _req(tuple(t.shape) == want[k][0], f"out[{k!r}] must be {want[k][0]}")
+        for k, (shape, dtype) in want.items():
+            if k not in out:
+                out[k] = torch.empty(shape, dtype=dtype, device=dev)
+        d = GroupedMatmulFp8Desc()
+        d.epilogue, d.out_dtype = int(epilogue), _OUT_CODE[out_dtype]
+        d.num_rows, d.in_features, d.out_features, d.num_experts = R, K, N, E
+        d.num_groups = group_list.shape[0] if group_list is not None else 0
+        d.x_row_stride, d.x_scale_stride = _row_bytes(x), _row_elems(x_scale)
+        d.y_row_stride = _row_bytes(out["y"])
+        d.x, d.x_scale, d.w, d.w_scale = _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale)
+        d.group_list = _ptr(group_list)
+        d.y = _ptr(out["y"])
+        if "y_scale" in out:
+            d.y_scale, d.y_scale_stride = _ptr(out["y_scale"]), _row_elems(out["y_scale"])
+        if ev_matmul is not None:
+            d.ev_matmul_begin, d.ev_matmul_end = _event_handle(ev_matmul[0]), _event_handle(ev_matmul[1])
+        self._bind("moe_grouped_matmul_fp8", d, dev, out, [x, x_scale, w, w_scale, group_list], workspace,
+                   moe_grouped_matmul_fp8_workspace_size(d))
+
+
+def moe_grouped_matmul_fp8(x, x_scale, w, w_scale, *, stream=None, **kw):
+    """Run the experts' products once on ``stream`` (default: the current stream); returns
+    dict(y) or, for float8_e4m3fn outputs, dict(y, y_scale), allocated on that stream."""
+    with _on(stream):
+        return GroupedMatmulFp8Call(x, x_scale, w, w_scale, **kw).run(stream)
+
+
+class LayerCall(_Call):
+    """A prepared moe_layer call: a whole expert layer for at most 64 tokens.
+
+    ``x`` [T, H] (float16 / bfloat16), ``expert_ids`` [T, K] int32 / int64,
+    ``expert_scales`` [T, K] (float16 / bfloat16 / float32) or None (1 each), ``active_mask``
+    [T, K] bool or None; the rows of all four may be strided.  ``w13`` [E, 2 F, H] (gate rows
+    then up rows) and ``w2`` [E, H, F] float8_e4m3fn with ``w13_scale`` [E, ceil(2 F / 128),
+    ceil(H / 128)] and ``w2_scale`` [E, ceil(H / 128), ceil(F / 128)], or bfloat16 without
+    scales (bfloat16 ``x``).  H and F must be multiples of 16.  Output ``y`` [T, H].
+    """
+
+    def __init__(self, x, expert_ids, w13, w2, *, w13_scale=None, w2_scale=None, expert_scales=None, active_mask=None,
+                 out=None, workspace=None, ev_layer=None):
+        _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [T, H]")
+        dev = x.device
+        _check_rows(x, "x", dev, (torch.float16, torch.bfloat16))
+        T, H = x.shape
+        _req(isinstance(expert_ids, torch.Tensor) and expert_ids.dim() == 2 and expert_ids.shape[0] == T,
+             f"expert_ids must be [T={T}, K]")
+        _check_rows(expert_ids, "expert_ids", dev, tuple(_ID_CODE))
+        K = expert_ids.shape[1]
+        for t, name, dtypes in ((expert_scales, "expert_scales", tuple(_FLOAT_CODE)), (active_mask, "active_mask", _BYTES)):
+            if t is not None:
+                _check_rows(t, name, dev, dtypes)
+                _req(tuple(t.shape) == (T, K), f"{name} must be [{T}, {K}]")
+        _req(isinstance(w13, torch.Tensor) and w13.dim() == 3 and w13.shape[1] % 2 == 0 and w13.shape[2] == H,
+             f"w13 must be [E, 2 F, H={H}]")
+        E, F = w13.shape[0], w13.shape[1] // 2
+        _check_tensor(w13, "w13", dev, (_FP8, torch.bfloat16))
+        _check_tensor(w2, "w2", dev, (w13.dtype,), (E, H, F))
+        fp8 = w13.dtype == _FP8
+        _req((w13_scale is not None) == fp8 and (w2_scale is not None) == fp8,
+             "w13_scale and w2_scale are given exactly with float8_e4m3fn weights")
+        if fp8:
+            _check_tensor(w13_scale, "w13_scale", dev, (torch.float32,), (E, _blocks(2 * F), _blocks(H)))
+            _check_tensor(w2_scale, "w2_scale", dev, (torch.float32,), (E, _blocks(H), _blocks(F)))
+        out = dict(out or {})
+        for k, t in out.items():
+            _req(k == "y", f"unknown output {k!r}")
+            _check_rows(t, "out['y']", dev, (x.dtype,))
+            _req(tuple(t.shape) == (T, H), f"out['y'] must be {(T, H)}")
+        if "y" not in out:
+            out["y"] = torch.empty((T, H), dtype=x.dtype, device=dev)
+        d = LayerDesc()
+        d.dtype = _FLOAT_CODE[x.dtype]
+        d.weight_dtype = FFNWB_DT_FP8_E4M3 if fp8 else FFNWB_DT_BF16
+        d.id_dtype = _ID_CODE[expert_ids.dtype]
+        d.scale_dtype = _FLOAT_CODE[expert_scales.dtype] if expert_scales is not None else 0
+        d.num_tokens, d.slots, d.hidden, d.inter_size, d.num_experts = T, K, H, F, E
+        d.x_row_stride, d.y_row_stride, d.expert_ids_stride = _row_bytes(x), _row_bytes(out["y"]), _row_elems(expert_ids)
+        d.x, d.expert_ids, d.w13, d.w2 = _ptr(x), _ptr(expert_ids), _ptr(w13), _ptr(w2)
+        d.w13_scale, d.w2_scale = _ptr(w13_scale), _ptr(w2_scale)
+        if expert_scales is not None:
+            d.expert_scales, d.expert_scales_stride = _ptr(expert_scales), _row_elems(expert_scales)
+        if active_mask is not None:
+            d.active_mask, d.active_mask_stride = _ptr(active_mask), _row_elems(active_mask)
+        d.y = _ptr(out["y"])
+        if ev_layer is not None:
+            d.ev_layer_begin, d.ev_layer_end = _event_handle(ev_layer[0]), _event_handle(ev_layer[1])
+        self._bind("moe_layer", d, dev, out,
+                   [x, expert_ids, w13, w2, w13_scale, w2_scale, expert_scales, active_mask], workspace,
+                   moe_layer_workspace_size(d))
+
+
+def moe_layer(x, expert_ids, w13, w2, *, stream=None, **kw):
+    """Run a whole expert layer once on ``stream`` (default: the current stream); returns
+    dict(y), allocated on that stream."""
+    with _on(stream):
+        return LayerCall(x, expert_ids, w13, w2, **kw).run(stream)

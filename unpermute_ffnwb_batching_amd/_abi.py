@@ -19,6 +19,11 @@ FFNWB_DT_INT8 = 2
 FFNWB_DT_FP32 = 3
 FFNWB_DT_INT32 = 4
 FFNWB_DT_INT64 = 5
+FFNWB_DT_FP8_E4M3 = 6
+
+FFNWB_FP8_BLOCK = 128
+FFNWB_EPI_NONE = 0
+FFNWB_EPI_SWIGLU = 1
 
 FFNWB_CTX_BYTES = 1024
 FFNWB_CTX_SHAPE = 1
@@ -94,4 +99,38 @@ class UpdateExpertDesc(ctypes.Structure):
         ("expert_ids_stride", _i64), ("eplb_table_stride", _i64), ("expert_scales_stride", _i64),
         ("threshold_stride", _i64), ("active_mask_stride", _i64), ("out_ids_stride", _i64),
         ("out_mask_stride", _i64),
+    ]
+
+
+class QuantFp8Desc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("reserved0", _i32),
+        ("num_rows", _i64), ("hidden", _i64),
+        ("x_row_stride", _i64), ("q_row_stride", _i64), ("scale_row_stride", _i64),
+        ("x", _vp), ("actual_rows", _vp), ("q", _vp), ("scale", _vp),
+        ("ev_quant_begin", _vp), ("ev_quant_end", _vp),
+    ]
+
+
+class GroupedMatmulFp8Desc(ctypes.Structure):
+    _fields_ = [
+        ("epilogue", _i32), ("out_dtype", _i32),
+        ("num_rows", _i64), ("in_features", _i64), ("out_features", _i64), ("num_experts", _i64),
+        ("num_groups", _i64),
+        ("x_row_stride", _i64), ("x_scale_stride", _i64), ("y_row_stride", _i64), ("y_scale_stride", _i64),
+        ("x", _vp), ("x_scale", _vp), ("w", _vp), ("w_scale", _vp), ("group_list", _vp),
+        ("y", _vp), ("y_scale", _vp),
+        ("ev_matmul_begin", _vp), ("ev_matmul_end", _vp),
+    ]
+
+
+class LayerDesc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("weight_dtype", _i32), ("id_dtype", _i32), ("scale_dtype", _i32),
+        ("num_tokens", _i64), ("slots", _i64), ("hidden", _i64), ("inter_size", _i64), ("num_experts", _i64),
+        ("x_row_stride", _i64), ("y_row_stride", _i64), ("expert_ids_stride", _i64),
+        ("expert_scales_stride", _i64), ("active_mask_stride", _i64),
+        ("x", _vp), ("expert_ids", _vp), ("expert_scales", _vp), ("active_mask", _vp),
+        ("w13", _vp), ("w13_scale", _vp), ("w2", _vp), ("w2_scale", _vp), ("y", _vp),
+        ("ev_layer_begin", _vp), ("ev_layer_end", _vp),
     ]

@@ -49,6 +49,12 @@ size_t moe_permute_desc_size(void) { return sizeof(moe_permute_desc); }
 
 size_t moe_update_expert_desc_size(void) { return sizeof(moe_update_expert_desc); }
 
+size_t moe_quant_fp8_desc_size(void) { return sizeof(moe_quant_fp8_desc); }
+
+size_t moe_grouped_matmul_fp8_desc_size(void) { return sizeof(moe_grouped_matmul_fp8_desc); }
+
+size_t moe_layer_desc_size(void) { return sizeof(moe_layer_desc); }
+
 const char* ffnwb_status_string(int status) {
   switch (status) {
     case FFNWB_OK: return "FFNWB_OK";
@@ -145,6 +151,56 @@ int moe_update_expert(const moe_update_expert_desc* d, void* workspace, size_t w
   const int st = plan_update_expert(d);
   if (st != FFNWB_OK) return st;
   return launch_update_expert(d, static_cast<hipStream_t>(stream));
+}
+
+int moe_quant_fp8_workspace_size(const moe_quant_fp8_desc* d, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  const int st = plan_quant_fp8(d);
+  if (st != FFNWB_OK) return st;
+  *ws_bytes = 0;
+  return FFNWB_OK;
+}
+
+int moe_quant_fp8(const moe_quant_fp8_desc* d, void* workspace, size_t ws_bytes, void* stream) {
+  (void)workspace;
+  (void)ws_bytes;
+  const int st = plan_quant_fp8(d);
+  if (st != FFNWB_OK) return st;
+  return launch_quant_fp8(d, static_cast<hipStream_t>(stream));
+}
+
+int moe_grouped_matmul_fp8_workspace_size(const moe_grouped_matmul_fp8_desc* d, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  MatmulPlan p;
+  const int st = plan_grouped_matmul(d, &p);
+  if (st != FFNWB_OK) return st;
+  *ws_bytes = p.ws_bytes;
+  return FFNWB_OK;
+}
+
+int moe_grouped_matmul_fp8(const moe_grouped_matmul_fp8_desc* d, void* workspace, size_t ws_bytes, void* stream) {
+  MatmulPlan p;
+  const int st = plan_grouped_matmul(d, &p);
+  if (st != FFNWB_OK) return st;
+  if (!workspace_ok(workspace, ws_bytes, p.ws_bytes)) return FFNWB_ERR_WORKSPACE;
+  return launch_grouped_matmul(d, p, workspace, static_cast<hipStream_t>(stream));
+}
+
+int moe_layer_workspace_size(const moe_layer_desc* d, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  LayerPlan p;
+  const int st = plan_layer(d, &p);
+  if (st != FFNWB_OK) return st;
+  *ws_bytes = p.ws_bytes;
+  return FFNWB_OK;
+}
+
+int moe_layer(const moe_layer_desc* d, void* workspace, size_t ws_bytes, void* stream) {
+  LayerPlan p;
+  const int st = plan_layer(d, &p);
+  if (st != FFNWB_OK) return st;
+  if (!workspace_ok(workspace, ws_bytes, p.ws_bytes)) return FFNWB_ERR_WORKSPACE;
+  return launch_layer(d, p, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

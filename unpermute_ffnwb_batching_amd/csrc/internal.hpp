@@ -122,6 +122,31 @@ int launch_permute(const moe_permute_desc* d, const PermutePlan& p, void* ws, hi
 int plan_update_expert(const moe_update_expert_desc* d);
 int launch_update_expert(const moe_update_expert_desc* d, hipStream_t s);
 
+int plan_quant_fp8(const moe_quant_fp8_desc* d);
+int launch_quant_fp8(const moe_quant_fp8_desc* d, hipStream_t s);
+
+struct MatmulPlan {
+  int64_t R = 0, K = 0, N = 0, F = 0;          // F = outputs per row
+  int64_t kb = 0, nb = 0;                      // 128-blocks along K and N
+  int64_t xs = 0, xss = 0, ys = 0, yss = 0;    // row strides: bytes, elements, bytes, elements
+  int64_t mt = 0;                              // row tile / 16
+  int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles
+  size_t ws_bytes = 0;
+};
+
+int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p);
+int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan& p, void* ws, hipStream_t s);
+
+struct LayerPlan {
+  int64_t T = 0, K = 0, H = 0, F = 0, E = 0;
+  int64_t xs = 0, ys = 0, is = 0, ss = 0, ms = 0;  // row strides: bytes, bytes, elements
+  int64_t ranks = 0;                               // most distinct experts: min(T * K, E)
+  size_t ws_bytes = 0;
+};
+
+int plan_layer(const moe_layer_desc* d, LayerPlan* p);
+int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStream_t s);
+
 // Widest row-copy access (16, 4 or 1 bytes) that two base addresses, two strides and the
 // row size all allow.
 inline int vec_class(uintptr_t a, uintptr_t b, int64_t s1, int64_t s2, int64_t bytes) {

@@ -1,0 +1,485 @@
+// A whole expert layer for a few tokens, in two launches.
+//
+// With at most 64 tokens the layer is the reading of its distinct experts' weights, once each:
+// everything else is small.  Launch 1 (gate and up products, SwiGLU) takes 16 columns of F of
+// one distinct expert per workgroup; launch 2 (down product, weighted sum) takes 16 columns of
+// H per workgroup and walks all experts, so the sum over a token's experts stays in one
+// workgroup: no atomics, no third launch, the same bits on every run.
+//
+// Weights are the A operand of 16x16x32 matrix instructions (16 weight rows by 32 columns),
+// straight from memory to registers; up to 16 tokens of the expert are the B operand.  e4m3
+// weights become the 16-bit type of the activations exactly, and the total of each 128-column
+// block is added to an FP32 sum times the block's scale.  h goes from launch 1 to launch 2 as a
+// pair of BF16 numbers hi + lo (16 significant bits in the range of FP32): one BF16 would cost
+// as much accuracy as the rounding of y itself, FP16 could overflow, and the second product is
+// free while the weights are being read.
+#include "fp8_block.hpp"
+#include "internal.hpp"
+
+namespace ffnwb {
+
+constexpr int kLyMaxTokens = 64;
+constexpr int kLyMaxSlots = 64;
+constexpr int kLyMaxIds = kLyMaxTokens * kLyMaxSlots;
+constexpr int kUpWaves = 4, kDownWaves = 8;
+
+struct LayerArgs {
+  int32_t T, K, E, H, F;
+  int32_t hb, fb;             // 128-blocks of H and F
+  int32_t nb13;               // 128-blocks of 2 F
+  int32_t ctiles;             // 16-column tiles of F
+  int32_t id64;
+  int32_t scale_dtype;
+  int64_t xs, ys, is, ss, ms;
+  const char* x;
+  const void* ids;
+  const void* scales;
+  const uint8_t* mask;
+  const char* w13;
+  const float* w13s;
+  const char* w2;
+  const float* w2s;
+  char* y;
+  // workspace
+  int32_t* ranks;             // [1] distinct experts
+  int32_t* expert;            // [ranks] ascending ids
+  int32_t* first;             // [ranks + 1] first entry of each
+  int32_t* slot;              // [T * K] entries: t * K + k, tokens ascending within an expert
+  float* weight;              // [T * K] the token's weight for the expert
+  char* hhi;                  // [T * K, F] BF16
+  char* hlo;
+};
+
+// ------------------------------------------------------------------ operands
+
+// One lane's share of 16 weight rows by 128 columns: four steps of 8 columns.  e4m3: a 16-byte
+// load holds 16 columns, two steps; BF16: 8 columns, one step.
+template <class T, bool kFp8>
+struct Weights {
+  static constexpr int kLoads = kFp8 ? 2 : 4;
+  static constexpr int kElt = kFp8 ? 1 : 2;
+  u32x4 v[kLoads];
+  // column of step s, for the lanes of group g
+  __device__ static int32_t col(int s, int32_t g) { return kFp8 ? (s / 2) * 64 + g * 16 + (s % 2) * 8 : s * 32 + g * 8; }
+  __device__ void load(const char* row, int32_t c0, int32_t g, int32_t end) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int32_t c = c0 + col(kFp8 ? 2 * i : i, g);
+      v[i] = c < end ? *reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(c) * kElt) : u32x4{0, 0, 0, 0};
+    }
+  }
+  __device__ u32x4 step(int s) const {
+    if constexpr (kFp8) {
+      const uint32_t a = v[s / 2][2 * (s % 2)], b = v[s / 2][2 * (s % 2) + 1];
+      return u32x4{Mat<T>::widen(a, false), Mat<T>::widen(a, true), Mat<T>::widen(b, false), Mat<T>::widen(b, true)};
+    } else {
+      return v[s];
+    }
+  }
+};
+
+// ------------------------------------------------------------------ routing
+
+// The id of slot (t, k), or -1 when it takes no part.
+__device__ __forceinline__ int32_t active_id(const LayerArgs& a, int32_t i) {
+  const int32_t t = i / a.K, k = i - t * a.K;
+  const int64_t at = t * a.is + k;
+  const int64_t id = a.id64 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
+  const bool on = a.mask == nullptr || a.mask[t * a.ms + k] != 0;
+  return on && id >= 0 && id < a.E ? static_cast<int32_t>(id) : -1;
+}
+
+// All ids into LDS and one bit for each expert that occurs.
+__device__ __forceinline__ void load_ids(const LayerArgs& a, int32_t* ids, uint32_t* bits) {
+  for (int32_t i = threadIdx.x; i < kMaxExperts / 32; i += blockDim.x) bits[i] = 0;
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < a.T * a.K; i += blockDim.x) {
+    const int32_t id = active_id(a, i);
+    ids[i] = id;
+    if (id >= 0) atomicOr(&bits[id / 32], 1u << (id % 32));
+  }
+  __syncthreads();
+}
+
+// Bits set in the words below each lane's four (wave 0 holds all 256 words), and in all.
+__device__ __forceinline__ int32_t bits_below(const uint32_t* bits, int32_t lane, int32_t& total) {
+  int32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mine += __popc(bits[4 * lane + j]);
+  int32_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int32_t v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  total = __shfl(incl, kWave - 1);
+  return incl - mine;
+}
+
+__device__ __forceinline__ float slot_scale(const LayerArgs& a, int32_t t, int32_t k) {
+  if (a.scales == nullptr) return 1.0f;
+  const int64_t at = t * a.ss + k;
+  return a.scale_dtype == FFNWB_DT_FP32   ? load_elem<TF32>(a.scales, at)
+         : a.scale_dtype == FFNWB_DT_BF16 ? load_elem<TBF16>(a.scales, at)
+                                          : load_elem<TF16>(a.scales, at);
+}
+
+// Workgroup 0 of launch 1: the experts, their tokens and weights, for launch 2.  A token that
+// names an expert twice has one entry, at its first slot, with the sum of the weights.
+__device__ void build_table(const LayerArgs& a, const int32_t* ids, const uint32_t* bits, int32_t* cursor, int32_t* below) {
+  const int32_t n = a.T * a.K, lane = threadIdx.x % kWave;
+  if (threadIdx.x < kWave) {
+    int32_t total;
+    int32_t at = bits_below(bits, lane, total);
+    for (int j = 0; j < 4; ++j) {
+      const int32_t w = 4 * lane + j;
+      below[w] = at;
+      for (uint32_t m = bits[w]; m != 0; m &= m - 1) a.expert[at++] = w * 32 + __builtin_ctz(m);
+    }
+    if (lane == 0) {
+      *a.ranks = total;
+      below[kMaxExperts / 32] = total;
+    }
+  }
+  __syncthreads();
+  const int32_t ranks = below[kMaxExperts / 32];
+  auto rank = [&](int32_t e) { return below[e / 32] + __popc(bits[e / 32] & ((1u << (e % 32)) - 1)); };
+  auto head = [&](int32_t i) {  // whether slot i is its token's first with its expert
+    const int32_t t0 = i / a.K * a.K;
+    for (int32_t j = t0; j < i; ++j)
+      if (ids[j] == ids[i]) return false;
+    return true;
+  };
+  for (int32_t r = threadIdx.x; r < ranks; r += blockDim.x) cursor[r] = 0;
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < n; i += blockDim.x)
+    if (ids[i] >= 0 && head(i)) atomicAdd(&cursor[rank(ids[i])], 1);
+  __syncthreads();
+  // exclusive sums, a run of ranks per lane of wave 0
+  if (threadIdx.x < kWave) {
+    const int32_t per = (ranks + kWave - 1) / kWave, r0 = min(lane * per, ranks), r1 = min(r0 + per, ranks);
+    int32_t mine = 0;
+    for (int32_t r = r0; r < r1; ++r) mine += cursor[r];
+    int32_t incl = mine;
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int32_t v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    int32_t at = incl - mine;
+    for (int32_t r = r0; r < r1; ++r) {
+      const int32_t c = cursor[r];
+      a.first[r] = at;
+      cursor[r] = at;
+      at += c;
+    }
+    if (lane == kWave - 1) a.first[ranks] = incl;
+  }
+  __syncthreads();
+  // tokens in order; the heads of one token have distinct experts
+  for (int32_t t = 0; t < a.T; ++t) {
+    for (int32_t k = threadIdx.x; k < a.K; k += blockDim.x) {
+      const int32_t i = t * a.K + k, e = ids[i];
+      if (e < 0 || !head(i)) continue;
+      float w = 0.0f;
+      for (int32_t j = k; j < a.K; ++j)
+        if (ids[t * a.K + j] == e) w += slot_scale(a, t, j);
+      const int32_t at = cursor[rank(e)]++;
+      a.slot[at] = i;
+      a.weight[at] = w;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ launch 1: gate, up, SwiGLU
+
+// h of 16 columns from f0 of expert e for its `count` tokens (at most MT * 16); list[j] is token
+// j's slot.  The four waves take every fourth 128-block of H; their totals are added in order.
+template <class T, bool kFp8, int MT>
+__device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count, const int32_t* list, float* red) {
+  using W = Weights<T, kFp8>;
+  const int32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, r = lane % 16, g = lane / 16;
+  const int64_t rowb = static_cast<int64_t>(a.H) * W::kElt;
+  const char* wp[2] = {a.w13 + (static_cast<int64_t>(e) * 2 * a.F + f0 + r) * rowb,
+                       a.w13 + (static_cast<int64_t>(e) * 2 * a.F + a.F + f0 + r) * rowb};
+  const float* wsp[2] = {nullptr, nullptr};
+  if constexpr (kFp8) {
+    wsp[0] = a.w13s + (static_cast<int64_t>(e) * a.nb13 + f0 / kBlk) * a.hb;
+    wsp[1] = a.w13s + (static_cast<int64_t>(e) * a.nb13 + (a.F + f0) / kBlk) * a.hb;
+  }
+  const char* xp[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xp[i] = a.x + (list[min(i * 16 + r, count - 1)] / a.K) * a.xs;
+  f32x4 tot[2][MT] = {};
+  for (int32_t b = wave; b < a.hb; b += kUpWaves) {
+    W w[2];
+    w[0].load(wp[0], b * kBlk, g, a.H);
+    w[1].load(wp[1], b * kBlk, g, a.H);
+    f32x4 p[2][MT] = {};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int32_t c = b * kBlk + W::col(s, g);
+      const u32x4 w0 = w[0].step(s), w1 = w[1].step(s);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const u32x4 xv = c < a.H ? *reinterpret_cast<const u32x4*>(xp[i] + static_cast<int64_t>(c) * 2) : u32x4{0, 0, 0, 0};
+        p[0][i] = Mat<T>::mul(w0, xv, p[0][i]);
+        p[1][i] = Mat<T>::mul(w1, xv, p[1][i]);
+      }
+    }
+    const float s0 = kFp8 ? wsp[0][b] : 1.0f, s1 = kFp8 ? wsp[1][b] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        tot[0][i][j] = __builtin_fmaf(s0, p[0][i][j], tot[0][i][j]);
+        tot[1][i][j] = __builtin_fmaf(s1, p[1][i][j], tot[1][i][j]);
+      }
+  }
+  f32x4* rv = reinterpret_cast<f32x4*>(red);  // [wave][2 MT][lane]
+  __syncthreads();                            // `list` may share red's memory with the ids
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    rv[(wave * 2 * MT + i) * kWave + lane] = tot[0][i];
+    rv[(wave * 2 * MT + MT + i) * kWave + lane] = tot[1][i];
+  }
+  __syncthreads();
+  for (int32_t i = wave; i < MT; i += kUpWaves) {
+    const int32_t j = i * 16 + r;
+    if (j >= count) continue;
+    f32x4 gv = {}, uv = {};
+#pragma unroll
+    for (int w = 0; w < kUpWaves; ++w) {
+      gv += rv[(w * 2 * MT + i) * kWave + lane];
+      uv += rv[(w * 2 * MT + MT + i) * kWave + lane];
+    }
+    u32x2 hi = {}, lo = {};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float h = swiglu(gv[q], uv[q]);
+      const uint32_t hb16 = f32_to_bf16_rne(h);
+      // an infinite or NaN h has no remainder
+      const float rest = h - bf16_to_f32(hb16);
+      const uint32_t lb16 = (hb16 & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_rne(rest);
+      hi[q / 2] |= hb16 << (16 * (q % 2));
+      lo[q / 2] |= lb16 << (16 * (q % 2));
+    }
+    const int64_t at = (static_cast<int64_t>(list[j]) * a.F + f0 + g * 4) * 2;
+    *reinterpret_cast<u32x2*>(a.hhi + at) = hi;
+    *reinterpret_cast<u32x2*>(a.hlo + at) = lo;
+  }
+}
+
+template <class T, bool kFp8>
+__global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) {
+  __shared__ __align__(16) int32_t scratch[kUpWaves * 8 * kWave * 4];  // ids, then the waves' totals
+  __shared__ uint32_t bits[kMaxExperts / 32];
+  __shared__ int32_t below[kMaxExperts / 32 + 1];
+  __shared__ int32_t list[kLyMaxTokens];
+  __shared__ int32_t chosen, count;
+  static_assert(kUpWaves * 8 * kWave * 4 >= 2 * kLyMaxIds, "ids and cursors share the totals' memory");
+  int32_t* ids = scratch;
+  load_ids(a, ids, bits);
+  if (blockIdx.x == 0) {
+    build_table(a, ids, bits, scratch + kLyMaxIds, below);
+    return;
+  }
+  const int32_t rank = (blockIdx.x - 1) / a.ctiles, c = blockIdx.x - 1 - rank * a.ctiles;
+  const int32_t lane = threadIdx.x % kWave;
+  if (threadIdx.x < kWave) {
+    int32_t total;
+    const int32_t below4 = bits_below(bits, lane, total);
+    if (lane == 0 && rank >= total) chosen = -1;
+    int32_t left = rank - below4;  // the rank's place among this lane's bits
+    for (int j = 0; j < 4; ++j) {
+      uint32_t m = bits[4 * lane + j];
+      const int32_t here = __popc(m);
+      if (left >= 0 && left < here) {
+        for (; left > 0; --left) m &= m - 1;
+        chosen = (4 * lane + j) * 32 + __builtin_ctz(m);
+        left = -1;
+      } else {
+        left -= here;
+      }
+    }
+    wave_lds_sync();
+    const int32_t e = chosen;
+    int32_t slot = -1;
+    if (e >= 0 && lane < a.T)
+      for (int32_t k = a.K - 1; k >= 0; --k)
+        if (ids[lane * a.K + k] == e) slot = lane * a.K + k;
+    const uint64_t has = wave_ballot(slot >= 0);
+    if (slot >= 0) list[count_below(has)] = slot;
+    if (lane == 0) count = __popcll(has);
+  }
+  __syncthreads();
+  const int32_t e = uniform(chosen), n = uniform(count);
+  if (e < 0) return;
+  float* red = reinterpret_cast<float*>(scratch);
+  if (n <= 16) up_tile<T, kFp8, 1>(a, e, c * 16, n, list, red);
+  else if (n <= 32) up_tile<T, kFp8, 2>(a, e, c * 16, n, list, red);
+  else up_tile<T, kFp8, 4>(a, e, c * 16, n, list, red);
+}
+
+// ------------------------------------------------------------------ launch 2: down, weighted sum
+
+// 16 columns of H.  The 128-blocks of F of all experts are numbered in one row and dealt to the
+// waves in turn; each wave adds its totals, times the tokens' weights, into sums of its own
+// [T][16], which are added in wave order.
+template <class T, bool kFp8>
+__global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs a) {
+  using W = Weights<TBF16, kFp8>;
+  extern __shared__ __align__(16) float acc[];  // [waves][T][16]
+  const int32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, r = lane % 16, g = lane / 16;
+  const int32_t n0 = blockIdx.x * 16;
+  for (int32_t i = threadIdx.x; i < kDownWaves * a.T * 16; i += blockDim.x) acc[i] = 0.0f;
+  __syncthreads();
+  f32x4* mine = reinterpret_cast<f32x4*>(acc) + wave * a.T * 4;
+  const int32_t ranks = uniform(*a.ranks);
+  const int64_t rowb = static_cast<int64_t>(a.F) * W::kElt;
+  for (int32_t k = 0; k < ranks; ++k) {
+    const int32_t b0 = (wave - k * a.fb) & (kDownWaves - 1);
+    if (b0 >= a.fb) continue;
+    const int32_t e = uniform(a.expert[k]), at = uniform(a.first[k]), n = uniform(a.first[k + 1]) - at;
+    const char* wp = a.w2 + (static_cast<int64_t>(e) * a.H + n0 + r) * rowb;
+    const float* wsp = kFp8 ? a.w2s + (static_cast<int64_t>(e) * a.hb + n0 / kBlk) * a.fb : nullptr;
+    int64_t hoff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hoff[i] = static_cast<int64_t>(a.slot[at + min(i * 16 + r, n - 1)]) * a.F * 2;
+    f32x4 tot[4] = {};
+    for (int32_t b = b0; b < a.fb; b += kDownWaves) {
+      W w;
+      w.load(wp, b * kBlk, g, a.F);
+      f32x4 p[4] = {};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int32_t c = b * kBlk + W::col(s, g);
+        const u32x4 wv = w.step(s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i * 16 >= n) break;
+          u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+          if (c < a.F) {
+            hi = *reinterpret_cast<const u32x4*>(a.hhi + hoff[i] + static_cast<int64_t>(c) * 2);
+            lo = *reinterpret_cast<const u32x4*>(a.hlo + hoff[i] + static_cast<int64_t>(c) * 2);
+          }
+          p[i] = Mat<TBF16>::mul(wv, lo, p[i]);
+          p[i] = Mat<TBF16>::mul(wv, hi, p[i]);
+        }
+      }
+      const float s = kFp8 ? wsp[b] : 1.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tot[i][j] = __builtin_fmaf(s, p[i][j], tot[i][j]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i * 16 + r < n) {
+        const float c = a.weight[at + i * 16 + r];
+        f32x4* to = mine + a.slot[at + i * 16 + r] / a.K * 4 + g;  // an expert's tokens are distinct
+        f32x4 v = *to;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(c, tot[i][j], v[j]);
+        *to = v;
+      }
+    }
+  }
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < a.T * 16; i += blockDim.x) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDownWaves; ++w) v += acc[w * a.T * 16 + i];
+    store_elem<T>(a.y + static_cast<int64_t>(i / 16) * a.ys, n0 + i % 16, v);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
+  if (d == nullptr || d->x == nullptr || d->expert_ids == nullptr || d->w13 == nullptr || d->w2 == nullptr || d->y == nullptr)
+    return FFNWB_ERR_PARAM_NULLPTR;
+  if (d->dtype != FFNWB_DT_FP16 && d->dtype != FFNWB_DT_BF16) return FFNWB_ERR_PARAM_INVALID;
+  const bool fp8 = d->weight_dtype == FFNWB_DT_FP8_E4M3;
+  if (!fp8 && !(d->weight_dtype == FFNWB_DT_BF16 && d->dtype == FFNWB_DT_BF16)) return FFNWB_ERR_PARAM_INVALID;
+  if (fp8 != (d->w13_scale != nullptr) || fp8 != (d->w2_scale != nullptr)) return FFNWB_ERR_PARAM_INVALID;
+  if (d->id_dtype != FFNWB_DT_INT32 && d->id_dtype != FFNWB_DT_INT64) return FFNWB_ERR_PARAM_INVALID;
+  if (d->expert_scales != nullptr && d->scale_dtype != FFNWB_DT_FP16 && d->scale_dtype != FFNWB_DT_BF16 &&
+      d->scale_dtype != FFNWB_DT_FP32)
+    return FFNWB_ERR_PARAM_INVALID;
+  if (d->num_tokens < 0 || d->num_tokens > kLyMaxTokens || d->slots <= 0 || d->slots > kLyMaxSlots) return FFNWB_ERR_PARAM_INVALID;
+  if (d->hidden <= 0 || d->hidden > (1 << 18) || d->hidden % 16 != 0) return FFNWB_ERR_PARAM_INVALID;
+  if (d->inter_size <= 0 || d->inter_size > (1 << 17) || d->inter_size % 16 != 0) return FFNWB_ERR_PARAM_INVALID;
+  if (d->num_experts < 1 || d->num_experts > kMaxExperts) return FFNWB_ERR_PARAM_INVALID;
+  p->T = d->num_tokens, p->K = d->slots, p->H = d->hidden, p->F = d->inter_size, p->E = d->num_experts;
+  p->xs = d->x_row_stride ? d->x_row_stride : p->H * 2;
+  p->ys = d->y_row_stride ? d->y_row_stride : p->H * 2;
+  p->is = d->expert_ids_stride ? d->expert_ids_stride : p->K;
+  p->ss = d->expert_scales_stride ? d->expert_scales_stride : p->K;
+  p->ms = d->active_mask_stride ? d->active_mask_stride : p->K;
+  const int64_t far = int64_t{1} << 40;  // row * stride stays inside 64 bits
+  if (p->xs < p->H * 2 || p->xs % 16 != 0 || p->ys < p->H * 2 || p->ys % 2 != 0) return FFNWB_ERR_PARAM_INVALID;
+  if (p->is < p->K || p->ss < p->K || p->ms < p->K) return FFNWB_ERR_PARAM_INVALID;
+  if (p->xs > far || p->ys > far || p->is > far || p->ss > far || p->ms > far) return FFNWB_ERR_PARAM_INVALID;
+  if ((reinterpret_cast<uintptr_t>(d->x) | reinterpret_cast<uintptr_t>(d->w13) | reinterpret_cast<uintptr_t>(d->w2)) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(d->y) % 2 != 0)
+    return FFNWB_ERR_PARAM_INVALID;
+  const int64_t n = p->T * p->K;
+  p->ranks = n < p->E ? n : p->E;
+  // one dimension of the grid: fewer than 2^32 threads
+  if (p->ranks * (p->F / 16) >= (int64_t{1} << 32) / (kUpWaves * kWave) - 1) return FFNWB_ERR_PARAM_INVALID;
+  Carve c;
+  if (n > 0) {
+    c.take<int32_t>(1);
+    c.take<int32_t>(static_cast<size_t>(p->ranks));
+    c.take<int32_t>(static_cast<size_t>(p->ranks) + 1);
+    c.take<int32_t>(static_cast<size_t>(n));
+    c.take<float>(static_cast<size_t>(n));
+    c.take<uint16_t>(static_cast<size_t>(n * p->F));
+    c.take<uint16_t>(static_cast<size_t>(n * p->F));
+  }
+  p->ws_bytes = c.off;
+  return FFNWB_OK;
+}
+
+template <class T, bool kFp8>
+static bool launch_t(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void* begin, void* end) {
+  const uint32_t grid = static_cast<uint32_t>(1 + p.ranks * a.ctiles);
+  if (!launch_bound(layer_up_kernel<T, kFp8>, dim3(grid), dim3(kUpWaves * kWave), 0, s, begin, nullptr, a)) return false;
+  return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16)), dim3(kDownWaves * kWave),
+                      static_cast<size_t>(kDownWaves * p.T * 16 * 4), s, nullptr, end, a);
+}
+
+int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStream_t s) {
+  if (p.T == 0) return FFNWB_OK;
+  LayerArgs a{};
+  a.T = static_cast<int32_t>(p.T), a.K = static_cast<int32_t>(p.K), a.E = static_cast<int32_t>(p.E);
+  a.H = static_cast<int32_t>(p.H), a.F = static_cast<int32_t>(p.F);
+  a.hb = (a.H + kBlk - 1) / kBlk, a.fb = (a.F + kBlk - 1) / kBlk, a.nb13 = (2 * a.F + kBlk - 1) / kBlk;
+  a.ctiles = a.F / 16;
+  a.id64 = d->id_dtype == FFNWB_DT_INT64;
+  a.scale_dtype = d->scale_dtype;
+  a.xs = p.xs, a.ys = p.ys, a.is = p.is, a.ss = p.ss, a.ms = p.ms;
+  a.x = static_cast<const char*>(d->x), a.ids = d->expert_ids, a.scales = d->expert_scales, a.mask = d->active_mask;
+  a.w13 = static_cast<const char*>(d->w13), a.w13s = d->w13_scale;
+  a.w2 = static_cast<const char*>(d->w2), a.w2s = d->w2_scale;
+  a.y = static_cast<char*>(d->y);
+  const size_t n = static_cast<size_t>(p.T * p.K);
+  Carve c;
+  c.base = static_cast<char*>(ws);
+  a.ranks = c.take<int32_t>(1);
+  a.expert = c.take<int32_t>(static_cast<size_t>(p.ranks));
+  a.first = c.take<int32_t>(static_cast<size_t>(p.ranks) + 1);
+  a.slot = c.take<int32_t>(n);
+  a.weight = c.take<float>(n);
+  a.hhi = reinterpret_cast<char*>(c.take<uint16_t>(n * p.F));
+  a.hlo = reinterpret_cast<char*>(c.take<uint16_t>(n * p.F));
+  const bool fp8 = d->weight_dtype == FFNWB_DT_FP8_E4M3;
+  void *b = d->ev_layer_begin, *e = d->ev_layer_end;
+  const bool ok = d->dtype == FFNWB_DT_FP16 ? launch_t<TF16, true>(a, p, s, b, e)
+                  : fp8                     ? launch_t<TBF16, true>(a, p, s, b, e)
+                                            : launch_t<TBF16, false>(a, p, s, b, e);
+  return ok ? FFNWB_OK : FFNWB_ERR_RUNTIME;
+}
+
+}  // namespace ffnwb

@@ -109,7 +109,7 @@ def _check_matmul(c, groups=None, epilogue="none", out_dtype=BF16):
     call = _matmul_call(c, groups, epilogue, out_dtype, out)
     call.run()
     torch.cuda.synchronize()
-    want, off, written = matmul_reference(c, groups, epilogue)
+    want, off, written = matmul_reference(c, groups, epilogue, out_dtype in (BF16, FP16))
     y = call.out["y"]
     idx = torch.from_numpy(written).cuda()
     if out_dtype == FP8:
@@ -185,7 +185,7 @@ def test_product_views_of_wider_buffers():
         print(f"product of strided views {epilogue} {out_dtype}", flush=True)
         call.run()
         torch.cuda.synchronize()
-        want, off, _ = matmul_reference(c, None, epilogue)
+        want, off, _ = matmul_reference(c, None, epilogue, out_dtype in (BF16, FP16))
         if out_dtype == FP8:
             quantised_close(out["y"], out["y_scale"], want, off)
         else:

@@ -13,7 +13,8 @@ struct MmArgs {
   int64_t rows, K, N, F;       // F = outputs per row (N, or N / 2 with SwiGLU)
   int64_t xs, xss, ys, yss;    // row strides: bytes, elements, bytes, elements
   int32_t kb, nb;              // 128-blocks along K and N
-  int32_t ntiles;              // column tiles
+  int32_t mtiles, ntiles;      // row tiles of a dense product, column tiles
+  bool vec;                    // four adjacent outputs are one aligned store
   const char* x;
   const float* x_scale;
   const char* w;
@@ -77,6 +78,20 @@ __global__ __launch_bounds__(kTableThreads) void mm_table_kernel(const int64_t* 
   }
 }
 
+// Row tile and column tile of a workgroup.  Workgroups go round the 8 XCDs, each with its own
+// L2: XCD x gets the x-th eighth of the tiles, and walks it 8 row tiles by all column tiles at
+// a time, row tiles first, so that workgroups running together share rows of x and of w.
+__device__ __forceinline__ bool tile_of_block(const MmArgs& a, int32_t& m, int32_t& c) {
+  constexpr int32_t kXcds = 8, kRun = 8;
+  const int32_t mt = a.table != nullptr ? *a.count : a.mtiles, total = mt * a.ntiles;
+  const int32_t per = (total + kXcds - 1) / kXcds, place = blockIdx.x / kXcds, t = blockIdx.x % kXcds * per + place;
+  if (place >= per || t >= total) return false;
+  const int32_t run = t / (kRun * a.ntiles), first = run * kRun, rows = min(kRun, mt - first), at = t - first * a.ntiles;
+  m = first + at % rows;
+  c = at / rows;
+  return true;
+}
+
 struct RowTile { int32_t expert, row0, rows; };
 
 // The row tile m, or rows = 0 past the last one.
@@ -92,7 +107,17 @@ __device__ __forceinline__ RowTile row_tile(const MmArgs& a, int32_t m, int32_t 
 
 // Four adjacent outputs n .. n + 3 of one row, those below `end`.
 template <class T>
-__device__ __forceinline__ void store4(char* row, int64_t n, int64_t end, const f32x4& v) {
+__device__ __forceinline__ void store4(char* row, int64_t n, int64_t end, const f32x4& v, bool vec) {
+  if (vec && n + 3 < end) {
+    if constexpr (T::kBytes == 4) {
+      *reinterpret_cast<f32x4*>(row + n * 4) = v;
+    } else {
+      const float f[8] = {v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+      const u32x4 h = Chunk<T>::narrow(f);
+      *reinterpret_cast<u32x2*>(row + n * 2) = u32x2{h[0], h[1]};
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (n + i < end) store_elem<T>(row, n + i, v[i]);
@@ -191,13 +216,19 @@ __global__ __launch_bounds__(kDirectWaves* kWave) void mm_direct_kernel(MmArgs a
       f32x4 h;
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = swiglu(s[0][j], s[1][j]);
-      store4<T>(row, n0 + g * 4, a.F, h);
+      store4<T>(row, n0 + g * 4, a.F, h, a.vec);
     } else {
-      store4<T>(row, n0 + g * 4, a.N, s[0]);
-      store4<T>(row, n1 + g * 4, a.N, s[1]);
+      store4<T>(row, n0 + g * 4, a.N, s[0], a.vec);
+      store4<T>(row, n1 + g * 4, a.N, s[1], a.vec);
     }
   }
 }
+
+}  // namespace ffnwb
+
+#include "mm_tile.hpp"
+
+namespace ffnwb {
 
 // ------------------------------------------------------------------ quantising a product
 //
@@ -238,6 +269,8 @@ __global__ __launch_bounds__(kMqThreads) void mm_quant_kernel(MmArgs a, const fl
 
 // ------------------------------------------------------------------ host side
 
+constexpr int64_t kCus = 256;
+
 static int64_t out_size(int32_t dt) { return dt == FFNWB_DT_FP32 ? 4 : dt == FFNWB_DT_FP8_E4M3 ? 1 : 2; }
 
 int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
@@ -276,18 +309,28 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t groups = d->group_list != nullptr ? d->num_groups : 1;
   const int64_t avg = (p->R + groups - 1) / groups;
-  p->mt = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
-  p->mtiles = (p->R + p->mt * 16 - 1) / (p->mt * 16) + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
-  p->ntiles = swiglu ? p->F / 16 : (p->N + 31) / 32;
-  // one dimension of the grid: fewer than 2^32 threads
-  if (p->mtiles * p->ntiles >= (int64_t{1} << 32) / (kDirectWaves * kWave)) return FFNWB_ERR_PARAM_INVALID;
+  const bool fast = !quant && d->out_dtype != FFNWB_DT_FP32;
+  auto shape = [&](bool tile, int64_t bm) {
+    p->tile = tile, p->bm = bm;
+    p->mtiles = (p->R + bm - 1) / bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
+    p->ntiles = tile ? (swiglu ? (p->F + 127) / 128 : (p->N + 255) / 256) : (swiglu ? p->F / 16 : (p->N + 31) / 32);
+    return p->mtiles * p->ntiles;
+  };
+  // Through LDS, with the largest tile that the groups fill on average and that leaves every CU
+  // one; straight to registers where even the smallest tiles are few, and where 256 rows
+  // of x pass the 32-bit offsets of the copies.
+  int64_t bm = avg > 1024 && fast ? 256 : avg > 128 ? 128 : avg > 64 ? 64 : 32;
+  while (bm > 32 && shape(true, bm) < kCus) bm /= 2;
+  if (p->xs > (1 << 22) || shape(true, bm) < kCus / 2) shape(false, avg <= 16 ? 16 : avg <= 32 ? 32 : 64);
+  // one dimension of the grid: fewer than 2^32 threads of at most 512 a workgroup
+  if (p->mtiles * p->ntiles >= (int64_t{1} << 22)) return FFNWB_ERR_PARAM_INVALID;
   p->ws_bytes = 0;
   Carve c;
   if (d->group_list != nullptr && p->R > 0) {
     c.take<int32_t>(1);
     c.take<int4>(static_cast<size_t>(p->mtiles));
   }
-  if (quant) c.take<float>(static_cast<size_t>(p->R * p->F));
+  if (quant && !p->tile) c.take<float>(static_cast<size_t>(p->R * p->F));
   p->ws_bytes = c.off;
   return FFNWB_OK;
 }
@@ -295,9 +338,29 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
 template <class T, int EPI>
 static bool launch_direct(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
   const dim3 grid(static_cast<uint32_t>(p.mtiles * p.ntiles)), block(kDirectWaves * kWave);
-  return p.mt == 1   ? launch_bound(mm_direct_kernel<T, EPI, 1>, grid, block, 0, s, b, e, a)
-         : p.mt == 2 ? launch_bound(mm_direct_kernel<T, EPI, 2>, grid, block, 0, s, b, e, a)
+  return p.bm == 16   ? launch_bound(mm_direct_kernel<T, EPI, 1>, grid, block, 0, s, b, e, a)
+         : p.bm == 32 ? launch_bound(mm_direct_kernel<T, EPI, 2>, grid, block, 0, s, b, e, a)
                      : launch_bound(mm_direct_kernel<T, EPI, 4>, grid, block, 0, s, b, e, a);
+}
+
+template <class T, int EPI, bool kQuant, bool kFast, int WM, int WN, int MF>
+static bool launch_tile_shape(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  using S = TileShape<WM, WN, MF>;
+  auto kernel = mm_tile_kernel<T, EPI, kQuant, kFast, WM, WN, MF>;
+  allow_large_lds(reinterpret_cast<const void*>(kernel), S::kLds);
+  const uint32_t grid = static_cast<uint32_t>((p.mtiles * p.ntiles + 7) / 8 * 8);
+  return launch_bound(kernel, dim3(grid), dim3(S::kThreads), S::kLds, s, b, e, a);
+}
+
+template <class T, int EPI, bool kQuant = false>
+static bool launch_tile(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  constexpr bool kFast = !kQuant && T::kBytes == 2;
+  if constexpr (kFast) {
+    if (p.bm == 256) return launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 8>(a, p, s, b, e);
+  }
+  return p.bm == 128  ? launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 4>(a, p, s, b, e)
+         : p.bm == 64 ? launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 2>(a, p, s, b, e)
+                      : launch_tile_shape<T, EPI, kQuant, kFast, 1, 4, 2>(a, p, s, b, e);
 }
 
 int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan& p, void* ws, hipStream_t s) {
@@ -307,6 +370,7 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
   a.rows = p.R, a.K = p.K, a.N = p.N, a.F = p.F;
   a.xs = p.xs, a.xss = p.xss, a.ys = p.ys, a.yss = p.yss;
   a.kb = static_cast<int32_t>(p.kb), a.nb = static_cast<int32_t>(p.nb), a.ntiles = static_cast<int32_t>(p.ntiles);
+  a.mtiles = static_cast<int32_t>(p.mtiles);
   a.x = static_cast<const char*>(d->x), a.x_scale = d->x_scale;
   a.w = static_cast<const char*>(d->w), a.w_scale = d->w_scale;
   a.y = static_cast<char*>(d->y), a.y_scale = d->y_scale;
@@ -316,13 +380,29 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
     int32_t* count = c.take<int32_t>(1);
     int4* table = c.take<int4>(static_cast<size_t>(p.mtiles));
     hipLaunchKernelGGL(mm_table_kernel, dim3(1), dim3(kTableThreads), 0, s, d->group_list, static_cast<int32_t>(d->num_groups),
-                       p.R, d->num_experts, static_cast<int32_t>(p.mt * 16), table, count);
+                       p.R, d->num_experts, static_cast<int32_t>(p.bm), table, count);
     if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
     a.table = table, a.count = count;
   }
-  float* h = quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
-  if (quant) a.y = reinterpret_cast<char*>(h), a.ys = p.F * 4;
+  const int64_t quad = 4 * out_size(d->out_dtype);
+  a.vec = ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(p.ys)) & (quad - 1)) == 0;
   void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
+  if (p.tile) {
+    bool ok;
+    if (d->epilogue == FFNWB_EPI_SWIGLU) {
+      ok = quant                           ? launch_tile<TF32, FFNWB_EPI_SWIGLU, true>(a, p, s, b, e)
+           : d->out_dtype == FFNWB_DT_FP16 ? launch_tile<TF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
+           : d->out_dtype == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
+                                           : launch_tile<TF32, FFNWB_EPI_SWIGLU>(a, p, s, b, e);
+    } else {
+      ok = d->out_dtype == FFNWB_DT_FP16   ? launch_tile<TF16, FFNWB_EPI_NONE>(a, p, s, b, e)
+           : d->out_dtype == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_NONE>(a, p, s, b, e)
+                                           : launch_tile<TF32, FFNWB_EPI_NONE>(a, p, s, b, e);
+    }
+    return ok ? FFNWB_OK : FFNWB_ERR_RUNTIME;
+  }
+  float* h = quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
+  if (quant) a.y = reinterpret_cast<char*>(h), a.ys = p.F * 4, a.vec = true;
   bool ok;
   if (d->epilogue == FFNWB_EPI_SWIGLU) {
     ok = d->out_dtype == FFNWB_DT_FP16   ? launch_direct<TF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
@@ -336,7 +416,7 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
   if (!ok) return FFNWB_ERR_RUNTIME;
   if (quant) {
     a.y = static_cast<char*>(d->y), a.ys = p.ys;
-    const int64_t bm = p.mt * 16, fb = (p.F + 127) / 128, per = (bm * fb * 16 + kMqThreads - 1) / kMqThreads;
+    const int64_t bm = p.bm, fb = (p.F + 127) / 128, per = (bm * fb * 16 + kMqThreads - 1) / kMqThreads;
     hipLaunchKernelGGL(mm_quant_kernel, dim3(static_cast<uint32_t>(p.mtiles * per)), dim3(kMqThreads), 0, s, a, h,
                        static_cast<int32_t>(bm));
     if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;

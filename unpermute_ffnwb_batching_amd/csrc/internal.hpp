@@ -129,7 +129,8 @@ struct MatmulPlan {
   int64_t R = 0, K = 0, N = 0, F = 0;          // F = outputs per row
   int64_t kb = 0, nb = 0;                      // 128-blocks along K and N
   int64_t xs = 0, xss = 0, ys = 0, yss = 0;    // row strides: bytes, elements, bytes, elements
-  int64_t mt = 0;                              // row tile / 16
+  bool tile = false;                           // through LDS, else straight to registers
+  int64_t bm = 0;                              // rows of a tile
   int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles
   size_t ws_bytes = 0;
 };

@@ -821,23 +821,29 @@ class _Call:
             _req(workspace.numel() >= ws_bytes, f"workspace has {workspace.numel()} bytes, the call needs {ws_bytes}")
         self.desc, self.out, self.workspace, self.ws_bytes = desc, out, workspace, ws_bytes
         self._name, self._device, self._keep = name, device, keep
+        self._fn = getattr(lib(), name)
         self._alloc_stream = _alloc_stream(device)
+        self._alloc_raw = self._alloc_stream.cuda_stream if self._alloc_stream is not None else None
         self._args = (ctypes.byref(desc), _ptr(workspace), ctypes.c_size_t(ws_bytes))
 
     def run(self, stream=None):
         """Enqueue the call on ``stream`` (default: the current stream of the tensors' device)."""
+        index = self._device.index
         if stream is None:
-            stream = torch.cuda.current_stream(self._device)
+            raw = torch._C._cuda_getCurrentRawStream(index)   # no Stream object in a serving loop's path
         else:
             _req(stream.device == self._device, f"stream is on {stream.device}, the tensors on {self._device}")
-        if torch.cuda.current_device() == self._device.index:
-            st = getattr(lib(), self._name)(*self._args, stream.cuda_stream)
+            raw = stream.cuda_stream
+        if torch._C._cuda_getDevice() == index:
+            st = self._fn(*self._args, raw)
         else:
-            with torch.cuda.device(self._device):
-                st = getattr(lib(), self._name)(*self._args, stream.cuda_stream)
+            with torch.cuda.device(index):
+                st = self._fn(*self._args, raw)
         if st != FFNWB_OK:
             raise FfnwbError(st, self._name)
-        _record_on([self.workspace, *self._keep, *self.out.values()], stream, self._alloc_stream)
+        if raw != self._alloc_raw:
+            _record_on([self.workspace, *self._keep, *self.out.values()],
+                       stream if stream is not None else torch.cuda.current_stream(index), self._alloc_stream)
         return self.out
 
 

@@ -142,6 +142,7 @@ struct LayerPlan {
   int64_t T = 0, K = 0, H = 0, F = 0, E = 0;
   int64_t xs = 0, ys = 0, is = 0, ss = 0, ms = 0;  // row strides: bytes, bytes, elements
   int64_t ranks = 0;                               // most distinct experts: min(T * K, E)
+  int64_t groups = 0;                              // most groups of up to 16 tokens of one expert
   size_t ws_bytes = 0;
 };
 

@@ -28,6 +28,7 @@ struct LayerArgs {
   int32_t hb, fb;             // 128-blocks of H and F
   int32_t nb13;               // 128-blocks of 2 F
   int32_t ctiles;             // 16-column tiles of F
+  int32_t groups_max;         // most groups of launch 2
   int32_t id64;
   int32_t scale_dtype;
   int64_t xs, ys, is, ss, ms;
@@ -41,9 +42,9 @@ struct LayerArgs {
   const float* w2s;
   char* y;
   // workspace
-  int32_t* ranks;             // [1] distinct experts
-  int32_t* expert;            // [ranks] ascending ids
-  int32_t* first;             // [ranks + 1] first entry of each
+  int32_t* groups;            // [1] groups of at most 16 tokens of one expert
+  int32_t* expert;            // [groups] ascending ids
+  int32_t* first;             // [groups + 1] first entry of each
   int32_t* slot;              // [T * K] entries: t * K + k, tokens ascending within an expert
   float* weight;              // [T * K] the token's weight for the expert
   char* hhi;                  // [T * K, F] BF16
@@ -124,8 +125,9 @@ __device__ __forceinline__ float slot_scale(const LayerArgs& a, int32_t t, int32
                                           : load_elem<TF16>(a.scales, at);
 }
 
-// Workgroup 0 of launch 1: the experts, their tokens and weights, for launch 2.  A token that
-// names an expert twice has one entry, at its first slot, with the sum of the weights.
+// Workgroup 0 of launch 1: the experts, their tokens (in groups of up to 16, one matrix operand)
+// and weights, for launch 2.  A token that names an expert twice has one entry, at its first
+// slot, with the sum of the weights.
 __device__ void build_table(const LayerArgs& a, const int32_t* ids, const uint32_t* bits, int32_t* cursor, int32_t* below) {
   const int32_t n = a.T * a.K, lane = threadIdx.x % kWave;
   if (threadIdx.x < kWave) {
@@ -134,12 +136,9 @@ __device__ void build_table(const LayerArgs& a, const int32_t* ids, const uint32
     for (int j = 0; j < 4; ++j) {
       const int32_t w = 4 * lane + j;
       below[w] = at;
-      for (uint32_t m = bits[w]; m != 0; m &= m - 1) a.expert[at++] = w * 32 + __builtin_ctz(m);
+      for (uint32_t m = bits[w]; m != 0; m &= m - 1) cursor[at++] = (w * 32 + __builtin_ctz(m)) << 8;  // id, no token yet
     }
-    if (lane == 0) {
-      *a.ranks = total;
-      below[kMaxExperts / 32] = total;
-    }
+    if (lane == 0) below[kMaxExperts / 32] = total;
   }
   __syncthreads();
   const int32_t ranks = below[kMaxExperts / 32];
@@ -150,29 +149,33 @@ __device__ void build_table(const LayerArgs& a, const int32_t* ids, const uint32
       if (ids[j] == ids[i]) return false;
     return true;
   };
-  for (int32_t r = threadIdx.x; r < ranks; r += blockDim.x) cursor[r] = 0;
-  __syncthreads();
   for (int32_t i = threadIdx.x; i < n; i += blockDim.x)
-    if (ids[i] >= 0 && head(i)) atomicAdd(&cursor[rank(ids[i])], 1);
+    if (ids[i] >= 0 && head(i)) atomicAdd(&cursor[rank(ids[i])], 1);  // at most 64
   __syncthreads();
-  // exclusive sums, a run of ranks per lane of wave 0
+  // exclusive sums of entries and of groups, a run of ranks per lane of wave 0
   if (threadIdx.x < kWave) {
     const int32_t per = (ranks + kWave - 1) / kWave, r0 = min(lane * per, ranks), r1 = min(r0 + per, ranks);
-    int32_t mine = 0;
-    for (int32_t r = r0; r < r1; ++r) mine += cursor[r];
-    int32_t incl = mine;
+    int32_t mine = 0, mine_g = 0;
+    for (int32_t r = r0; r < r1; ++r) mine += cursor[r] & 255, mine_g += ((cursor[r] & 255) + 15) / 16;
+    int32_t incl = mine, incl_g = mine_g;
     for (int d = 1; d < kWave; d <<= 1) {
-      const int32_t v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
+      const int32_t v = __shfl_up(incl, d), vg = __shfl_up(incl_g, d);
+      if (lane >= d) incl += v, incl_g += vg;
     }
-    int32_t at = incl - mine;
+    int32_t at = incl - mine, group = incl_g - mine_g;
     for (int32_t r = r0; r < r1; ++r) {
-      const int32_t c = cursor[r];
-      a.first[r] = at;
+      const int32_t c = cursor[r] & 255, e = cursor[r] >> 8;
+      for (int32_t i = 0; i < c; i += 16) {
+        a.expert[group] = e;
+        a.first[group++] = at + i;
+      }
       cursor[r] = at;
       at += c;
     }
-    if (lane == kWave - 1) a.first[ranks] = incl;
+    if (lane == kWave - 1) {
+      *a.groups = incl_g;
+      a.first[incl_g] = incl;
+    }
   }
   __syncthreads();
   // tokens in order; the heads of one token have distinct experts
@@ -211,23 +214,40 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
 #pragma unroll
   for (int i = 0; i < MT; ++i) xp[i] = a.x + (list[min(i * 16 + r, count - 1)] / a.K) * a.xs;
   f32x4 tot[2][MT] = {};
-  for (int32_t b = wave; b < a.hb; b += kUpWaves) {
+  // the next block's weights (and, for up to 16 tokens, its activations) are on their way while
+  // one is multiplied
+  struct Block {
     W w[2];
-    w[0].load(wp[0], b * kBlk, g, a.H);
-    w[1].load(wp[1], b * kBlk, g, a.H);
+    u32x4 x[MT == 1 ? 4 : 1];
+  } blk[2];
+  auto x_at = [&](int i, int32_t c) {
+    return c < a.H ? *reinterpret_cast<const u32x4*>(xp[i] + static_cast<int64_t>(c) * 2) : u32x4{0, 0, 0, 0};
+  };
+  auto load = [&](Block& v, int32_t b) {
+    if (b >= a.hb) return;
+    v.w[0].load(wp[0], b * kBlk, g, a.H);
+    v.w[1].load(wp[1], b * kBlk, g, a.H);
+    if constexpr (MT == 1) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v.x[s] = x_at(0, b * kBlk + W::col(s, g));
+    }
+  };
+  auto multiply = [&](const Block& v, int32_t b) {
+    if (b >= a.hb) return;
+    const float s0 = kFp8 ? wsp[0][b] : 1.0f, s1 = kFp8 ? wsp[1][b] : 1.0f;
     f32x4 p[2][MT] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int32_t c = b * kBlk + W::col(s, g);
-      const u32x4 w0 = w[0].step(s), w1 = w[1].step(s);
+      const u32x4 w0 = v.w[0].step(s), w1 = v.w[1].step(s);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const u32x4 xv = c < a.H ? *reinterpret_cast<const u32x4*>(xp[i] + static_cast<int64_t>(c) * 2) : u32x4{0, 0, 0, 0};
+        u32x4 xv;
+        if constexpr (MT == 1) xv = v.x[s];
+        else xv = x_at(i, b * kBlk + W::col(s, g));
         p[0][i] = Mat<T>::mul(w0, xv, p[0][i]);
         p[1][i] = Mat<T>::mul(w1, xv, p[1][i]);
       }
     }
-    const float s0 = kFp8 ? wsp[0][b] : 1.0f, s1 = kFp8 ? wsp[1][b] : 1.0f;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -235,6 +255,13 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
         tot[0][i][j] = __builtin_fmaf(s0, p[0][i][j], tot[0][i][j]);
         tot[1][i][j] = __builtin_fmaf(s1, p[1][i][j], tot[1][i][j]);
       }
+  };
+  load(blk[0], wave);
+  for (int32_t b = wave; b < a.hb; b += 2 * kUpWaves) {
+    load(blk[1], b + kUpWaves);
+    multiply(blk[0], b);
+    load(blk[0], b + 2 * kUpWaves);
+    multiply(blk[1], b + kUpWaves);
   }
   f32x4* rv = reinterpret_cast<f32x4*>(red);  // [wave][2 MT][lane]
   __syncthreads();                            // `list` may share red's memory with the ids
@@ -323,68 +350,98 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) 
 
 // ------------------------------------------------------------------ launch 2: down, weighted sum
 
-// 16 columns of H.  The 128-blocks of F of all experts are numbered in one row and dealt to the
+// 16 columns of H.  The 128-blocks of F of all groups are numbered in one row and dealt to the
 // waves in turn; each wave adds its totals, times the tokens' weights, into sums of its own
-// [T][16], which are added in wave order.
+// [T][16], which are added in wave order.  The table of experts and entries is copied to LDS
+// first, so that only the loads of weights and h themselves go to memory in the loop, and those
+// of a wave's next block are issued before its present one is multiplied.
 template <class T, bool kFp8>
-__global__ __launch_bounds__(kDownWaves* kWave) void layer_down_kernel(LayerArgs a) {
+__global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerArgs a) {
   using W = Weights<TBF16, kFp8>;
-  extern __shared__ __align__(16) float acc[];  // [waves][T][16]
-  const int32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, r = lane % 16, g = lane / 16;
+  extern __shared__ __align__(16) float acc[];  // [waves][T][16], then the table
+  const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), r = lane % 16, g = lane / 16;
   const int32_t n0 = blockIdx.x * 16;
+  const int32_t groups = uniform(*a.groups);
+  int32_t* le = reinterpret_cast<int32_t*>(acc + kDownWaves * a.T * 16);  // [groups] experts
+  int32_t* lf = le + a.groups_max;                                        // [groups + 1] first entries
+  int32_t* ls = lf + a.groups_max + 1;                                    // [entries] slots
+  float* lw = reinterpret_cast<float*>(ls + a.T * a.K);                   // [entries] weights
   for (int32_t i = threadIdx.x; i < kDownWaves * a.T * 16; i += blockDim.x) acc[i] = 0.0f;
+  for (int32_t i = threadIdx.x; i <= groups; i += blockDim.x) {
+    if (i < groups) le[i] = a.expert[i];
+    lf[i] = a.first[i];
+  }
+  for (int32_t i = threadIdx.x; i < a.T * a.K; i += blockDim.x) {  // past the last entry: not used
+    ls[i] = a.slot[i];
+    lw[i] = a.weight[i];
+  }
   __syncthreads();
   f32x4* mine = reinterpret_cast<f32x4*>(acc) + wave * a.T * 4;
-  const int32_t ranks = uniform(*a.ranks);
   const int64_t rowb = static_cast<int64_t>(a.F) * W::kElt;
-  for (int32_t k = 0; k < ranks; ++k) {
-    const int32_t b0 = (wave - k * a.fb) & (kDownWaves - 1);
-    if (b0 >= a.fb) continue;
-    const int32_t e = uniform(a.expert[k]), at = uniform(a.first[k]), n = uniform(a.first[k + 1]) - at;
-    const char* wp = a.w2 + (static_cast<int64_t>(e) * a.H + n0 + r) * rowb;
-    const float* wsp = kFp8 ? a.w2s + (static_cast<int64_t>(e) * a.hb + n0 / kBlk) * a.fb : nullptr;
-    int64_t hoff[4];
+  struct Block {
+    W w;
+    u32x4 hi[4], lo[4];
+    float s;
+    int32_t group;   // >= groups: none
+  } blk[2];
+  int32_t group = 0, at = wave;  // the next block to load
+  auto load = [&](Block& v) {
+    while (at >= a.fb && group < groups) at -= a.fb, ++group;
+    v.group = group;
+    if (group >= groups) return;
+    const int32_t e = uniform(le[group]), first = lf[group], n = lf[group + 1] - first, c0 = at * kBlk;
+    v.w.load(a.w2 + (static_cast<int64_t>(e) * a.H + n0 + r) * rowb, c0, g, a.F);
+    v.s = kFp8 ? a.w2s[(static_cast<int64_t>(e) * a.hb + n0 / kBlk) * a.fb + at] : 1.0f;
+    const int64_t row = static_cast<int64_t>(ls[first + min(r, n - 1)]) * a.F;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) hoff[i] = static_cast<int64_t>(a.slot[at + min(i * 16 + r, n - 1)]) * a.F * 2;
-    f32x4 tot[4] = {};
-    for (int32_t b = b0; b < a.fb; b += kDownWaves) {
-      W w;
-      w.load(wp, b * kBlk, g, a.F);
-      f32x4 p[4] = {};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int32_t c = b * kBlk + W::col(s, g);
-        const u32x4 wv = w.step(s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i * 16 >= n) break;
-          u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-          if (c < a.F) {
-            hi = *reinterpret_cast<const u32x4*>(a.hhi + hoff[i] + static_cast<int64_t>(c) * 2);
-            lo = *reinterpret_cast<const u32x4*>(a.hlo + hoff[i] + static_cast<int64_t>(c) * 2);
-          }
-          p[i] = Mat<TBF16>::mul(wv, lo, p[i]);
-          p[i] = Mat<TBF16>::mul(wv, hi, p[i]);
-        }
-      }
-      const float s = kFp8 ? wsp[b] : 1.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tot[i][j] = __builtin_fmaf(s, p[i][j], tot[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i * 16 + r < n) {
-        const float c = a.weight[at + i * 16 + r];
-        f32x4* to = mine + a.slot[at + i * 16 + r] / a.K * 4 + g;  // an expert's tokens are distinct
-        f32x4 v = *to;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(c, tot[i][j], v[j]);
-        *to = v;
+    for (int s = 0; s < 4; ++s) {
+      const int32_t c = c0 + W::col(s, g);
+      v.hi[s] = v.lo[s] = u32x4{0, 0, 0, 0};
+      if (c < a.F) {
+        v.hi[s] = *reinterpret_cast<const u32x4*>(a.hhi + (row + c) * 2);
+        v.lo[s] = *reinterpret_cast<const u32x4*>(a.hlo + (row + c) * 2);
       }
     }
+    at += kDownWaves;
+  };
+  f32x4 tot = {0, 0, 0, 0};
+  int32_t cur = -1;
+  auto finish = [&] {  // the totals of a group's tokens into this wave's sums
+    const int32_t first = lf[cur], n = lf[cur + 1] - first;
+    if (r < n) {
+      f32x4* to = mine + ls[first + r] / a.K * 4 + g;  // an expert's tokens are distinct
+      const float c = lw[first + r];
+      f32x4 v = *to;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __builtin_fmaf(c, tot[j], v[j]);
+      *to = v;
+    }
+    tot = f32x4{0, 0, 0, 0};
+  };
+  auto multiply = [&](const Block& v) {
+    if (v.group >= groups) return;
+    if (cur != v.group) {
+      if (cur >= 0) finish();
+      cur = v.group;
+    }
+    f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const u32x4 wv = v.w.step(s);
+      p = Mat<TBF16>::mul(wv, v.lo[s], p);
+      p = Mat<TBF16>::mul(wv, v.hi[s], p);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tot[j] = __builtin_fmaf(v.s, p[j], tot[j]);
+  };
+  load(blk[0]);
+  while (blk[0].group < groups) {
+    load(blk[1]);
+    multiply(blk[0]);
+    load(blk[0]);
+    multiply(blk[1]);
   }
+  if (cur >= 0) finish();
   __syncthreads();
   for (int32_t i = threadIdx.x; i < a.T * 16; i += blockDim.x) {
     float v = 0.0f;
@@ -426,13 +483,14 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t n = p->T * p->K;
   p->ranks = n < p->E ? n : p->E;
+  p->groups = p->ranks + n / 16 < n ? p->ranks + n / 16 : n;
   // one dimension of the grid: fewer than 2^32 threads
   if (p->ranks * (p->F / 16) >= (int64_t{1} << 32) / (kUpWaves * kWave) - 1) return FFNWB_ERR_PARAM_INVALID;
   Carve c;
   if (n > 0) {
     c.take<int32_t>(1);
-    c.take<int32_t>(static_cast<size_t>(p->ranks));
-    c.take<int32_t>(static_cast<size_t>(p->ranks) + 1);
+    c.take<int32_t>(static_cast<size_t>(p->groups));
+    c.take<int32_t>(static_cast<size_t>(p->groups) + 1);
     c.take<int32_t>(static_cast<size_t>(n));
     c.take<float>(static_cast<size_t>(n));
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
@@ -446,8 +504,10 @@ template <class T, bool kFp8>
 static bool launch_t(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void* begin, void* end) {
   const uint32_t grid = static_cast<uint32_t>(1 + p.ranks * a.ctiles);
   if (!launch_bound(layer_up_kernel<T, kFp8>, dim3(grid), dim3(kUpWaves * kWave), 0, s, begin, nullptr, a)) return false;
-  return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16)), dim3(kDownWaves * kWave),
-                      static_cast<size_t>(kDownWaves * p.T * 16 * 4), s, nullptr, end, a);
+  const size_t lds = (kDownWaves * p.T * 16 + 2 * p.groups + 1 + 2 * p.T * p.K) * 4;
+  allow_large_lds(reinterpret_cast<const void*>(layer_down_kernel<T, kFp8>), lds);
+  return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16)), dim3(kDownWaves * kWave), lds, s, nullptr,
+                      end, a);
 }
 
 int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStream_t s) {
@@ -457,6 +517,7 @@ int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStrea
   a.H = static_cast<int32_t>(p.H), a.F = static_cast<int32_t>(p.F);
   a.hb = (a.H + kBlk - 1) / kBlk, a.fb = (a.F + kBlk - 1) / kBlk, a.nb13 = (2 * a.F + kBlk - 1) / kBlk;
   a.ctiles = a.F / 16;
+  a.groups_max = static_cast<int32_t>(p.groups);
   a.id64 = d->id_dtype == FFNWB_DT_INT64;
   a.scale_dtype = d->scale_dtype;
   a.xs = p.xs, a.ys = p.ys, a.is = p.is, a.ss = p.ss, a.ms = p.ms;
@@ -467,9 +528,9 @@ int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStrea
   const size_t n = static_cast<size_t>(p.T * p.K);
   Carve c;
   c.base = static_cast<char*>(ws);
-  a.ranks = c.take<int32_t>(1);
-  a.expert = c.take<int32_t>(static_cast<size_t>(p.ranks));
-  a.first = c.take<int32_t>(static_cast<size_t>(p.ranks) + 1);
+  a.groups = c.take<int32_t>(1);
+  a.expert = c.take<int32_t>(static_cast<size_t>(p.groups));
+  a.first = c.take<int32_t>(static_cast<size_t>(p.groups) + 1);
   a.slot = c.take<int32_t>(n);
   a.weight = c.take<float>(n);
   a.hhi = reinterpret_cast<char*>(c.take<uint16_t>(n * p.F));

@@ -354,7 +354,11 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) 
 // waves in turn; each wave adds its totals, times the tokens' weights, into sums of its own
 // [T][16], which are added in wave order.  The table of experts and entries is copied to LDS
 // first, so that only the loads of weights and h themselves go to memory in the loop, and those
-// of a wave's next block are issued before its present one is multiplied.
+// of a wave's next block are issued before its present one is multiplied.  A group of up to 8
+// tokens takes the upper and lower parts of h as the two halves of one operand, which halves the
+// loads of h: they cost more of the CU's load path than e4m3 weights do (16 tokens' layer of
+// hidden 7168 519 -> 457 us).  BF16 weights are twice as many bytes, and their two blocks fill the
+// registers: they always take the parts apart (64 tokens, hidden 4096: 131 us, with the choice 177).
 template <class T, bool kFp8>
 __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerArgs a) {
   using W = Weights<TBF16, kFp8>;
@@ -380,8 +384,9 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
   const int64_t rowb = static_cast<int64_t>(a.F) * W::kElt;
   struct Block {
     W w;
-    u32x4 hi[4], lo[4];
+    u32x4 h[4], lo[4];
     float s;
+    bool both;       // the parts of h in operands of their own
     int32_t group;   // >= groups: none
   } blk[2];
   int32_t group = 0, at = wave;  // the next block to load
@@ -392,14 +397,19 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
     const int32_t e = uniform(le[group]), first = lf[group], n = lf[group + 1] - first, c0 = at * kBlk;
     v.w.load(a.w2 + (static_cast<int64_t>(e) * a.H + n0 + r) * rowb, c0, g, a.F);
     v.s = kFp8 ? a.w2s[(static_cast<int64_t>(e) * a.hb + n0 / kBlk) * a.fb + at] : 1.0f;
-    const int64_t row = static_cast<int64_t>(ls[first + min(r, n - 1)]) * a.F;
+    v.both = !kFp8 || uniform(n) > 8;
+    const int64_t row = static_cast<int64_t>(ls[first + min(v.both ? r : r & 7, n - 1)]) * a.F;
+    const char* h0 = v.both || r < 8 ? a.hhi : a.hlo;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const int32_t c = c0 + W::col(s, g);
-      v.hi[s] = v.lo[s] = u32x4{0, 0, 0, 0};
-      if (c < a.F) {
-        v.hi[s] = *reinterpret_cast<const u32x4*>(a.hhi + (row + c) * 2);
-        v.lo[s] = *reinterpret_cast<const u32x4*>(a.hlo + (row + c) * 2);
+      v.h[s] = c < a.F ? *reinterpret_cast<const u32x4*>(h0 + (row + c) * 2) : u32x4{0, 0, 0, 0};
+    }
+    if (v.both) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const int32_t c = c0 + W::col(s, g);
+        v.lo[s] = c < a.F ? *reinterpret_cast<const u32x4*>(a.hlo + (row + c) * 2) : u32x4{0, 0, 0, 0};
       }
     }
     at += kDownWaves;
@@ -408,6 +418,10 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
   int32_t cur = -1;
   auto finish = [&] {  // the totals of a group's tokens into this wave's sums
     const int32_t first = lf[cur], n = lf[cur + 1] - first;
+    if (kFp8 && n <= 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tot[j] += __shfl_xor(tot[j], 8);  // the parts of h
+    }
     if (r < n) {
       f32x4* to = mine + ls[first + r] / a.K * 4 + g;  // an expert's tokens are distinct
       const float c = lw[first + r];
@@ -428,8 +442,8 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const u32x4 wv = v.w.step(s);
-      p = Mat<TBF16>::mul(wv, v.lo[s], p);
-      p = Mat<TBF16>::mul(wv, v.hi[s], p);
+      if (v.both) p = Mat<TBF16>::mul(wv, v.lo[s], p);
+      p = Mat<TBF16>::mul(wv, v.h[s], p);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) tot[j] = __builtin_fmaf(v.s, p[j], tot[j]);

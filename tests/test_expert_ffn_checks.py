@@ -110,8 +110,9 @@ def test_invalid_parameters(name, over):
 
 
 def test_workspace_is_checked_before_any_device_work():
-    for name in ("moe_grouped_matmul_fp8", "moe_layer"):
-        d = MAKE[name]()
+    for name, over in (("moe_grouped_matmul_fp8", dict(num_groups=2000)),
+                       ("moe_grouped_matmul_fp8", dict(epilogue=1, out_features=64, out_dtype=6)), ("moe_layer", {})):
+        d = MAKE[name](**over)
         st, n = _ws(name, d)
         assert st == 0 and n > 0
         call = getattr(F.lib(), name)
@@ -170,7 +171,8 @@ def test_valid_calls_build():
         dict(group_list=torch.zeros(4, 2, dtype=i32)), dict(group_list=torch.zeros(8, dtype=i64)),
         dict(group_list=torch.zeros(4, 4, dtype=i64)[:, ::2]), dict(out_dtype=torch.int8),
         dict(out={"y": torch.zeros(8, 95, dtype=BF16)}), dict(out={"y": torch.zeros(8, 96)}), dict(out={"y_scale": torch.zeros(8, 1)}),
-        dict(workspace=torch.zeros(8, dtype=torch.uint8)), dict(workspace=torch.zeros(1 << 16)))],
+        dict(workspace=torch.zeros(8, dtype=torch.uint8), group_list=torch.zeros(2000, 2, dtype=i64)),
+        dict(workspace=torch.zeros(1 << 16), group_list=torch.zeros(2000, 2, dtype=i64)))],
     *[(_layer_call, o) for o in (
         dict(x=torch.zeros(4, 256)), dict(x=torch.zeros(4, 512, dtype=BF16)[:, ::2]), dict(expert_ids=torch.zeros(3, 3, dtype=i32)),
         dict(expert_ids=torch.zeros(4, 3)), dict(expert_scales=torch.zeros(4, 2)), dict(active_mask=torch.ones(4)),

@@ -10,10 +10,12 @@
 namespace ffnwb {
 
 struct MmArgs {
-  int64_t rows, K, N, F;       // F = outputs per row (N, or N / 2 with SwiGLU)
+  int64_t K, N, F;             // F = outputs per row (N, or N / 2 with SwiGLU)
   int64_t xs, xss, ys, yss;    // row strides: bytes, elements, bytes, elements
+  int32_t rows;
   int32_t kb, nb;              // 128-blocks along K and N
-  int32_t mtiles, ntiles;      // row tiles of a dense product, column tiles
+  int32_t ntiles;              // column tiles
+  int32_t ngroups, nexperts;
   bool vec;                    // four adjacent outputs are one aligned store
   const char* x;
   const float* x_scale;
@@ -21,88 +23,152 @@ struct MmArgs {
   const float* w_scale;
   char* y;
   float* y_scale;
-  const int4* table;           // row tiles {expert, first row, rows, 0}, or NULL for a dense product
+  const int64_t* groups;       // {expert, rows} pairs, or NULL for one dense product
+  const int4* table;           // row tiles {expert, first row, rows, 0} of more than kWaveGroups groups
   const int32_t* count;        // [1] row tiles of the table
 };
 
-// ------------------------------------------------------------------ tile table
+// ------------------------------------------------------------------ row tiles
 
-constexpr int kTableThreads = 1024;
-
-// Row tiles of bm rows (a power of two) in group order.  Each thread takes a run of
-// consecutive groups; sums over threads give every run its first row and first tile.
-// Counts are clamped so that the rows never pass `rows`: the table then has at most
-// ceil(rows / bm) + min(groups, rows) entries.
-__global__ __launch_bounds__(kTableThreads) void mm_table_kernel(const int64_t* groups, int32_t ngroups, int64_t rows,
-                                                                 int64_t nexperts, int32_t bm, int4* table, int32_t* count) {
-  __shared__ int64_t sum_rows[kTableThreads];
-  __shared__ int32_t sum_tiles[kTableThreads];
-  const int32_t per = (ngroups + kTableThreads - 1) / kTableThreads;
-  const int32_t g0 = threadIdx.x * per, g1 = min(g0 + per, ngroups);
-  int64_t mine = 0;
-  for (int32_t g = g0; g < g1; ++g) mine += min(max(groups[2 * g + 1], int64_t{0}), rows);
-  sum_rows[threadIdx.x] = mine;
-  __syncthreads();
-  for (int d = 1; d < kTableThreads; d <<= 1) {
-    const int64_t v = threadIdx.x >= static_cast<uint32_t>(d) ? sum_rows[threadIdx.x - d] : 0;
-    __syncthreads();
-    sum_rows[threadIdx.x] += v;
-    __syncthreads();
-  }
-  const int64_t first = min(sum_rows[threadIdx.x] - mine, rows);
-  int64_t at = first;
-  int32_t tiles = 0;
-  for (int32_t g = g0; g < g1; ++g) {
-    const int64_t n = min(min(max(groups[2 * g + 1], int64_t{0}), rows), rows - at), key = groups[2 * g];
-    if (key >= 0 && key < nexperts) tiles += static_cast<int32_t>((n + bm - 1) / bm);
-    at += n;
-  }
-  sum_tiles[threadIdx.x] = tiles;
-  __syncthreads();
-  for (int d = 1; d < kTableThreads; d <<= 1) {
-    const int32_t v = threadIdx.x >= static_cast<uint32_t>(d) ? sum_tiles[threadIdx.x - d] : 0;
-    __syncthreads();
-    sum_tiles[threadIdx.x] += v;
-    __syncthreads();
-  }
-  int32_t t = sum_tiles[threadIdx.x] - tiles;
-  if (threadIdx.x == kTableThreads - 1) *count = sum_tiles[threadIdx.x];
-  at = first;
-  for (int32_t g = g0; g < g1; ++g) {
-    const int64_t n = min(min(max(groups[2 * g + 1], int64_t{0}), rows), rows - at), key = groups[2 * g];
-    if (key >= 0 && key < nexperts) {
-      for (int64_t r = 0; r < n; r += bm)
-        table[t++] = int4{static_cast<int>(key), static_cast<int>(at + r), static_cast<int>(min(n - r, int64_t{bm})), 0};
-    }
-    at += n;
-  }
+// Sums over the lanes up to and including this one, saturating at `cap` (terms are >= 0, so the
+// order of the additions does not matter).
+__device__ __forceinline__ int32_t wave_scan(int32_t v, int32_t cap) {
+#define FFNWB_SCAN_STEP(ctrl, rows) v = min(v + __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xf, false), cap)
+  FFNWB_SCAN_STEP(0x111, 0xf);  // within rows of 16 lanes: one lane below, two, four, eight
+  FFNWB_SCAN_STEP(0x112, 0xf);
+  FFNWB_SCAN_STEP(0x114, 0xf);
+  FFNWB_SCAN_STEP(0x118, 0xf);
+  FFNWB_SCAN_STEP(0x142, 0xa);  // lane 15 of a row into the next row, lane 31 into the upper half
+  FFNWB_SCAN_STEP(0x143, 0xc);
+#undef FFNWB_SCAN_STEP
+  return v;
 }
 
-// Row tile and column tile of a workgroup.  Workgroups go round the 8 XCDs, each with its own
-// L2: XCD x gets the x-th eighth of the tiles, and walks it 8 row tiles by all column tiles at
-// a time, row tiles first, so that workgroups running together share rows of x and of w.
-__device__ __forceinline__ bool tile_of_block(const MmArgs& a, int32_t& m, int32_t& c) {
-  constexpr int32_t kXcds = 8, kRun = 8;
-  const int32_t mt = a.table != nullptr ? *a.count : a.mtiles, total = mt * a.ntiles;
-  const int32_t per = (total + kXcds - 1) / kXcds, place = blockIdx.x / kXcds, t = blockIdx.x % kXcds * per + place;
-  if (place >= per || t >= total) return false;
-  const int32_t run = t / (kRun * a.ntiles), first = run * kRun, rows = min(kRun, mt - first), at = t - first * a.ntiles;
-  m = first + at % rows;
-  c = at / rows;
-  return true;
+// Rows of a group that starts at row `at`, and whether they belong to an expert.
+__device__ __forceinline__ int32_t group_rows(int64_t count, int32_t at, int32_t rows) {
+  return static_cast<int32_t>(min(max(count, int64_t{0}), static_cast<int64_t>(rows - at)));
 }
 
 struct RowTile { int32_t expert, row0, rows; };
 
-// The row tile m, or rows = 0 past the last one.
-__device__ __forceinline__ RowTile row_tile(const MmArgs& a, int32_t m, int32_t bm) {
-  if (a.table == nullptr) {
-    const int64_t r0 = static_cast<int64_t>(m) * bm;
-    return RowTile{0, static_cast<int32_t>(r0), static_cast<int32_t>(min(a.rows - r0, int64_t{bm}))};
+constexpr int kWaveGroups = 256;  // groups that one wave lists by itself, four to a lane
+
+// The row tiles of all groups, as every wave of a product's kernel works them out for itself:
+// for up to 256 groups that costs a kernel about 1 us, and a launch of its own 5 us.
+struct WaveTiles {
+  int32_t tiles = 0, first_tile = 0, first_row = 0;  // of this lane's groups
+  int32_t total = 0;
+  int32_t key[4], n[4];
+  __device__ void list(const MmArgs& a, int32_t bm) {
+    const int32_t g0 = 4 * static_cast<int32_t>(lane_id());
+    int64_t cnt[4];
+    int32_t mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = g0 + j < a.ngroups;
+      const int64_t k = in ? a.groups[2 * (g0 + j)] : -1;
+      cnt[j] = in ? a.groups[2 * (g0 + j) + 1] : 0;
+      key[j] = k >= 0 && k < a.nexperts ? static_cast<int32_t>(k) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine = min(mine + group_rows(cnt[j], 0, a.rows), a.rows);
+    const int32_t upto = wave_scan(mine, a.rows);
+    // rows before this lane's: a saturated sum does not subtract, so take the neighbour's
+    first_row = __shfl_up(upto, 1);
+    if (g0 == 0) first_row = 0;
+    int32_t at = first_row;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      n[j] = group_rows(cnt[j], at, a.rows);
+      at += n[j];
+      if (key[j] >= 0) tiles += (n[j] + bm - 1) / bm;
+    }
+    const int32_t incl = wave_scan(tiles, 0x7fffffff);
+    first_tile = incl - tiles;
+    total = __builtin_amdgcn_readlane(incl, kWave - 1);
   }
-  if (m >= *a.count) return RowTile{0, 0, 0};
-  const int4 t = a.table[m];
-  return RowTile{uniform(t.x), uniform(t.y), uniform(t.z)};
+  __device__ RowTile at(int32_t m, int32_t bm) const {
+    const uint64_t has = wave_ballot(first_tile <= m && m < first_tile + tiles);
+    const int32_t lane = __builtin_ctzll(has);
+    int32_t t = m - first_tile, row = first_row;
+    int4 f = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int32_t here = key[j] >= 0 ? (n[j] + bm - 1) / bm : 0;
+      if (t >= 0 && t < here) f = int4{key[j], row + t * bm, min(n[j] - t * bm, bm), 0};
+      t -= here;
+      row += n[j];
+    }
+    return RowTile{__builtin_amdgcn_readlane(f.x, lane), __builtin_amdgcn_readlane(f.y, lane), __builtin_amdgcn_readlane(f.z, lane)};
+  }
+};
+
+constexpr int kTableThreads = 1024;
+
+// The same list for more groups, in a launch of its own.  Each thread takes a run of consecutive
+// groups.  The table has at most ceil(rows / bm) + min(groups, rows) entries.
+__global__ __launch_bounds__(kTableThreads) void mm_table_kernel(MmArgs a, int32_t bm, int4* table, int32_t* count) {
+  __shared__ int32_t wave_rows[kTableThreads / kWave], wave_tiles[kTableThreads / kWave];
+  const int32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  const int32_t per = (a.ngroups + kTableThreads - 1) / kTableThreads;
+  const int32_t g0 = threadIdx.x * per, g1 = min(g0 + per, a.ngroups);
+  int32_t mine = 0;
+  for (int32_t g = g0; g < g1; ++g) mine = min(mine + group_rows(a.groups[2 * g + 1], 0, a.rows), a.rows);
+  int32_t incl = wave_scan(mine, a.rows);
+  int32_t first = __shfl_up(incl, 1);
+  if (lane == 0) first = 0;
+  if (lane == kWave - 1) wave_rows[wave] = incl;
+  __syncthreads();
+  for (int32_t w = 0; w < wave; ++w) first = min(first + wave_rows[w], a.rows);
+  int32_t at = first, tiles = 0;
+  for (int32_t g = g0; g < g1; ++g) {
+    const int32_t n = group_rows(a.groups[2 * g + 1], at, a.rows);
+    const int64_t key = a.groups[2 * g];
+    if (key >= 0 && key < a.nexperts) tiles += (n + bm - 1) / bm;
+    at += n;
+  }
+  incl = wave_scan(tiles, 0x7fffffff);
+  if (lane == kWave - 1) wave_tiles[wave] = incl;
+  __syncthreads();
+  int32_t t = incl - tiles;
+  for (int32_t w = 0; w < wave; ++w) t += wave_tiles[w];
+  if (threadIdx.x == kTableThreads - 1) *count = t + tiles;
+  at = first;
+  for (int32_t g = g0; g < g1; ++g) {
+    const int32_t n = group_rows(a.groups[2 * g + 1], at, a.rows);
+    const int64_t key = a.groups[2 * g];
+    if (key >= 0 && key < a.nexperts)
+      for (int32_t r = 0; r < n; r += bm) table[t++] = int4{static_cast<int>(key), at + r, min(n - r, bm), 0};
+    at += n;
+  }
+}
+
+// The row tile and column tile of a workgroup; false for a workgroup without one.  Workgroups go
+// round the 8 XCDs, each with its own L2: XCD x gets the x-th eighth of the tiles, and walks it
+// 8 row tiles by all column tiles at a time, row tiles first, so that workgroups running
+// together share rows of x and of w.
+__device__ __forceinline__ bool find_tile(const MmArgs& a, int32_t bm, RowTile& rt, int32_t& c) {
+  constexpr int32_t kXcds = 8, kRun = 8;
+  WaveTiles wt;
+  int32_t mt;
+  if (a.groups == nullptr) mt = (a.rows + bm - 1) / bm;
+  else if (a.table != nullptr) mt = *a.count;
+  else wt.list(a, bm), mt = wt.total;
+  const int32_t total = mt * a.ntiles;
+  const int32_t per = (total + kXcds - 1) / kXcds, place = blockIdx.x / kXcds, t = blockIdx.x % kXcds * per + place;
+  if (place >= per || t >= total) return false;
+  const int32_t run = t / (kRun * a.ntiles), first = run * kRun, rows = min(kRun, mt - first), in = t - first * a.ntiles;
+  const int32_t m = first + in % rows;
+  c = in / rows;
+  if (a.groups == nullptr) {
+    rt = RowTile{0, m * bm, min(a.rows - m * bm, bm)};
+  } else if (a.table != nullptr) {
+    const int4 v = a.table[m];
+    rt = RowTile{uniform(v.x), uniform(v.y), uniform(v.z)};
+  } else {
+    rt = wt.at(m, bm);
+  }
+  return true;
 }
 
 // Four adjacent outputs n .. n + 3 of one row, those below `end`.
@@ -125,30 +191,28 @@ __device__ __forceinline__ void store4(char* row, int64_t n, int64_t end, const 
 
 // ------------------------------------------------------------------ direct kernel
 //
-// A workgroup of 4 waves takes MT * 16 rows by 32 columns (SwiGLU: 16 gate and 16 up columns);
-// each wave takes every fourth block along K straight from memory to registers, and the four
-// totals are added in wave order.  The weights are read once per row tile.
-
-constexpr int kDirectWaves = 4;
+// For few rows, where the weights are read once and latency counts.  A workgroup takes MT * 16
+// rows by 16 columns (SwiGLU: 16 gate and the 16 up columns that go with them); its waves take
+// the 128-column blocks of K in turn, straight from memory to registers, a wave's next block
+// ahead of its present one, and their totals are added in wave order.
 
 template <class T, int EPI, int MT>
-__global__ __launch_bounds__(kDirectWaves* kWave) void mm_direct_kernel(MmArgs a) {
-  __shared__ float red[kDirectWaves][2 * MT][kWave][4];
-  const int32_t m = blockIdx.x / a.ntiles, c = blockIdx.x - m * a.ntiles;
-  const RowTile rt = row_tile(a, m, MT * 16);
-  if (rt.rows <= 0) return;
-  const int32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+__global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm_direct_kernel(MmArgs a) {
+  constexpr int NF = EPI == FFNWB_EPI_SWIGLU ? 2 : 1;
+  extern __shared__ __align__(16) f32x4 red[];  // [waves][NF * MT][lanes]
+  RowTile rt;
+  int32_t c;
+  if (!find_tile(a, MT * 16, rt, c)) return;
+  const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), waves = blockDim.x / kWave;
   const int32_t r = lane % 16, g = lane / 16;
-  // the two fragments' first weight rows
-  const int64_t n0 = EPI == FFNWB_EPI_SWIGLU ? int64_t{c} * 16 : int64_t{c} * 32;
-  const int64_t n1 = EPI == FFNWB_EPI_SWIGLU ? a.F + n0 : n0 + 16;
-  const char* wp[2];
-  const float* wsp[2];
+  const int64_t n0 = int64_t{c} * 16;
+  const char* wp[NF];
+  const float* wsp[NF];
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const int64_t nf = f == 0 ? n0 : n1;
+  for (int f = 0; f < NF; ++f) {
+    const int64_t nf = n0 + f * a.F;  // the fragment's first weight row
     wp[f] = a.w + (static_cast<int64_t>(rt.expert) * a.N + min(nf + r, a.N - 1)) * a.K;
-    wsp[f] = a.w_scale + (static_cast<int64_t>(rt.expert) * a.nb + min(nf, a.N - 1) / kBlk) * a.kb;
+    wsp[f] = a.w_scale + (static_cast<int64_t>(rt.expert) * a.nb + nf / kBlk) * a.kb;
   }
   const char* xp[MT];
   const float* xsp[MT];
@@ -158,69 +222,77 @@ __global__ __launch_bounds__(kDirectWaves* kWave) void mm_direct_kernel(MmArgs a
     xp[i] = a.x + row * a.xs;
     xsp[i] = a.x_scale + row * a.xss;
   }
-  f32x4 tot[2][MT] = {};
+  struct Block {
+    u32x4 w[NF][2], x[MT][2];
+    float ws[NF], xs[MT];
+  } blk[2];
   const u32x4 zero = {0, 0, 0, 0};
-  for (int32_t b = wave; b < a.kb; b += kDirectWaves) {
+  auto load = [&](Block& v, int32_t b) {
+    if (b >= a.kb) return;
     const int64_t k0 = static_cast<int64_t>(b) * kBlk + g * 16, k1 = k0 + 64;
-    const bool in0 = k0 < a.K, in1 = k1 < a.K;   // K is a multiple of 16
-    u32x4 wv[2][2];
+    const bool in0 = k0 < a.K, in1 = k1 < a.K;  // K is a multiple of 16
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      wv[f][0] = in0 ? *reinterpret_cast<const u32x4*>(wp[f] + k0) : zero;
-      wv[f][1] = in1 ? *reinterpret_cast<const u32x4*>(wp[f] + k1) : zero;
+    for (int f = 0; f < NF; ++f) {
+      v.w[f][0] = in0 ? *reinterpret_cast<const u32x4*>(wp[f] + k0) : zero;
+      v.w[f][1] = in1 ? *reinterpret_cast<const u32x4*>(wp[f] + k1) : zero;
+      v.ws[f] = wsp[f][b];
     }
-    f32x4 p[2][MT] = {};
-    float xsc[MT];
-    u32x4 xv[MT][2];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      xsc[i] = xsp[i][b];
-      xv[i][0] = in0 ? *reinterpret_cast<const u32x4*>(xp[i] + k0) : zero;
-      xv[i][1] = in1 ? *reinterpret_cast<const u32x4*>(xp[i] + k1) : zero;
+      v.x[i][0] = in0 ? *reinterpret_cast<const u32x4*>(xp[i] + k0) : zero;
+      v.x[i][1] = in1 ? *reinterpret_cast<const u32x4*>(xp[i] + k1) : zero;
+      v.xs[i] = xsp[i][b];
     }
+  };
+  f32x4 tot[NF][MT] = {};
+  auto multiply = [&](const Block& v, int32_t b) {
+    if (b >= a.kb) return;
+    f32x4 p[NF][MT] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {  // 8 columns of each lane
-      const u32x4 w0 = widen8(wv[0][s / 2][2 * (s % 2)], wv[0][s / 2][2 * (s % 2) + 1]);
-      const u32x4 w1 = widen8(wv[1][s / 2][2 * (s % 2)], wv[1][s / 2][2 * (s % 2) + 1]);
+      u32x4 w8[NF];
+#pragma unroll
+      for (int f = 0; f < NF; ++f) w8[f] = widen8(v.w[f][s / 2][2 * (s % 2)], v.w[f][s / 2][2 * (s % 2) + 1]);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const u32x4 x8 = widen8(xv[i][s / 2][2 * (s % 2)], xv[i][s / 2][2 * (s % 2) + 1]);
-        p[0][i] = Mat<TBF16>::mul(w0, x8, p[0][i]);
-        p[1][i] = Mat<TBF16>::mul(w1, x8, p[1][i]);
+        const u32x4 x8 = widen8(v.x[i][s / 2][2 * (s % 2)], v.x[i][s / 2][2 * (s % 2) + 1]);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) p[f][i] = Mat<TBF16>::mul(w8[f], x8, p[f][i]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float s = xsc[i] * wsp[f][b];
+      for (int f = 0; f < NF; ++f) {
+        const float s = v.xs[i] * v.ws[f];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tot[f][i][j] = __builtin_fmaf(s, p[f][i][j], tot[f][i][j]);
       }
-    }
+  };
+  load(blk[0], wave);
+  for (int32_t b = wave; b < a.kb; b += 2 * waves) {
+    load(blk[1], b + waves);
+    multiply(blk[0], b);
+    load(blk[0], b + 2 * waves);
+    multiply(blk[1], b + waves);
   }
 #pragma unroll
-  for (int f = 0; f < 2; ++f)
+  for (int f = 0; f < NF; ++f)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(red[wave][f * MT + i][lane]) = tot[f][i];
+    for (int i = 0; i < MT; ++i) red[(wave * NF * MT + f * MT + i) * kWave + lane] = tot[f][i];
   __syncthreads();
-  for (int i = wave; i < MT; i += kDirectWaves) {
-    f32x4 s[2] = {};
+  for (int32_t i = wave; i < MT; i += waves) {
+    f32x4 s[NF] = {};
+    for (int32_t w = 0; w < waves; ++w)
 #pragma unroll
-    for (int w = 0; w < kDirectWaves; ++w)
-#pragma unroll
-      for (int f = 0; f < 2; ++f) s[f] += *reinterpret_cast<const f32x4*>(red[w][f * MT + i][lane]);
+      for (int f = 0; f < NF; ++f) s[f] += red[(w * NF * MT + f * MT + i) * kWave + lane];
     if (i * 16 + r >= rt.rows) continue;
     char* row = a.y + static_cast<int64_t>(rt.row0 + i * 16 + r) * a.ys;
     if constexpr (EPI == FFNWB_EPI_SWIGLU) {
-      f32x4 h;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = swiglu(s[0][j], s[1][j]);
-      store4<T>(row, n0 + g * 4, a.F, h, a.vec);
-    } else {
-      store4<T>(row, n0 + g * 4, a.N, s[0], a.vec);
-      store4<T>(row, n1 + g * 4, a.N, s[1], a.vec);
+      for (int j = 0; j < 4; ++j) s[0][j] = swiglu(s[0][j], s[1][j]);
     }
+    store4<T>(row, n0 + g * 4, a.F, s[0], a.vec);
   }
 }
 
@@ -233,17 +305,17 @@ namespace ffnwb {
 // ------------------------------------------------------------------ quantising a product
 //
 // For the products whose column tiles are narrower than a block: SwiGLU results h [R, F] in
-// FP32 to e4m3 rows, row tile by row tile so that rows of no expert stay as they were.
-// 16 lanes take a block, as in moe_quant_fp8.
+// FP32 to e4m3 rows.  16 lanes take a block, as in moe_quant_fp8; a workgroup takes 16 blocks of
+// a row tile, so that rows of no expert stay as they were.
 
 constexpr int kMqThreads = 256;
 
 __global__ __launch_bounds__(kMqThreads) void mm_quant_kernel(MmArgs a, const float* h, int32_t bm) {
   const int32_t fb = static_cast<int32_t>((a.F + kBlk - 1) / kBlk);
-  const int32_t per = (bm * fb * 16 + kMqThreads - 1) / kMqThreads;  // workgroups of a row tile
-  const int32_t m = blockIdx.x / per;
-  const RowTile rt = row_tile(a, m, bm);
-  const int32_t u = (blockIdx.x - m * per) * (kMqThreads / 16) + threadIdx.x / 16;
+  RowTile rt;
+  int32_t part;
+  if (!find_tile(a, bm, rt, part)) return;
+  const int32_t u = part * (kMqThreads / 16) + threadIdx.x / 16;
   const int32_t i = u / fb, b = u - i * fb;
   const int64_t row = rt.row0 + i, f0 = static_cast<int64_t>(b) * kBlk + threadIdx.x % 16 * 8;
   const bool in = i < rt.rows && f0 < a.F;  // F is a multiple of 16
@@ -313,7 +385,7 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   auto shape = [&](bool tile, int64_t bm) {
     p->tile = tile, p->bm = bm;
     p->mtiles = (p->R + bm - 1) / bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
-    p->ntiles = tile ? (swiglu ? (p->F + 127) / 128 : (p->N + 255) / 256) : (swiglu ? p->F / 16 : (p->N + 31) / 32);
+    p->ntiles = tile ? (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256) : (p->F + 15) / 16;
     return p->mtiles * p->ntiles;
   };
   // Through LDS, with the largest tile that the groups fill on average and that leaves every CU
@@ -322,11 +394,15 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   int64_t bm = avg > 1024 && fast ? 256 : avg > 128 ? 128 : avg > 64 ? 64 : 32;
   while (bm > 32 && shape(true, bm) < kCus) bm /= 2;
   if (p->xs > (1 << 22) || shape(true, bm) < kCus / 2) shape(false, avg <= 16 ? 16 : avg <= 32 ? 32 : 64);
-  // one dimension of the grid: fewer than 2^32 threads of at most 512 a workgroup
-  if (p->mtiles * p->ntiles >= (int64_t{1} << 22)) return FFNWB_ERR_PARAM_INVALID;
+  // one dimension of the grid: fewer than 2^32 threads of at most 1024 a workgroup
+  if (p->mtiles * p->ntiles > (int64_t{1} << 22) - 8) return FFNWB_ERR_PARAM_INVALID;
+  p->quant_parts = (p->bm * fb + kMqThreads / 16 - 1) / (kMqThreads / 16);
+  if (quant && !p->tile && p->mtiles * p->quant_parts > (int64_t{1} << 22) - 8) return FFNWB_ERR_PARAM_INVALID;
   p->ws_bytes = 0;
   Carve c;
-  if (d->group_list != nullptr && p->R > 0) {
+  // The list in every workgroup costs each about 1 us, two to a CU at a time; the launch 4 us.
+  p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > 16 * kCus));
+  if (p->table) {
     c.take<int32_t>(1);
     c.take<int4>(static_cast<size_t>(p->mtiles));
   }
@@ -335,12 +411,26 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   return FFNWB_OK;
 }
 
+// Workgroups round the XCDs (find_tile): a multiple of 8.
+static uint32_t tile_grid(int64_t tiles) { return static_cast<uint32_t>((tiles + 7) / 8 * 8); }
+
+template <class T, int EPI, int MT>
+static bool launch_direct_rows(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  // Waves of a workgroup: at least one block of K each, two where there are enough workgroups
+  // to fill the chip.
+  int waves = 4;
+  while (waves < (MT == 1 ? 16 : 8) && waves * 2 <= p.kb && p.mtiles * p.ntiles * waves < kCus * 16) waves *= 2;
+  const size_t lds = static_cast<size_t>(waves) * (EPI == FFNWB_EPI_SWIGLU ? 2 : 1) * MT * kWave * 16;
+  auto kernel = mm_direct_kernel<T, EPI, MT>;
+  allow_large_lds(reinterpret_cast<const void*>(kernel), lds);
+  return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles)), dim3(static_cast<uint32_t>(waves * kWave)), lds, s, b, e, a);
+}
+
 template <class T, int EPI>
 static bool launch_direct(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
-  const dim3 grid(static_cast<uint32_t>(p.mtiles * p.ntiles)), block(kDirectWaves * kWave);
-  return p.bm == 16   ? launch_bound(mm_direct_kernel<T, EPI, 1>, grid, block, 0, s, b, e, a)
-         : p.bm == 32 ? launch_bound(mm_direct_kernel<T, EPI, 2>, grid, block, 0, s, b, e, a)
-                     : launch_bound(mm_direct_kernel<T, EPI, 4>, grid, block, 0, s, b, e, a);
+  return p.bm == 16   ? launch_direct_rows<T, EPI, 1>(a, p, s, b, e)
+         : p.bm == 32 ? launch_direct_rows<T, EPI, 2>(a, p, s, b, e)
+                      : launch_direct_rows<T, EPI, 4>(a, p, s, b, e);
 }
 
 template <class T, int EPI, bool kQuant, bool kFast, int WM, int WN, int MF>
@@ -348,8 +438,7 @@ static bool launch_tile_shape(const MmArgs& a, const MatmulPlan& p, hipStream_t 
   using S = TileShape<WM, WN, MF>;
   auto kernel = mm_tile_kernel<T, EPI, kQuant, kFast, WM, WN, MF>;
   allow_large_lds(reinterpret_cast<const void*>(kernel), S::kLds);
-  const uint32_t grid = static_cast<uint32_t>((p.mtiles * p.ntiles + 7) / 8 * 8);
-  return launch_bound(kernel, dim3(grid), dim3(S::kThreads), S::kLds, s, b, e, a);
+  return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles)), dim3(S::kThreads), S::kLds, s, b, e, a);
 }
 
 template <class T, int EPI, bool kQuant = false>
@@ -367,20 +456,20 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
   if (p.R == 0) return FFNWB_OK;
   const bool quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
   MmArgs a{};
-  a.rows = p.R, a.K = p.K, a.N = p.N, a.F = p.F;
+  a.rows = static_cast<int32_t>(p.R), a.K = p.K, a.N = p.N, a.F = p.F;
   a.xs = p.xs, a.xss = p.xss, a.ys = p.ys, a.yss = p.yss;
   a.kb = static_cast<int32_t>(p.kb), a.nb = static_cast<int32_t>(p.nb), a.ntiles = static_cast<int32_t>(p.ntiles);
-  a.mtiles = static_cast<int32_t>(p.mtiles);
+  a.ngroups = static_cast<int32_t>(d->num_groups), a.nexperts = static_cast<int32_t>(d->num_experts);
+  a.groups = d->group_list;
   a.x = static_cast<const char*>(d->x), a.x_scale = d->x_scale;
   a.w = static_cast<const char*>(d->w), a.w_scale = d->w_scale;
   a.y = static_cast<char*>(d->y), a.y_scale = d->y_scale;
   Carve c;
   c.base = static_cast<char*>(ws);
-  if (d->group_list != nullptr) {
+  if (p.table) {
     int32_t* count = c.take<int32_t>(1);
     int4* table = c.take<int4>(static_cast<size_t>(p.mtiles));
-    hipLaunchKernelGGL(mm_table_kernel, dim3(1), dim3(kTableThreads), 0, s, d->group_list, static_cast<int32_t>(d->num_groups),
-                       p.R, d->num_experts, static_cast<int32_t>(p.bm), table, count);
+    hipLaunchKernelGGL(mm_table_kernel, dim3(1), dim3(kTableThreads), 0, s, a, static_cast<int32_t>(p.bm), table, count);
     if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
     a.table = table, a.count = count;
   }
@@ -416,9 +505,9 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
   if (!ok) return FFNWB_ERR_RUNTIME;
   if (quant) {
     a.y = static_cast<char*>(d->y), a.ys = p.ys;
-    const int64_t bm = p.bm, fb = (p.F + 127) / 128, per = (bm * fb * 16 + kMqThreads - 1) / kMqThreads;
-    hipLaunchKernelGGL(mm_quant_kernel, dim3(static_cast<uint32_t>(p.mtiles * per)), dim3(kMqThreads), 0, s, a, h,
-                       static_cast<int32_t>(bm));
+    a.ntiles = static_cast<int32_t>(p.quant_parts);
+    hipLaunchKernelGGL(mm_quant_kernel, dim3(tile_grid(p.mtiles * p.quant_parts)), dim3(kMqThreads), 0, s, a, h,
+                       static_cast<int32_t>(p.bm));
     if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
   }
   return FFNWB_OK;

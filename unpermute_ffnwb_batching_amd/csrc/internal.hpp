@@ -132,6 +132,8 @@ struct MatmulPlan {
   bool tile = false;                           // through LDS, else straight to registers
   int64_t bm = 0;                              // rows of a tile
   int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles
+  int64_t quant_parts = 0;                     // workgroups that quantise a row tile
+  bool table = false;                          // row tiles listed by a launch of their own
   size_t ws_bytes = 0;
 };
 

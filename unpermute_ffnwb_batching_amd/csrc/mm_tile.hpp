@@ -62,10 +62,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
   extern __shared__ __align__(16) char lds[];
   float* xsl = reinterpret_cast<float*>(lds + 2 * S::kRows * kBlk);  // [2][kScaleRuns][kScales]
 
-  int32_t m, c;
-  if (!tile_of_block(a, m, c)) return;
-  const RowTile rt = row_tile(a, m, S::kBM);
-  if (rt.rows <= 0) return;
+  RowTile rt;
+  int32_t c;
+  if (!find_tile(a, S::kBM, rt, c)) return;
   const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), r = lane % 16, g = lane / 16;
   const int32_t wm = wave / WN, wn = wave % WN;
   const int64_t c0 = static_cast<int64_t>(c) * (kSwiglu ? 128 : 256);  // first output column

@@ -17,6 +17,7 @@ struct MmArgs {
   int32_t ntiles;              // column tiles
   int32_t ngroups, nexperts;
   bool vec;                    // four adjacent outputs are one aligned store
+  int32_t unit;                // rows of y are whole aligned units of 16 or 4 bytes, or elements (0)
   const char* x;
   const float* x_scale;
   const char* w;
@@ -345,6 +346,42 @@ constexpr int64_t kCus = 256;
 
 static int64_t out_size(int32_t dt) { return dt == FFNWB_DT_FP32 ? 4 : dt == FFNWB_DT_FP8_E4M3 ? 1 : 2; }
 
+// Waves of a direct workgroup: at least one block of K each, two where there are enough
+// workgroups to fill the chip.
+static int direct_waves(int64_t tiles, int64_t kb, int64_t bm) {
+  int waves = 4;
+  while (waves < (bm == 16 ? 16 : 8) && waves * 2 <= kb && tiles * waves < kCus * 16) waves *= 2;
+  return waves;
+}
+
+// Microseconds that a product takes with the given kernel and tile rows: rounds of workgroups
+// that fit the chip together, times what one needs for its blocks of K; the figures (us per
+// block and round) are measured.  A group's last tile is counted as 0.7 of one.
+static double expected_us(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t groups, bool swiglu, bool quant, bool fast,
+                          bool tile, int64_t bm) {
+  const int64_t kb = (K + 127) / 128, some = groups < rows ? groups : rows;
+  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.7 * some : static_cast<double>((rows + bm - 1) / bm);
+  auto rounds = [](double wgs, int64_t together) { return wgs <= together ? 1.0 : __builtin_ceil(wgs / together); };
+  if (tile) {
+    const double tiles = mt * ((F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
+    double us = fast ? (bm == 256 ? 2.3 : bm == 128 ? 1.3 : 0.93) : (bm == 128 ? 2.15 : 1.35);
+    int64_t together = kCus;
+    if (bm == 32) {  // two to a CU
+      us = fast ? (tiles > kCus ? 1.0 : 0.72) : (tiles > kCus ? 1.8 : 1.3);
+      together = 2 * kCus;
+    }
+    return 3.0 + rounds(tiles, together) * (kb * us + 2.8);
+  }
+  const int64_t nt = (F + 15) / 16;
+  const int waves = direct_waves(((rows + bm - 1) / bm + some) * nt, kb, bm);
+  // waves of a CU by the kernels' registers
+  const int fit = bm == 16 ? (swiglu ? 20 : 28) : bm == 32 ? (swiglu ? 12 : 20) : (swiglu ? 8 : 12);
+  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 2.0 : 1.3) * (bm == 64 ? 1.3 : 1.0);
+  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus : kCus) * ((kb + waves - 1) / waves * us + 0.7);
+  const double weights = mt * N * K / 9000e3;  // read again for every row tile, from L2
+  return 3.0 + (work > weights ? work : weights) + (quant ? 3.0 : 0.0);
+}
+
 int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   if (d == nullptr || d->x == nullptr || d->x_scale == nullptr || d->w == nullptr || d->w_scale == nullptr || d->y == nullptr)
     return FFNWB_ERR_PARAM_NULLPTR;
@@ -380,7 +417,6 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
       reinterpret_cast<uintptr_t>(d->y) % elt != 0)
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t groups = d->group_list != nullptr ? d->num_groups : 1;
-  const int64_t avg = (p->R + groups - 1) / groups;
   const bool fast = !quant && d->out_dtype != FFNWB_DT_FP32;
   auto shape = [&](bool tile, int64_t bm) {
     p->tile = tile, p->bm = bm;
@@ -388,12 +424,20 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     p->ntiles = tile ? (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256) : (p->F + 15) / 16;
     return p->mtiles * p->ntiles;
   };
-  // Through LDS, with the largest tile that the groups fill on average and that leaves every CU
-  // one; straight to registers where even the smallest tiles are few, and where 256 rows
-  // of x pass the 32-bit offsets of the copies.
-  int64_t bm = avg > 1024 && fast ? 256 : avg > 128 ? 128 : avg > 64 ? 64 : 32;
-  while (bm > 32 && shape(true, bm) < kCus) bm /= 2;
-  if (p->xs > (1 << 22) || shape(true, bm) < kCus / 2) shape(false, avg <= 16 ? 16 : avg <= 32 ? 32 : 64);
+  // The kernel and the rows of its tiles: the least of the times expected.  Over 400 random sizes
+  // (1 to 65536 rows, K and N to 8192, 0 to 256 groups) the choice is 3% slower than the best of
+  // the shapes on average; a fixed rule (the largest tile that the groups fill and that gives
+  // every CU one) was 15%.  256 rows of x, and the gate rows of w, have to be inside the 32-bit
+  // offsets of the tile kernel.
+  const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
+  double best = 0;
+  int64_t best_bm = 0;
+  for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {  // negative: direct
+    if (bm > 0 && (!near || (bm == 256 && !fast))) continue;
+    const double t = expected_us(p->R, p->N, p->K, p->F, d->num_groups, swiglu, quant, fast, bm > 0, bm > 0 ? bm : -bm);
+    if (best_bm == 0 || t < best) best = t, best_bm = bm;
+  }
+  shape(best_bm > 0, best_bm > 0 ? best_bm : -best_bm);
   // one dimension of the grid: fewer than 2^32 threads of at most 1024 a workgroup
   if (p->mtiles * p->ntiles > (int64_t{1} << 22) - 8) return FFNWB_ERR_PARAM_INVALID;
   p->quant_parts = (p->bm * fb + kMqThreads / 16 - 1) / (kMqThreads / 16);
@@ -416,10 +460,7 @@ static uint32_t tile_grid(int64_t tiles) { return static_cast<uint32_t>((tiles +
 
 template <class T, int EPI, int MT>
 static bool launch_direct_rows(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
-  // Waves of a workgroup: at least one block of K each, two where there are enough workgroups
-  // to fill the chip.
-  int waves = 4;
-  while (waves < (MT == 1 ? 16 : 8) && waves * 2 <= p.kb && p.mtiles * p.ntiles * waves < kCus * 16) waves *= 2;
+  const int waves = direct_waves(p.mtiles * p.ntiles, p.kb, p.bm);
   const size_t lds = static_cast<size_t>(waves) * (EPI == FFNWB_EPI_SWIGLU ? 2 : 1) * MT * kWave * 16;
   auto kernel = mm_direct_kernel<T, EPI, MT>;
   allow_large_lds(reinterpret_cast<const void*>(kernel), lds);
@@ -475,6 +516,8 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
   }
   const int64_t quad = 4 * out_size(d->out_dtype);
   a.vec = ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(p.ys)) & (quad - 1)) == 0;
+  const uint64_t all = reinterpret_cast<uintptr_t>(a.y) | static_cast<uint64_t>(p.ys) | static_cast<uint64_t>(p.F * (quad / 4));
+  a.unit = (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 0;
   void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
   if (p.tile) {
     bool ok;

@@ -24,20 +24,31 @@ __device__ __forceinline__ f32x4 mul_e4m3(const u32x4 (&a)[2], const u32x4 (&b)[
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 }
 
-// 16 bytes per lane from `src` to LDS at `dst` + 16 * lane; `dst` is the same in all lanes.
-__device__ __forceinline__ void copy16_to_lds(const char* src, char* dst) {
-  __builtin_amdgcn_global_load_lds(reinterpret_cast<const __attribute__((address_space(1))) void*>(reinterpret_cast<uintptr_t>(src)),
-                                   reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(dst)),
-                                   16, 0, 0);
+// 16 bytes per lane, from a uniform base + lane offset + uniform offset, to LDS at `dst` + 16 *
+// lane; `dst` is the same in all lanes.  Nothing is read from `bytes` past the base on.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer make_buffer(const char* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, static_cast<uint32_t>(min(bytes, int64_t{0xffffffff})),
+                                           0x00027000);
+}
+__device__ __forceinline__ void copy16_to_lds(Buffer base, uint32_t lane_offset, uint32_t offset, char* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(dst)),
+                                           16, lane_offset, offset, 0, 0);
 }
 
-// All of this wave's copies have landed, then all waves' have.
-__device__ __forceinline__ void copies_done() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-}
+// A barrier for the waves' LDS reads and writes, which leaves copies to LDS on their way:
+// __syncthreads would wait for them too.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-__device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
+// This wave's copies have landed, all or (`some`, uniform) all but the last kLeft; then all
+// waves' have.  The branch is inside the assembly: one in the compiler's sight would let it move
+// the arithmetic of a step behind it, with every sum of the step held in registers until then.
+template <int kLeft>
+__device__ __forceinline__ void copies_done(bool some) {
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lsome%=\n\ts_waitcnt vmcnt(0)\n.Lsome%=:\n\ts_waitcnt vmcnt(%1)"
+               ::"s"(uniform(static_cast<int32_t>(some))), "n"(kLeft) : "memory", "scc");
+  lds_barrier();
+}
 
 template <int WM, int WN, int MF>
 struct TileShape {
@@ -45,13 +56,29 @@ struct TileShape {
   static constexpr int kNF = 16 / WN;              // column fragments of a wave: 256 columns in all
   static constexpr int kBM = WM * MF * 16;
   static constexpr int kRows = kBM + 256;          // rows of a buffer, x then w
-  static constexpr int kCopies = kRows / 8 / (WM * WN);
+  static constexpr int kXCopies = kBM / 8 / (WM * WN), kWCopies = 256 / 8 / (WM * WN);  // of 8 rows
   static constexpr int kScaleRuns = 8;             // blocks of the scales held at once
   static constexpr int kScales = kBM + 16;         // scales of a block: rows of x, then column fragments
   static constexpr int kScaleLoads = (kScales * kScaleRuns + kThreads - 1) / kThreads;
   static constexpr int kLds = 2 * kRows * kBlk + 2 * kScales * kScaleRuns * 4;
-  static_assert(kRows % (8 * WM * WN) == 0, "every wave copies the same number of rows");
+  static_assert(kBM % (8 * WM * WN) == 0 && 256 % (8 * WM * WN) == 0, "every wave copies the same number of rows");
 };
+
+// Rows of a tile from LDS to memory, U bytes per lane.
+template <int U, int kPitch, int kThreads>
+__device__ __forceinline__ void copy_out(const char* lds, char* y, int64_t stride, int32_t rows, int32_t bytes) {
+  constexpr int kUnits = kPitch / U;
+  for (int32_t i = threadIdx.x; i < rows * kUnits; i += kThreads) {
+    const int32_t row = i / kUnits, at = i % kUnits * U;
+    if (at >= bytes) continue;
+    const char* from = lds + row * kPitch + ((at / 16 ^ (row & 7)) * 16 + at % 16);
+    char* to = y + row * stride + at;
+    if constexpr (U == 16) *reinterpret_cast<u32x4*>(to) = *reinterpret_cast<const u32x4*>(from);
+    else if constexpr (U == 4) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+    else if constexpr (U == 2) *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<const uint16_t*>(from);
+    else *to = *from;
+  }
+}
 
 // kFast: e4m3 matrix instructions; else the operands are widened to BF16 (see fp8_block.hpp).
 template <class T, int EPI, bool kQuant, bool kFast, int WM, int WN, int MF>
@@ -78,32 +105,41 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
       return min(c0 + q, a.N - 1);
     }
   };
-  // 32-bit offsets from the tile's first rows (256 rows of x are below 2^31 bytes)
-  const char* xbase = a.x + rt.row0 * a.xs;
-  const char* wbase = a.w + static_cast<int64_t>(rt.expert) * a.N * a.K;
-  uint32_t src[S::kCopies];
+  // Copy j of a wave takes 8 rows, one chunk per lane: 32-bit offsets from the tile's first rows
+  // (256 rows of x, and of w as far as the up columns, are below 2^32 bytes in this kernel).
+  const int64_t w0 = weight_row(0);
+  const Buffer xbuf = make_buffer(a.x + rt.row0 * a.xs, (rt.rows - 1) * a.xs + a.K);
+  const Buffer wbuf = make_buffer(a.w + (static_cast<int64_t>(rt.expert) * a.N + w0) * a.K, (a.N - w0) * a.K);
+  const uint32_t chunk = ((lane % 8) ^ (lane / 8)) * 16;
+  uint32_t xsrc[S::kXCopies], wsrc[S::kWCopies];
 #pragma unroll
-  for (int j = 0; j < S::kCopies; ++j) {
-    const int32_t row = (j * WM * WN + wave) * 8 + lane / 8;
-    src[j] = ((lane % 8) ^ (lane / 8)) * 16 +
-             static_cast<uint32_t>(row < S::kBM ? min(row, rt.rows - 1) * a.xs : weight_row(row - S::kBM) * a.K);
-  }
-  const int32_t tail = static_cast<int32_t>(a.K % kBlk);  // columns of a short last block
-  auto fetch = [&](int32_t b) {
-    char* to = lds + (b & 1) * S::kRows * kBlk;
-    const int32_t k0 = b * kBlk;
-    if (tail != 0 && b == a.kb - 1) {
-      const bool cut = ((lane % 8) ^ (lane / 8)) * 16 >= tail;
+  for (int j = 0; j < S::kXCopies; ++j)
+    xsrc[j] = chunk + static_cast<uint32_t>(min((j * WM * WN + wave) * 8 + lane / 8, rt.rows - 1) * a.xs);
 #pragma unroll
-      for (int j = 0; j < S::kCopies; ++j) {
-        const char* p = ((j * WM * WN + wave) * 8 < S::kBM ? xbase : wbase) + k0 + src[j];
-        copy16_to_lds(cut ? reinterpret_cast<const char*>(&kZeroChunk) : p, to + (j * WM * WN + wave) * 1024);
-      }
-    } else {
+  for (int j = 0; j < S::kWCopies; ++j)
+    wsrc[j] = chunk + static_cast<uint32_t>((weight_row((j * WM * WN + wave) * 8 + lane / 8) - w0) * a.K);
+  // LDS: x of even and odd blocks, w of even and odd blocks, scales
+  auto fetch_x = [&](int32_t b) {
+    char* to = lds + (b & 1) * S::kBM * kBlk;
 #pragma unroll
-      for (int j = 0; j < S::kCopies; ++j)
-        copy16_to_lds(((j * WM * WN + wave) * 8 < S::kBM ? xbase : wbase) + k0 + src[j], to + (j * WM * WN + wave) * 1024);
+    for (int j = 0; j < S::kXCopies; ++j) copy16_to_lds(xbuf, xsrc[j], b * kBlk, to + (j * WM * WN + wave) * 1024);
+  };
+  auto fetch_w = [&](int32_t b) {
+    char* to = lds + 2 * S::kBM * kBlk + (b & 1) * 256 * kBlk;
+#pragma unroll
+    for (int j = 0; j < S::kWCopies; ++j) copy16_to_lds(wbuf, wsrc[j], b * kBlk, to + (j * WM * WN + wave) * 1024);
+  };
+  // A short last block: the chunks past K (of the next row, or not there) become zeros.
+  const int32_t full = static_cast<int32_t>(a.K % kBlk) / 16;
+  auto clear_tail = [&] {
+    char* xb = lds + ((a.kb - 1) & 1) * S::kBM * kBlk;
+    char* wb = lds + 2 * S::kBM * kBlk + ((a.kb - 1) & 1) * 256 * kBlk;
+    for (int32_t i = threadIdx.x; i < S::kRows * (8 - full); i += S::kThreads) {
+      const int32_t row = i / (8 - full), ch = full + i % (8 - full);
+      char* at = row < S::kBM ? xb + row * kBlk : wb + (row - S::kBM) * kBlk;
+      *reinterpret_cast<u32x4*>(at + (ch ^ (row & 7)) * 16) = u32x4{0, 0, 0, 0};
     }
+    __syncthreads();
   };
   // The scales of 8 blocks at a time, 8 lanes per row of x or column fragment of w; they go
   // through registers to LDS 6 blocks later, held [block][row].  A fragment's 16 columns lie in
@@ -130,145 +166,181 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
     }
   };
 
-  fetch(0);
+  fetch_x(0);
+  fetch_w(0);
   scales_load(0);
   scales_store(0);
-  copies_done();
+  if (a.kb > 1) fetch_w(1);
+  copies_done<S::kWCopies>(a.kb > 1);
 
+  // Step b: x of block b + 1 is fetched from its start; the waves take their fragments of w into
+  // registers, which frees that buffer for block b + 2.  So w has two steps to arrive and x one.
   f32x4 tot[MF][NF] = {};
   for (int32_t b = 0; b < a.kb; ++b) {
     const int32_t turn = b % S::kScaleRuns, next = b - turn + S::kScaleRuns;
     if (turn == S::kScaleRuns - 2 && next < a.kb) scales_store(next);
     if (turn == 0 && next < a.kb) scales_load(next);
-    if (b + 1 < a.kb) fetch(b + 1);
-    // one stretch of code from here to the end of the step, in the order written
-    const char* buf = lds + (b & 1) * S::kRows * kBlk;
+    if (b + 1 < a.kb) fetch_x(b + 1);
+    else if (full != 0) clear_tail();
+    const char* xb = lds + (b & 1) * S::kBM * kBlk;
+    const char* wb = lds + 2 * S::kBM * kBlk + (b & 1) * 256 * kBlk;
     const float* scb = xsl + ((b / S::kScaleRuns & 1) * S::kScaleRuns + turn) * S::kScales;
     constexpr int NS = kSwiglu ? NF : 1;  // without SwiGLU a wave's columns lie in one block of 128
-    float ws[NS];
-#pragma unroll
-    for (int f = 0; f < NS; ++f) ws[f] = scb[S::kBM + wn * NF + f];
+    constexpr int kParts = kFast ? 2 : 4;  // registers of a fragment, in fours
     const int32_t ch0 = (g ^ (r & 7)) * 16, ch1 = ((4 + g) ^ (r & 7)) * 16;
-    u32x4 wf[NF][kFast ? 2 : 4];
+    u32x4 wv[NF][2], xv[2][2];
+    float ws[NS], xs[MF];
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      const char* row = buf + (S::kBM + (wn * NF + f) * 16 + r) * kBlk;
-      const u32x4 v0 = *reinterpret_cast<const u32x4*>(row + ch0), v1 = *reinterpret_cast<const u32x4*>(row + ch1);
-      if constexpr (kFast) {
-        wf[f][0] = v0, wf[f][1] = v1;
-      } else {
-        wf[f][0] = widen8(v0[0], v0[1]), wf[f][1] = widen8(v0[2], v0[3]);
-        wf[f][2] = widen8(v1[0], v1[1]), wf[f][3] = widen8(v1[2], v1[3]);
-      }
+      const char* row = wb + ((wn * NF + f) * 16 + r) * kBlk;
+      wv[f][0] = *reinterpret_cast<const u32x4*>(row + ch0);
+      wv[f][1] = *reinterpret_cast<const u32x4*>(row + ch1);
     }
-    // fragment i + 1 of x is read while i is multiplied; the other wave of the SIMD multiplies
-    // while this one scales its sums
-    u32x4 xv[2][2];
-    auto read = [&](int i) {
-      const char* row = buf + ((wm * MF + i) * 16 + r) * kBlk;
+    auto read_x = [&](int i) {
+      const char* row = xb + ((wm * MF + i) * 16 + r) * kBlk;
       xv[i & 1][0] = *reinterpret_cast<const u32x4*>(row + ch0);
       xv[i & 1][1] = *reinterpret_cast<const u32x4*>(row + ch1);
     };
-    read(0);
+    read_x(0);
+#pragma unroll
+    for (int f = 0; f < NS; ++f) ws[f] = scb[S::kBM + wn * NF + f];
+#pragma unroll
+    for (int i = 0; i < MF; ++i) xs[i] = scb[(wm * MF + i) * 16 + r];
+    if constexpr (MF > 1) read_x(1);
+    if (b + 2 < a.kb) {
+      lds_barrier();  // every wave has its fragments of w
+      fetch_w(b + 2);
+    }
+    // One stretch of code from here to the end of the step: a fragment of x is multiplied while the
+    // sums of the one before are scaled and the one after next is read.
+    u32x4 wf[NF][kParts], xf[2][kParts];
+    f32x4 p[2][NF];
+    auto widen = [](const u32x4 (&v)[2], u32x4 (&to)[kParts]) {
+      if constexpr (kFast) {
+        to[0] = v[0], to[1] = v[1];
+      } else {
+        to[0] = widen8(v[0][0], v[0][1]), to[1] = widen8(v[0][2], v[0][3]);
+        to[2] = widen8(v[1][0], v[1][1]), to[3] = widen8(v[1][2], v[1][3]);
+      }
+    };
+    auto scale = [&](int i) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const float s = xs[i] * ws[kSwiglu ? f : 0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tot[i][f][j] = __builtin_fmaf(s, p[i & 1][f][j], tot[i][f][j]);
+      }
+    };
+#pragma unroll
+    for (int f = 0; f < NF; ++f) widen(wv[f], wf[f]);
+    widen(xv[0], xf[0]);
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
-      if (i + 1 < MF) read(i + 1);
-      const float xs = scb[(wm * MF + i) * 16 + r];
-      f32x4 p[NF];
-      const u32x4 v0 = xv[i & 1][0], v1 = xv[i & 1][1];
       if constexpr (kFast) {
-        const u32x4 xf[2] = {v0, v1};
 #pragma unroll
-        for (int f = 0; f < NF; ++f) p[f] = mul_e4m3(wf[f], xf);
+        for (int f = 0; f < NF; ++f) p[i & 1][f] = mul_e4m3(wf[f], xf[i & 1]);
       } else {
-        const u32x4 xf[4] = {widen8(v0[0], v0[1]), widen8(v0[2], v0[3]), widen8(v1[0], v1[1]), widen8(v1[2], v1[3])};
 #pragma unroll
-        for (int f = 0; f < NF; ++f) p[f] = f32x4{0, 0, 0, 0};
+        for (int f = 0; f < NF; ++f) p[i & 1][f] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-          for (int f = 0; f < NF; ++f) p[f] = Mat<TBF16>::mul(wf[f][s], xf[s], p[f]);
+          for (int f = 0; f < NF; ++f) p[i & 1][f] = Mat<TBF16>::mul(wf[f][s], xf[i & 1][s], p[i & 1][f]);
       }
+      if (i + 1 < MF) widen(xv[(i + 1) & 1], xf[(i + 1) & 1]);
+      if (i + 2 < MF) read_x(i + 2);
+      if (i > 0) scale(i - 1);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const float s = xs * ws[kSwiglu ? f : 0];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tot[i][f][j] = __builtin_fmaf(s, p[f][j], tot[i][f][j]);
+      for (int q = 0; q < (kFast ? NF : 4 * NF); ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // a matrix instruction,
+        __builtin_amdgcn_sched_group_barrier(0x002, kFast ? 5 : 2, 0); // then vector ones
+        if (q < 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // and a read
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    copies_done();
+    scale(MF - 1);
+    copies_done<S::kWCopies>(b + 2 < a.kb);
   }
 
-  if constexpr (!kSwiglu) {
-#pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const int32_t row = (wm * MF + i) * 16 + r;
-      if (row >= rt.rows) continue;
-      char* y = a.y + (rt.row0 + row) * a.ys;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) store4<T>(y, c0 + (wn * NF + f) * 16 + g * 4, a.N, tot[i][f], a.vec);
-    }
-  } else {
-    constexpr int HF = NF / 2;  // output fragments of a wave
+  // Results go through LDS, so that memory sees whole lines: a matrix result is 16 rows by 4
+  // adjacent columns per lane.  Row r of the tile is kPitch bytes, its 16-byte chunks at
+  // position c ^ (r % 8) as above.
+  constexpr int kElt = kQuant ? 1 : T::kBytes;
+  constexpr int kCols = kSwiglu ? 128 : 256, kPitch = kCols * kElt;
+  constexpr int OF = kSwiglu ? NF / 2 : NF;  // result fragments of a wave
+  const int64_t limit = kSwiglu ? a.F : a.N;
+  if constexpr (kSwiglu) {
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-      for (int f = 0; f < HF; ++f)
+      for (int f = 0; f < OF; ++f)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tot[i][f][j] = swiglu(tot[i][f][j], tot[i][HF + f][j]);
-    const int64_t f0 = c0 + wn * HF * 16 + g * 4;
-    if constexpr (!kQuant) {
+        for (int j = 0; j < 4; ++j) tot[i][f][j] = swiglu(tot[i][f][j], tot[i][OF + f][j]);
+  }
+  float scale[kQuant ? MF : 1];
+  if constexpr (kQuant) {
+    // the row's largest |h| over the tile's 128 columns, one block: lanes, then waves
+    uint32_t* amax = reinterpret_cast<uint32_t*>(xsl);  // [kBM][WN], in the scales' memory
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      uint32_t big = 0;
+#pragma unroll
+      for (int f = 0; f < OF; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c0 + (wn * OF + f) * 16 < limit) big = max(big, __float_as_uint(tot[i][f][j]) & 0x7fffffffu);
+      big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 16)));
+      big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 32)));
+      if (g == 0) amax[((wm * MF + i) * 16 + r) * WN + wn] = big;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+      const int32_t row = (wm * MF + i) * 16 + r;
+      uint32_t big = 0;
+#pragma unroll
+      for (int w = 0; w < WN; ++w) big = max(big, amax[row * WN + w]);
+      scale[i] = block_scale(big);
+      if (wn == 0 && g == 0 && row < rt.rows) a.y_scale[(rt.row0 + row) * a.yss + c] = scale[i];
+    }
+  }
+  // FP32 tiles of 128 rows are wider than the buffers: the waves of one half of the rows after
+  // those of the other.
+  constexpr int kParts = S::kBM * kPitch > 2 * S::kRows * kBlk ? 2 : 1;
+  constexpr int kPartRows = S::kBM / kParts;
+  static_assert(kParts == 1 || WM == 2, "a part is the rows of some of the waves");
+#pragma unroll
+  for (int part = 0; part < kParts; ++part) {
+    if (part > 0) __syncthreads();
+    if (kParts == 1 || wm == part) {
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
-        const int32_t row = (wm * MF + i) * 16 + r;
-        if (row >= rt.rows) continue;
-        char* y = a.y + (rt.row0 + row) * a.ys;
+        const int32_t row = ((kParts == 1 ? wm * MF : 0) + i) * 16 + r;
 #pragma unroll
-        for (int f = 0; f < HF; ++f) store4<T>(y, f0 + f * 16, a.F, tot[i][f], a.vec);
-      }
-    } else {
-      // the row's largest |h| over the tile's 128 columns, one block: lanes, then waves
-      uint32_t* amax = reinterpret_cast<uint32_t*>(lds);  // [kBM][WN]
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        uint32_t big = 0;
-#pragma unroll
-        for (int f = 0; f < HF; ++f)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (f0 + f * 16 < a.F) big = max(big, __float_as_uint(tot[i][f][j]) & 0x7fffffffu);
-        big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 16)));
-        big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 32)));
-        if (g == 0) amax[((wm * MF + i) * 16 + r) * WN + wn] = big;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const int32_t row = (wm * MF + i) * 16 + r;
-        uint32_t big = 0;
-#pragma unroll
-        for (int w = 0; w < WN; ++w) big = max(big, amax[row * WN + w]);
-        const float s = block_scale(big);
-        if (row >= rt.rows) continue;
-        char* y = a.y + (rt.row0 + row) * a.ys;
-#pragma unroll
-        for (int f = 0; f < HF; ++f) {
-          float q[4] = {tot[i][f][0], tot[i][f][1], tot[i][f][2], tot[i][f][3]};
-          block_quotients(q, s);
-          const uint32_t v = pack_e4m3(q[0], q[1], q[2], q[3]);
-          if (f0 + f * 16 >= a.F) continue;  // F is a multiple of 16
-          char* to = y + f0 + f * 16;
-          if (a.vec) {
-            *reinterpret_cast<uint32_t*>(to) = v;
+        for (int f = 0; f < OF; ++f) {
+          const int32_t at = ((wn * OF + f) * 16 + g * 4) * kElt;  // byte of the row
+          char* to = lds + row * kPitch + ((at / 16 ^ (row & 7)) * 16 + at % 16);
+          if constexpr (kQuant) {
+            float q[4] = {tot[i][f][0], tot[i][f][1], tot[i][f][2], tot[i][f][3]};
+            block_quotients(q, scale[i]);
+            *reinterpret_cast<uint32_t*>(to) = pack_e4m3(q[0], q[1], q[2], q[3]);
+          } else if constexpr (kElt == 2) {
+            const float v[8] = {tot[i][f][0], tot[i][f][1], tot[i][f][2], tot[i][f][3], 0, 0, 0, 0};
+            const u32x4 h = Chunk<T>::narrow(v);
+            *reinterpret_cast<u32x2*>(to) = u32x2{h[0], h[1]};
           } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) to[j] = static_cast<char>((v >> (8 * j)) & 0xffu);
+            *reinterpret_cast<f32x4*>(to) = tot[i][f];
           }
         }
-        if (wn == 0 && g == 0) a.y_scale[(rt.row0 + row) * a.yss + c] = s;
       }
     }
+    __syncthreads();
+    const int32_t rows = min(rt.rows - part * kPartRows, kPartRows);
+    const int32_t bytes = static_cast<int32_t>(min(limit - c0, int64_t{kCols})) * kElt;  // of a row
+    char* y = a.y + (rt.row0 + part * kPartRows) * a.ys + c0 * kElt;
+    if (a.unit == 16) copy_out<16, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
+    else if (a.unit == 4) copy_out<4, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
+    else copy_out<kElt, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
   }
 }
 

@@ -49,6 +49,9 @@ struct LayerArgs {
   float* weight;              // [T * K] the token's weight for the expert
   char* hhi;                  // [T * K, F] BF16
   char* hlo;
+  int32_t parts;              // workgroups of a column tile of launch 2
+  int32_t* arrived;           // [H / 16] of them that are done (more than one part)
+  float* partial;             // [H / 16, parts, T, 16]
 };
 
 // ------------------------------------------------------------------ operands
@@ -91,12 +94,12 @@ __device__ __forceinline__ int32_t active_id(const LayerArgs& a, int32_t i) {
 }
 
 // All ids into LDS and one bit for each expert that occurs.
-__device__ __forceinline__ void load_ids(const LayerArgs& a, int32_t* ids, uint32_t* bits) {
+__device__ __forceinline__ void load_ids(const LayerArgs& a, int16_t* ids, uint32_t* bits) {
   for (int32_t i = threadIdx.x; i < kMaxExperts / 32; i += blockDim.x) bits[i] = 0;
   __syncthreads();
   for (int32_t i = threadIdx.x; i < a.T * a.K; i += blockDim.x) {
     const int32_t id = active_id(a, i);
-    ids[i] = id;
+    ids[i] = static_cast<int16_t>(id);  // below 8192
     if (id >= 0) atomicOr(&bits[id / 32], 1u << (id % 32));
   }
   __syncthreads();
@@ -126,71 +129,85 @@ __device__ __forceinline__ float slot_scale(const LayerArgs& a, int32_t t, int32
 }
 
 // Workgroup 0 of launch 1: the experts, their tokens (in groups of up to 16, one matrix operand)
-// and weights, for launch 2.  A token that names an expert twice has one entry, at its first
-// slot, with the sum of the weights.
-__device__ void build_table(const LayerArgs& a, const int32_t* ids, const uint32_t* bits, int32_t* cursor, int32_t* below) {
-  const int32_t n = a.T * a.K, lane = threadIdx.x % kWave;
+// and weights, for launch 2.  An expert's tokens are the bits of a mask, so that every slot finds
+// its entry's place by counting bits; a token that names an expert twice has one entry, at its
+// first slot, with the sum of the weights.
+struct TableLds {
+  int16_t ids[kLyMaxIds];
+  uint16_t first[kLyMaxIds];      // [rank] first entry
+  uint32_t mask[kLyMaxIds][2];    // [rank] tokens
+};
+
+__device__ void build_table(const LayerArgs& a, TableLds& s, const uint32_t* bits, int32_t* below) {
+  const int32_t n = a.T * a.K, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  __shared__ int32_t sums[2][kUpWaves];
+  static_assert(kMaxExperts / 32 == kUpWaves * kWave, "one word of the experts' bits to a thread");
+  if (a.parts > 1)
+    for (int32_t i = threadIdx.x; i < a.H / 16; i += blockDim.x) a.arrived[i] = 0;
   if (threadIdx.x < kWave) {
     int32_t total;
     int32_t at = bits_below(bits, lane, total);
     for (int j = 0; j < 4; ++j) {
-      const int32_t w = 4 * lane + j;
-      below[w] = at;
-      for (uint32_t m = bits[w]; m != 0; m &= m - 1) cursor[at++] = (w * 32 + __builtin_ctz(m)) << 8;  // id, no token yet
+      below[4 * lane + j] = at;
+      at += __popc(bits[4 * lane + j]);
     }
     if (lane == 0) below[kMaxExperts / 32] = total;
   }
   __syncthreads();
   const int32_t ranks = below[kMaxExperts / 32];
-  auto rank = [&](int32_t e) { return below[e / 32] + __popc(bits[e / 32] & ((1u << (e % 32)) - 1)); };
-  auto head = [&](int32_t i) {  // whether slot i is its token's first with its expert
-    const int32_t t0 = i / a.K * a.K;
-    for (int32_t j = t0; j < i; ++j)
-      if (ids[j] == ids[i]) return false;
-    return true;
-  };
-  for (int32_t i = threadIdx.x; i < n; i += blockDim.x)
-    if (ids[i] >= 0 && head(i)) atomicAdd(&cursor[rank(ids[i])], 1);  // at most 64
+  for (int32_t i = threadIdx.x; i < ranks; i += blockDim.x) s.mask[i][0] = s.mask[i][1] = 0;
   __syncthreads();
-  // exclusive sums of entries and of groups, a run of ranks per lane of wave 0
-  if (threadIdx.x < kWave) {
-    const int32_t per = (ranks + kWave - 1) / kWave, r0 = min(lane * per, ranks), r1 = min(r0 + per, ranks);
-    int32_t mine = 0, mine_g = 0;
-    for (int32_t r = r0; r < r1; ++r) mine += cursor[r] & 255, mine_g += ((cursor[r] & 255) + 15) / 16;
-    int32_t incl = mine, incl_g = mine_g;
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int32_t v = __shfl_up(incl, d), vg = __shfl_up(incl_g, d);
-      if (lane >= d) incl += v, incl_g += vg;
-    }
-    int32_t at = incl - mine, group = incl_g - mine_g;
-    for (int32_t r = r0; r < r1; ++r) {
-      const int32_t c = cursor[r] & 255, e = cursor[r] >> 8;
-      for (int32_t i = 0; i < c; i += 16) {
-        a.expert[group] = e;
-        a.first[group++] = at + i;
-      }
-      cursor[r] = at;
-      at += c;
-    }
-    if (lane == kWave - 1) {
-      *a.groups = incl_g;
-      a.first[incl_g] = incl;
-    }
+  auto rank = [&](int32_t e) { return below[e / 32] + __popc(bits[e / 32] & ((1u << (e % 32)) - 1)); };
+  for (int32_t i = threadIdx.x; i < n; i += blockDim.x) {
+    const int32_t t = i / a.K;
+    if (s.ids[i] >= 0) atomicOr(&s.mask[rank(s.ids[i])][t / 32], 1u << (t % 32));
   }
   __syncthreads();
-  // tokens in order; the heads of one token have distinct experts
-  for (int32_t t = 0; t < a.T; ++t) {
-    for (int32_t k = threadIdx.x; k < a.K; k += blockDim.x) {
-      const int32_t i = t * a.K + k, e = ids[i];
-      if (e < 0 || !head(i)) continue;
-      float w = 0.0f;
-      for (int32_t j = k; j < a.K; ++j)
-        if (ids[t * a.K + j] == e) w += slot_scale(a, t, j);
-      const int32_t at = cursor[rank(e)]++;
-      a.slot[at] = i;
-      a.weight[at] = w;
+  // exclusive sums of entries and of groups over the experts, a word of experts to a thread
+  const uint32_t word = bits[threadIdx.x];
+  const int32_t r0 = below[threadIdx.x], r1 = r0 + __popc(word);
+  auto tokens = [&](int32_t r) { return __popc(s.mask[r][0]) + __popc(s.mask[r][1]); };
+  int32_t mine = 0, mine_g = 0;
+  for (int32_t r = r0; r < r1; ++r) mine += tokens(r), mine_g += (tokens(r) + 15) / 16;
+  int32_t incl = mine, incl_g = mine_g;
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int32_t v = __shfl_up(incl, d), vg = __shfl_up(incl_g, d);
+    if (lane >= d) incl += v, incl_g += vg;
+  }
+  if (lane == kWave - 1) sums[0][wave] = incl, sums[1][wave] = incl_g;
+  __syncthreads();
+  int32_t at = incl - mine, group = incl_g - mine_g;
+  for (int32_t w = 0; w < wave; ++w) at += sums[0][w], group += sums[1][w];
+  uint32_t m = word;
+  for (int32_t r = r0; r < r1; ++r, m &= m - 1) {
+    s.first[r] = static_cast<uint16_t>(at);
+    const int32_t c = tokens(r);
+    for (int32_t i = 0; i < c; i += 16) {
+      a.expert[group] = static_cast<int32_t>(threadIdx.x) * 32 + __builtin_ctz(m);
+      a.first[group++] = at + i;
     }
-    __syncthreads();
+    at += c;
+  }
+  if (threadIdx.x == blockDim.x - 1) {
+    *a.groups = group;
+    a.first[group] = at;
+  }
+  __syncthreads();
+  for (int32_t i = threadIdx.x; i < n; i += blockDim.x) {
+    const int32_t e = s.ids[i], t = i / a.K, t0 = t * a.K;
+    if (e < 0) continue;
+    bool head = true;
+    for (int32_t j = t0; j < i; ++j) head = head && s.ids[j] != e;
+    if (!head) continue;
+    float w = 0.0f;
+    for (int32_t j = i; j < t0 + a.K; ++j)
+      if (s.ids[j] == e) w += slot_scale(a, t, j - t0);
+    const int32_t r = rank(e);
+    const uint32_t lo = t < 32 ? s.mask[r][0] & ((1u << t) - 1) : s.mask[r][0];
+    const uint32_t hi = t < 32 ? 0u : s.mask[r][1] & ((1u << (t - 32)) - 1);
+    const int32_t entry = s.first[r] + __popc(lo) + __popc(hi);
+    a.slot[entry] = i;
+    a.weight[entry] = w;
   }
 }
 
@@ -299,20 +316,46 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
 
 template <class T, bool kFp8>
 __global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) {
-  __shared__ __align__(16) int32_t scratch[kUpWaves * 8 * kWave * 4];  // ids, then the waves' totals
+  __shared__ __align__(16) union {
+    TableLds table;
+    float totals[kUpWaves * 8 * kWave * 4];  // of the waves, up to 64 tokens
+  } scratch;
   __shared__ uint32_t bits[kMaxExperts / 32];
   __shared__ int32_t below[kMaxExperts / 32 + 1];
-  __shared__ int32_t list[kLyMaxTokens];
+  __shared__ int32_t lists[kUpWaves][kLyMaxTokens];
   __shared__ int32_t chosen, count;
-  static_assert(kUpWaves * 8 * kWave * 4 >= 2 * kLyMaxIds, "ids and cursors share the totals' memory");
-  int32_t* ids = scratch;
-  load_ids(a, ids, bits);
-  if (blockIdx.x == 0) {
-    build_table(a, ids, bits, scratch + kLyMaxIds, below);
+  int16_t* ids = scratch.table.ids;
+  float* red = scratch.totals;
+  const int32_t rank = (static_cast<int32_t>(blockIdx.x) - 1) / a.ctiles, c = static_cast<int32_t>(blockIdx.x) - 1 - rank * a.ctiles;
+  const int32_t lane = threadIdx.x % kWave;
+  if (blockIdx.x != 0 && a.T * a.K <= kWave) {
+    // Up to 64 slots are one to a lane, and every wave finds the workgroup's expert (the rank-th
+    // in the order of the slots) by itself: two barriers and a pass through LDS less.
+    int32_t* list = lists[threadIdx.x / kWave];
+    const int32_t id = lane < a.T * a.K ? active_id(a, lane) : -1;
+    uint64_t rest = wave_ballot(id >= 0);
+    for (int32_t k = 0; k < rank && rest != 0; ++k)
+      rest &= ~wave_ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(rest)));
+    if (rest == 0) return;
+    const int32_t e = __builtin_amdgcn_readlane(id, __builtin_ctzll(rest));
+    const uint64_t has = wave_ballot(id == e);
+    const uint64_t before = (uint64_t{1} << lane) - 1, token = before & ~((uint64_t{1} << (lane / a.K * a.K)) - 1);
+    const bool head = id == e && (has & token) == 0;  // the token's first slot with e
+    const uint64_t heads = wave_ballot(head);
+    if (head) list[count_below(heads)] = lane;
+    wave_lds_sync();
+    const int32_t n = __popcll(heads);
+    if (n <= 16) up_tile<T, kFp8, 1>(a, e, c * 16, n, list, red);
+    else if (n <= 32) up_tile<T, kFp8, 2>(a, e, c * 16, n, list, red);
+    else up_tile<T, kFp8, 4>(a, e, c * 16, n, list, red);
     return;
   }
-  const int32_t rank = (blockIdx.x - 1) / a.ctiles, c = blockIdx.x - 1 - rank * a.ctiles;
-  const int32_t lane = threadIdx.x % kWave;
+  int32_t* list = lists[0];
+  load_ids(a, ids, bits);
+  if (blockIdx.x == 0) {
+    build_table(a, scratch.table, bits, below);
+    return;
+  }
   if (threadIdx.x < kWave) {
     int32_t total;
     const int32_t below4 = bits_below(bits, lane, total);
@@ -342,7 +385,6 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) 
   __syncthreads();
   const int32_t e = uniform(chosen), n = uniform(count);
   if (e < 0) return;
-  float* red = reinterpret_cast<float*>(scratch);
   if (n <= 16) up_tile<T, kFp8, 1>(a, e, c * 16, n, list, red);
   else if (n <= 32) up_tile<T, kFp8, 2>(a, e, c * 16, n, list, red);
   else up_tile<T, kFp8, 4>(a, e, c * 16, n, list, red);
@@ -364,7 +406,7 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
   using W = Weights<TBF16, kFp8>;
   extern __shared__ __align__(16) float acc[];  // [waves][T][16], then the table
   const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), r = lane % 16, g = lane / 16;
-  const int32_t n0 = blockIdx.x * 16;
+  const int32_t tile = blockIdx.x / a.parts, part = blockIdx.x - tile * a.parts, n0 = tile * 16;
   const int32_t groups = uniform(*a.groups);
   int32_t* le = reinterpret_cast<int32_t*>(acc + kDownWaves * a.T * 16);  // [groups] experts
   int32_t* lf = le + a.groups_max;                                        // [groups + 1] first entries
@@ -389,7 +431,7 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
     bool both;       // the parts of h in operands of their own
     int32_t group;   // >= groups: none
   } blk[2];
-  int32_t group = 0, at = wave;  // the next block to load
+  int32_t group = 0, at = part * kDownWaves + wave;  // the next block to load
   auto load = [&](Block& v) {
     while (at >= a.fb && group < groups) at -= a.fb, ++group;
     v.group = group;
@@ -412,7 +454,7 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
         v.lo[s] = c < a.F ? *reinterpret_cast<const u32x4*>(a.hlo + (row + c) * 2) : u32x4{0, 0, 0, 0};
       }
     }
-    at += kDownWaves;
+    at += a.parts * kDownWaves;
   };
   f32x4 tot = {0, 0, 0, 0};
   int32_t cur = -1;
@@ -457,10 +499,36 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
   }
   if (cur >= 0) finish();
   __syncthreads();
+  float* out = a.partial + static_cast<int64_t>(tile) * a.parts * a.T * 16;
   for (int32_t i = threadIdx.x; i < a.T * 16; i += blockDim.x) {
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < kDownWaves; ++w) v += acc[w * a.T * 16 + i];
+    if (a.parts == 1) store_elem<T>(a.y + static_cast<int64_t>(i / 16) * a.ys, n0 + i % 16, v);
+    else __hip_atomic_store(out + part * a.T * 16 + i, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (a.parts == 1) return;
+  // The part that arrives last adds them all, in order, whichever it is.  The sums, the count and
+  // the reading of the sums are atomics of device scope, which pass the L2 of the XCD by; a wave
+  // counts itself only when its sums are there.  (A fence instead writes back the whole L2 of
+  // the XCD, for every workgroup: 100 us.)
+  __shared__ bool last;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(a.arrived + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.parts - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int32_t i = threadIdx.x; i < a.T * 16; i += blockDim.x) {
+    float v = 0.0f;
+    for (int32_t p0 = 0; p0 < a.parts; p0 += 8) {  // eight loads at a time
+      float s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        s[j] = __hip_atomic_load(out + min(p0 + j, a.parts - 1) * a.T * 16 + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v += p0 + j < a.parts ? s[j] : 0.0f;
+    }
     store_elem<T>(a.y + static_cast<int64_t>(i / 16) * a.ys, n0 + i % 16, v);
   }
 }
@@ -509,6 +577,16 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
     c.take<float>(static_cast<size_t>(n));
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
+    // Launch 2 has H / 16 column tiles: below 512 their blocks of F are split over several
+    // workgroups each, as long as every wave may have one (at most 32).
+    const int64_t tiles = p->H / 16, blocks = p->groups * ((p->F + 127) / 128);
+    p->parts = 512 / tiles < 32 ? 512 / tiles : 32;
+    if (p->parts > (blocks + kDownWaves - 1) / kDownWaves) p->parts = (blocks + kDownWaves - 1) / kDownWaves;
+    if (p->parts < 1) p->parts = 1;
+    if (p->parts > 1) {
+      c.take<int32_t>(static_cast<size_t>(tiles));
+      c.take<float>(static_cast<size_t>(tiles * p->parts * p->T * 16));
+    }
   }
   p->ws_bytes = c.off;
   return FFNWB_OK;
@@ -520,7 +598,7 @@ static bool launch_t(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void
   if (!launch_bound(layer_up_kernel<T, kFp8>, dim3(grid), dim3(kUpWaves * kWave), 0, s, begin, nullptr, a)) return false;
   const size_t lds = (kDownWaves * p.T * 16 + 2 * p.groups + 1 + 2 * p.T * p.K) * 4;
   allow_large_lds(reinterpret_cast<const void*>(layer_down_kernel<T, kFp8>), lds);
-  return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16)), dim3(kDownWaves * kWave), lds, s, nullptr,
+  return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16 * p.parts)), dim3(kDownWaves * kWave), lds, s, nullptr,
                       end, a);
 }
 
@@ -549,6 +627,11 @@ int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStrea
   a.weight = c.take<float>(n);
   a.hhi = reinterpret_cast<char*>(c.take<uint16_t>(n * p.F));
   a.hlo = reinterpret_cast<char*>(c.take<uint16_t>(n * p.F));
+  a.parts = static_cast<int32_t>(p.parts);
+  if (p.parts > 1) {
+    a.arrived = c.take<int32_t>(static_cast<size_t>(p.H / 16));
+    a.partial = c.take<float>(static_cast<size_t>(p.H * p.parts * p.T));
+  }
   const bool fp8 = d->weight_dtype == FFNWB_DT_FP8_E4M3;
   void *b = d->ev_layer_begin, *e = d->ev_layer_end;
   const bool ok = d->dtype == FFNWB_DT_FP16 ? launch_t<TF16, true>(a, p, s, b, e)

@@ -619,7 +619,7 @@ typedef struct moe_layer_desc {
 /* Validates *d and returns the workspace size in bytes (host only).  Errors:
    FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes or a required array NULL), FFNWB_ERR_PARAM_INVALID
    (a code, range, multiple or alignment above violated, a stride below its row or above
-   2^40, min(T K, E) * F / 16 of 2^24 - 1 or more; scales of weights given with
+   2^40, min(T K, E) * F / 16 of 2^23 - 1 or more; scales of weights given with
    BF16 weights, or missing with e4m3 ones). */
 int moe_layer_workspace_size(const moe_layer_desc* d, size_t* ws_bytes);
 

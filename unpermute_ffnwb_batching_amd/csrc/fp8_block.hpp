@@ -18,6 +18,10 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// Loads from global memory: pointers taken out of a structure would be loaded from as "flat".
+__device__ __forceinline__ u32x4 load16(const void* p) { return *(const __attribute__((address_space(1))) u32x4*)p; }
+__device__ __forceinline__ float load_f32(const float* p) { return *(const __attribute__((address_space(1))) float*)p; }
+
 // The scale of a block whose largest |x| has the FP32 bits `amax_bits`.  Taken as integers
 // (monotonic in |x|, NaN above infinity above every finite value), so that a NaN or an
 // infinity in the block reaches its scale.  2^-126 keeps the quotients of tiny blocks finite.

@@ -227,27 +227,38 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm_direct_kernel(MmArgs 
     u32x4 w[NF][2], x[MT][2];
     float ws[NF], xs[MT];
   } blk[2];
-  const u32x4 zero = {0, 0, 0, 0};
+  // A block's columns; past the end of K the row's last ones (no branch in the way of the loads),
+  // which `multiply` clears.
+  const int32_t last = static_cast<int32_t>(a.K) - 16;
   auto load = [&](Block& v, int32_t b) {
     if (b >= a.kb) return;
-    const int64_t k0 = static_cast<int64_t>(b) * kBlk + g * 16, k1 = k0 + 64;
-    const bool in0 = k0 < a.K, in1 = k1 < a.K;  // K is a multiple of 16
+    const int32_t k0 = min(b * kBlk + g * 16, last), k1 = min(b * kBlk + 64 + g * 16, last);
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-      v.w[f][0] = in0 ? *reinterpret_cast<const u32x4*>(wp[f] + k0) : zero;
-      v.w[f][1] = in1 ? *reinterpret_cast<const u32x4*>(wp[f] + k1) : zero;
-      v.ws[f] = wsp[f][b];
+      v.w[f][0] = load16(wp[f] + k0);
+      v.w[f][1] = load16(wp[f] + k1);
+      v.ws[f] = load_f32(wsp[f] + b);
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      v.x[i][0] = in0 ? *reinterpret_cast<const u32x4*>(xp[i] + k0) : zero;
-      v.x[i][1] = in1 ? *reinterpret_cast<const u32x4*>(xp[i] + k1) : zero;
-      v.xs[i] = xsp[i][b];
+      v.x[i][0] = load16(xp[i] + k0);
+      v.x[i][1] = load16(xp[i] + k1);
+      v.xs[i] = load_f32(xsp[i] + b);
     }
   };
   f32x4 tot[NF][MT] = {};
-  auto multiply = [&](const Block& v, int32_t b) {
+  auto multiply = [&](Block& v, int32_t b) {
     if (b >= a.kb) return;
+    if ((b + 1) * kBlk > a.K) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (b * kBlk + h * 64 + g * 16 > last) {
+#pragma unroll
+          for (int f = 0; f < NF; ++f) v.w[f][h] = u32x4{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < MT; ++i) v.x[i][h] = u32x4{0, 0, 0, 0};
+        }
+    }
     f32x4 p[NF][MT] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {  // 8 columns of each lane

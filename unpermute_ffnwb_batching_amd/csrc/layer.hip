@@ -20,8 +20,7 @@ namespace ffnwb {
 
 constexpr int kLyMaxTokens = 64;
 constexpr int kLyMaxSlots = 64;
-constexpr int kLyMaxIds = kLyMaxTokens * kLyMaxSlots;
-constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kUpMaxWaves = 8, kDownWaves = 8;
 
 struct LayerArgs {
   int32_t T, K, E, H, F;
@@ -65,12 +64,17 @@ struct Weights {
   u32x4 v[kLoads];
   // column of step s, for the lanes of group g
   __device__ static int32_t col(int s, int32_t g) { return kFp8 ? (s / 2) * 64 + g * 16 + (s % 2) * 8 : s * 32 + g * 8; }
+  // Columns c0 .. c0 + 127 of a row of `end`; past its end, the row's last columns (no branch in
+  // the way of the loads), which `cut` clears.
   __device__ void load(const char* row, int32_t c0, int32_t g, int32_t end) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int32_t c = c0 + col(kFp8 ? 2 * i : i, g);
-      v[i] = c < end ? *reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(c) * kElt) : u32x4{0, 0, 0, 0};
-    }
+    for (int i = 0; i < kLoads; ++i)
+      v[i] = load16(row + static_cast<int64_t>(min(c0 + col(kFp8 ? 2 * i : i, g), end - 16 / kElt)) * kElt);
+  }
+  __device__ void cut(int32_t c0, int32_t g, int32_t end) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      if (c0 + col(kFp8 ? 2 * i : i, g) >= end) v[i] = u32x4{0, 0, 0, 0};
   }
   __device__ u32x4 step(int s) const {
     if constexpr (kFp8) {
@@ -132,16 +136,18 @@ __device__ __forceinline__ float slot_scale(const LayerArgs& a, int32_t t, int32
 // and weights, for launch 2.  An expert's tokens are the bits of a mask, so that every slot finds
 // its entry's place by counting bits; a token that names an expert twice has one entry, at its
 // first slot, with the sum of the weights.
+template <int kIds>
 struct TableLds {
-  int16_t ids[kLyMaxIds];
-  uint16_t first[kLyMaxIds];      // [rank] first entry
-  uint32_t mask[kLyMaxIds][2];    // [rank] tokens
+  int16_t ids[kIds];
+  uint16_t first[kIds];      // [rank] first entry
+  uint32_t mask[kIds][2];    // [rank] tokens
 };
 
-__device__ void build_table(const LayerArgs& a, TableLds& s, const uint32_t* bits, int32_t* below) {
+template <int kIds>
+__device__ void build_table(const LayerArgs& a, TableLds<kIds>& s, const uint32_t* bits, int32_t* below) {
   const int32_t n = a.T * a.K, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  __shared__ int32_t sums[2][kUpWaves];
-  static_assert(kMaxExperts / 32 == kUpWaves * kWave, "one word of the experts' bits to a thread");
+  constexpr int kWords = kMaxExperts / 32;  // of the experts' bits, one to a thread (of at least as many)
+  __shared__ int32_t sums[2][kUpMaxWaves];
   if (a.parts > 1)
     for (int32_t i = threadIdx.x; i < a.H / 16; i += blockDim.x) a.arrived[i] = 0;
   if (threadIdx.x < kWave) {
@@ -163,9 +169,9 @@ __device__ void build_table(const LayerArgs& a, TableLds& s, const uint32_t* bit
     if (s.ids[i] >= 0) atomicOr(&s.mask[rank(s.ids[i])][t / 32], 1u << (t % 32));
   }
   __syncthreads();
-  // exclusive sums of entries and of groups over the experts, a word of experts to a thread
-  const uint32_t word = bits[threadIdx.x];
-  const int32_t r0 = below[threadIdx.x], r1 = r0 + __popc(word);
+  // exclusive sums of entries and of groups over the experts
+  const uint32_t word = threadIdx.x < kWords ? bits[threadIdx.x] : 0;
+  const int32_t r0 = threadIdx.x < kWords ? below[threadIdx.x] : ranks, r1 = r0 + __popc(word);
   auto tokens = [&](int32_t r) { return __popc(s.mask[r][0]) + __popc(s.mask[r][1]); };
   int32_t mine = 0, mine_g = 0;
   for (int32_t r = r0; r < r1; ++r) mine += tokens(r), mine_g += (tokens(r) + 15) / 16;
@@ -214,11 +220,14 @@ __device__ void build_table(const LayerArgs& a, TableLds& s, const uint32_t* bit
 // ------------------------------------------------------------------ launch 1: gate, up, SwiGLU
 
 // h of 16 columns from f0 of expert e for its `count` tokens (at most MT * 16); list[j] is token
-// j's slot.  The four waves take every fourth 128-block of H; their totals are added in order.
-template <class T, bool kFp8, int MT>
+// j's slot.  The waves of a tile take the 128-blocks of H in turn; their totals are added in
+// order.  With kSplit = 1 every wave has a tile of its own (f0 may then be past F).
+template <class T, bool kFp8, int MT, int kSplit>
 __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count, const int32_t* list, float* red) {
   using W = Weights<T, kFp8>;
-  const int32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, r = lane % 16, g = lane / 16;
+  const int32_t lane = threadIdx.x % kWave, r = lane % 16, g = lane / 16;
+  const int32_t wave = kSplit == 1 ? 0 : uniform(threadIdx.x / kWave);
+  if (kSplit == 1 && f0 >= a.F) return;
   const int64_t rowb = static_cast<int64_t>(a.H) * W::kElt;
   const char* wp[2] = {a.w13 + (static_cast<int64_t>(e) * 2 * a.F + f0 + r) * rowb,
                        a.w13 + (static_cast<int64_t>(e) * 2 * a.F + a.F + f0 + r) * rowb};
@@ -237,9 +246,7 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
     W w[2];
     u32x4 x[MT == 1 ? 4 : 1];
   } blk[2];
-  auto x_at = [&](int i, int32_t c) {
-    return c < a.H ? *reinterpret_cast<const u32x4*>(xp[i] + static_cast<int64_t>(c) * 2) : u32x4{0, 0, 0, 0};
-  };
+  auto x_at = [&](int i, int32_t c) { return load16(xp[i] + static_cast<int64_t>(min(c, a.H - 8)) * 2); };
   auto load = [&](Block& v, int32_t b) {
     if (b >= a.hb) return;
     v.w[0].load(wp[0], b * kBlk, g, a.H);
@@ -249,9 +256,14 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
       for (int s = 0; s < 4; ++s) v.x[s] = x_at(0, b * kBlk + W::col(s, g));
     }
   };
-  auto multiply = [&](const Block& v, int32_t b) {
+  auto multiply = [&](Block& v, int32_t b) {
     if (b >= a.hb) return;
-    const float s0 = kFp8 ? wsp[0][b] : 1.0f, s1 = kFp8 ? wsp[1][b] : 1.0f;
+    const float s0 = kFp8 ? load_f32(wsp[0] + b) : 1.0f, s1 = kFp8 ? load_f32(wsp[1] + b) : 1.0f;
+    const bool tail = (b + 1) * kBlk > a.H;
+    if (tail) {
+      v.w[0].cut(b * kBlk, g, a.H);
+      v.w[1].cut(b * kBlk, g, a.H);
+    }
     f32x4 p[2][MT] = {};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -261,6 +273,7 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
         u32x4 xv;
         if constexpr (MT == 1) xv = v.x[s];
         else xv = x_at(i, b * kBlk + W::col(s, g));
+        if (tail && b * kBlk + W::col(s, g) >= a.H) xv = u32x4{0, 0, 0, 0};
         p[0][i] = Mat<T>::mul(w0, xv, p[0][i]);
         p[1][i] = Mat<T>::mul(w1, xv, p[1][i]);
       }
@@ -274,28 +287,34 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
       }
   };
   load(blk[0], wave);
-  for (int32_t b = wave; b < a.hb; b += 2 * kUpWaves) {
-    load(blk[1], b + kUpWaves);
+  for (int32_t b = wave; b < a.hb; b += 2 * kSplit) {
+    load(blk[1], b + kSplit);
     multiply(blk[0], b);
-    load(blk[0], b + 2 * kUpWaves);
-    multiply(blk[1], b + kUpWaves);
+    load(blk[0], b + 2 * kSplit);
+    multiply(blk[1], b + kSplit);
   }
   f32x4* rv = reinterpret_cast<f32x4*>(red);  // [wave][2 MT][lane]
-  __syncthreads();                            // `list` may share red's memory with the ids
+  if constexpr (kSplit > 1) {
+    __syncthreads();  // the ids share red's memory
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    rv[(wave * 2 * MT + i) * kWave + lane] = tot[0][i];
-    rv[(wave * 2 * MT + MT + i) * kWave + lane] = tot[1][i];
+    for (int i = 0; i < MT; ++i) {
+      rv[(wave * 2 * MT + i) * kWave + lane] = tot[0][i];
+      rv[(wave * 2 * MT + MT + i) * kWave + lane] = tot[1][i];
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  for (int32_t i = wave; i < MT; i += kUpWaves) {
-    const int32_t j = i * 16 + r;
-    if (j >= count) continue;
-    f32x4 gv = {}, uv = {};
 #pragma unroll
-    for (int w = 0; w < kUpWaves; ++w) {
-      gv += rv[(w * 2 * MT + i) * kWave + lane];
-      uv += rv[(w * 2 * MT + MT + i) * kWave + lane];
+  for (int32_t i = 0; i < MT; ++i) {
+    const int32_t j = i * 16 + r;
+    if (j >= count || (kSplit > 1 && i % kSplit != wave)) continue;
+    f32x4 gv = tot[0][i], uv = tot[1][i];
+    if constexpr (kSplit > 1) {
+      gv = uv = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int32_t w = 0; w < kSplit; ++w) {
+        gv += rv[(w * 2 * MT + i) * kWave + lane];
+        uv += rv[(w * 2 * MT + MT + i) * kWave + lane];
+      }
     }
     u32x2 hi = {}, lo = {};
 #pragma unroll
@@ -314,19 +333,36 @@ __device__ void up_tile(const LayerArgs& a, int32_t e, int32_t f0, int32_t count
   }
 }
 
-template <class T, bool kFp8>
-__global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) {
-  __shared__ __align__(16) union {
-    TableLds table;
-    float totals[kUpWaves * 8 * kWave * 4];  // of the waves, up to 64 tokens
-  } scratch;
+// h of one expert's tokens, 16 to an operand.
+template <class T, bool kFp8, int kTokens, int kSplit>
+__device__ __forceinline__ void up_tokens(const LayerArgs& a, int32_t e, int32_t f0, int32_t n, const int32_t* list, float* red) {
+  if constexpr (kTokens == 16) {
+    up_tile<T, kFp8, 1, kSplit>(a, e, f0, n, list, red);
+  } else {
+    if (n <= 16) up_tile<T, kFp8, 1, kSplit>(a, e, f0, n, list, red);
+    else if (n <= 32) up_tile<T, kFp8, 2, kSplit>(a, e, f0, n, list, red);
+    else up_tile<T, kFp8, 4, kSplit>(a, e, f0, n, list, red);
+  }
+}
+
+// kTokens: the most tokens, 16 or 64.  The registers and LDS of 64 leave a CU 3 workgroups of 4
+// waves, those of 16 leave it 4 (one token's layer of hidden 7168 and inter 2048, 1152 workgroups:
+// 58 us with the former, 46 us with the latter).
+template <class T, bool kFp8, int kTokens, int kSplit>
+__global__ __launch_bounds__((kSplit == 1 ? 4 : kSplit) * kWave) void layer_up_kernel(LayerArgs a) {
+  extern __shared__ __align__(16) char scratch[];  // the table's, then the waves' totals
   __shared__ uint32_t bits[kMaxExperts / 32];
   __shared__ int32_t below[kMaxExperts / 32 + 1];
-  __shared__ int32_t lists[kUpWaves][kLyMaxTokens];
+  __shared__ int32_t lists[kUpMaxWaves][kLyMaxTokens];
   __shared__ int32_t chosen, count;
-  int16_t* ids = scratch.table.ids;
-  float* red = scratch.totals;
-  const int32_t rank = (static_cast<int32_t>(blockIdx.x) - 1) / a.ctiles, c = static_cast<int32_t>(blockIdx.x) - 1 - rank * a.ctiles;
+  using Table = TableLds<kTokens * kLyMaxSlots>;
+  Table& table = *reinterpret_cast<Table*>(scratch);
+  int16_t* ids = table.ids;
+  float* red = reinterpret_cast<float*>(scratch);
+  const int32_t per = kSplit == 1 ? (a.ctiles + 3) / 4 : a.ctiles;  // workgroups of an expert
+  const int32_t rank = (static_cast<int32_t>(blockIdx.x) - 1) / per;
+  const int32_t c = (static_cast<int32_t>(blockIdx.x) - 1 - rank * per) * (kSplit == 1 ? 4 : 1) +
+                    (kSplit == 1 ? static_cast<int32_t>(threadIdx.x / kWave) : 0);
   const int32_t lane = threadIdx.x % kWave;
   if (blockIdx.x != 0 && a.T * a.K <= kWave) {
     // Up to 64 slots are one to a lane, and every wave finds the workgroup's expert (the rank-th
@@ -345,15 +381,13 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) 
     if (head) list[count_below(heads)] = lane;
     wave_lds_sync();
     const int32_t n = __popcll(heads);
-    if (n <= 16) up_tile<T, kFp8, 1>(a, e, c * 16, n, list, red);
-    else if (n <= 32) up_tile<T, kFp8, 2>(a, e, c * 16, n, list, red);
-    else up_tile<T, kFp8, 4>(a, e, c * 16, n, list, red);
+    up_tokens<T, kFp8, kTokens, kSplit>(a, e, c * 16, n, list, red);
     return;
   }
   int32_t* list = lists[0];
   load_ids(a, ids, bits);
   if (blockIdx.x == 0) {
-    build_table(a, scratch.table, bits, below);
+    build_table(a, table, bits, below);
     return;
   }
   if (threadIdx.x < kWave) {
@@ -385,9 +419,7 @@ __global__ __launch_bounds__(kUpWaves* kWave) void layer_up_kernel(LayerArgs a) 
   __syncthreads();
   const int32_t e = uniform(chosen), n = uniform(count);
   if (e < 0) return;
-  if (n <= 16) up_tile<T, kFp8, 1>(a, e, c * 16, n, list, red);
-  else if (n <= 32) up_tile<T, kFp8, 2>(a, e, c * 16, n, list, red);
-  else up_tile<T, kFp8, 4>(a, e, c * 16, n, list, red);
+  up_tokens<T, kFp8, kTokens, kSplit>(a, e, c * 16, n, list, red);
 }
 
 // ------------------------------------------------------------------ launch 2: down, weighted sum
@@ -430,6 +462,7 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
     float s;
     bool both;       // the parts of h in operands of their own
     int32_t group;   // >= groups: none
+    int32_t c0;
   } blk[2];
   int32_t group = 0, at = part * kDownWaves + wave;  // the next block to load
   auto load = [&](Block& v) {
@@ -438,20 +471,19 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
     if (group >= groups) return;
     const int32_t e = uniform(le[group]), first = lf[group], n = lf[group + 1] - first, c0 = at * kBlk;
     v.w.load(a.w2 + (static_cast<int64_t>(e) * a.H + n0 + r) * rowb, c0, g, a.F);
-    v.s = kFp8 ? a.w2s[(static_cast<int64_t>(e) * a.hb + n0 / kBlk) * a.fb + at] : 1.0f;
+    v.s = kFp8 ? load_f32(a.w2s + (static_cast<int64_t>(e) * a.hb + n0 / kBlk) * a.fb + at) : 1.0f;
+    v.c0 = c0;
     v.both = !kFp8 || uniform(n) > 8;
     const int64_t row = static_cast<int64_t>(ls[first + min(v.both ? r : r & 7, n - 1)]) * a.F;
     const char* h0 = v.both || r < 8 ? a.hhi : a.hlo;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int32_t c = c0 + W::col(s, g);
-      v.h[s] = c < a.F ? *reinterpret_cast<const u32x4*>(h0 + (row + c) * 2) : u32x4{0, 0, 0, 0};
+      v.h[s] = load16(h0 + (row + min(c0 + W::col(s, g), a.F - 8)) * 2);
     }
     if (v.both) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const int32_t c = c0 + W::col(s, g);
-        v.lo[s] = c < a.F ? *reinterpret_cast<const u32x4*>(a.hlo + (row + c) * 2) : u32x4{0, 0, 0, 0};
+        v.lo[s] = load16(a.hlo + (row + min(c0 + W::col(s, g), a.F - 8)) * 2);
       }
     }
     at += a.parts * kDownWaves;
@@ -474,11 +506,17 @@ __global__ __launch_bounds__(kDownWaves* kWave, 4) void layer_down_kernel(LayerA
     }
     tot = f32x4{0, 0, 0, 0};
   };
-  auto multiply = [&](const Block& v) {
+  auto multiply = [&](Block& v) {
     if (v.group >= groups) return;
     if (cur != v.group) {
       if (cur >= 0) finish();
       cur = v.group;
+    }
+    if (v.c0 + kBlk > a.F) {
+      v.w.cut(v.c0, g, a.F);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (v.c0 + W::col(s, g) >= a.F) v.h[s] = v.lo[s] = u32x4{0, 0, 0, 0};
     }
     f32x4 p = {0, 0, 0, 0};
 #pragma unroll
@@ -567,7 +605,11 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
   p->ranks = n < p->E ? n : p->E;
   p->groups = p->ranks + n / 16 < n ? p->ranks + n / 16 : n;
   // one dimension of the grid: fewer than 2^32 threads
-  if (p->ranks * (p->F / 16) >= (int64_t{1} << 32) / (kUpWaves * kWave) - 1) return FFNWB_ERR_PARAM_INVALID;
+  if (p->ranks * (p->F / 16) >= (int64_t{1} << 32) / (kUpMaxWaves * kWave) - 1) return FFNWB_ERR_PARAM_INVALID;
+  // Launch 1: four waves to a tile, eight where the tiles are few and H is long; a tile to each
+  // wave where H has fewer blocks than four.
+  const int64_t hb = (p->H + 127) / 128;
+  p->split = hb < 4 ? 1 : hb >= 16 && p->ranks * (p->F / 16) < 1024 ? 8 : 4;
   Carve c;
   if (n > 0) {
     c.take<int32_t>(1);
@@ -577,11 +619,12 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
     c.take<float>(static_cast<size_t>(n));
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
-    // Launch 2 has H / 16 column tiles: below 512 their blocks of F are split over several
-    // workgroups each, as long as every wave may have one (at most 32).
+    // Launch 2 has H / 16 column tiles: below 256 their blocks of F are split over several
+    // workgroups each, as long as every wave may have two (at most 32 workgroups).  One token's 6
+    // experts of hidden 2944 and inter 496: 102 us by one workgroup a tile, 17 us by two.
     const int64_t tiles = p->H / 16, blocks = p->groups * ((p->F + 127) / 128);
-    p->parts = 512 / tiles < 32 ? 512 / tiles : 32;
-    if (p->parts > (blocks + kDownWaves - 1) / kDownWaves) p->parts = (blocks + kDownWaves - 1) / kDownWaves;
+    p->parts = tiles >= 256 ? 1 : 512 / tiles < 32 ? 512 / tiles : 32;
+    if (p->parts > blocks / (2 * kDownWaves)) p->parts = blocks / (2 * kDownWaves);
     if (p->parts < 1) p->parts = 1;
     if (p->parts > 1) {
       c.take<int32_t>(static_cast<size_t>(tiles));
@@ -592,10 +635,26 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
   return FFNWB_OK;
 }
 
+template <class T, bool kFp8, int kTokens, int kSplit>
+static bool launch_up(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void* begin) {
+  const uint32_t grid = static_cast<uint32_t>(1 + p.ranks * (kSplit == 1 ? (a.ctiles + 3) / 4 : a.ctiles));
+  const size_t table = sizeof(TableLds<kTokens * kLyMaxSlots>), totals = size_t{kSplit} * 2 * (kTokens / 16) * kWave * 16;
+  const size_t lds = table > totals ? table : totals;
+  auto kernel = layer_up_kernel<T, kFp8, kTokens, kSplit>;
+  allow_large_lds(reinterpret_cast<const void*>(kernel), lds);
+  return launch_bound(kernel, dim3(grid), dim3((kSplit == 1 ? 4 : kSplit) * kWave), lds, s, begin, nullptr, a);
+}
+
+template <class T, bool kFp8, int kTokens>
+static bool launch_up(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void* begin) {
+  return p.split == 1   ? launch_up<T, kFp8, kTokens, 1>(a, p, s, begin)
+         : p.split == 4 ? launch_up<T, kFp8, kTokens, 4>(a, p, s, begin)
+                        : launch_up<T, kFp8, kTokens, 8>(a, p, s, begin);
+}
+
 template <class T, bool kFp8>
 static bool launch_t(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void* begin, void* end) {
-  const uint32_t grid = static_cast<uint32_t>(1 + p.ranks * a.ctiles);
-  if (!launch_bound(layer_up_kernel<T, kFp8>, dim3(grid), dim3(kUpWaves * kWave), 0, s, begin, nullptr, a)) return false;
+  if (!(p.T <= 16 ? launch_up<T, kFp8, 16>(a, p, s, begin) : launch_up<T, kFp8, 64>(a, p, s, begin))) return false;
   const size_t lds = (kDownWaves * p.T * 16 + 2 * p.groups + 1 + 2 * p.T * p.K) * 4;
   allow_large_lds(reinterpret_cast<const void*>(layer_down_kernel<T, kFp8>), lds);
   return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16 * p.parts)), dim3(kDownWaves * kWave), lds, s, nullptr,

@@ -225,6 +225,27 @@ def test_no_rows():
     torch.cuda.synchronize()
 
 
+def test_rows_past_4_gib():
+    # rows 64 MiB apart: the last ones start beyond 2^32 bytes, and 256 rows pass 32-bit offsets
+    rows, k, n = 70, 256, 96
+    c = matmul_inputs(16, rows, k, n)
+    stride = 1 << 26
+    wide = torch.empty(rows * stride, dtype=torch.uint8, device="cuda").view(rows, stride)
+    x = wide[:, 64:64 + k].view(FP8)
+    x.view(torch.uint8).copy_(dev(c["x"]))
+    y = torch.empty((rows, 1 << 25), dtype=BF16, device="cuda")[:, :n]
+    q = wide[:, 4096:4096 + 130].view(FP8)
+    print("product and quantising of rows 64 MiB apart", flush=True)
+    F.moe_grouped_matmul_fp8(x, dev(c["xs"]), fp8(c["w"]), dev(c["ws"]), out={"y": y})
+    src = torch.randn(rows, 130, device="cuda")
+    F.moe_quant_fp8(src, out={"q": q})
+    torch.cuda.synchronize()
+    want, off, _ = matmul_reference(c, None, "none", True)
+    close(y, want, off, BF16)
+    codes, _ = O.quantise_rows(src.cpu().numpy())
+    np.testing.assert_array_equal(q.contiguous().view(torch.uint8).cpu().numpy(), codes)
+
+
 def test_weights_past_4_gib():
     # the last expert's weights start beyond 2^32 bytes
     experts, n, k = 40, 8192, 16384
@@ -259,6 +280,32 @@ def _check_layer(c, dtype, mask=None):
     want, off = layer_reference(c, dev(c["x"], dtype), mask)
     close(call.out["y"], want, off, dtype)
     return call
+
+
+def test_layer_every_slot_an_expert_of_its_own():
+    # 64 tokens x 64 slots over 8192 experts: the largest table (4096 experts of one token each)
+    T, K, E, H, inter = 64, 64, 8192, 16, 16
+    rng = np.random.default_rng(51)
+    c = layer_inputs(52, T, K, 4, H, inter)
+    pick = rng.permutation(E)[:T * K].reshape(T, K).astype(np.int32)
+    kind = pick % 4                              # expert e has the weights of kind e % 4
+    w13, w13s, w2, w2s = (np.tile(c[k], (E // 4,) + (1,) * (c[k].ndim - 1)) for k in ("w13", "w13s", "w2", "w2s"))
+    call = F.LayerCall(dev(c["x"], BF16), dev(pick), fp8(w13), fp8(w2), w13_scale=dev(w13s), w2_scale=dev(w2s),
+                       expert_scales=dev(c["scales"]))
+    print("layer: 4096 experts", flush=True)
+    call.run()
+    torch.cuda.synchronize()
+    c["ids"] = kind.astype(np.int32)
+    want, off = layer_reference(c, dev(c["x"], BF16))
+    close(call.out["y"], want, off, BF16)
+
+
+def test_layer_every_token_on_the_same_experts():
+    # 64 tokens on each of 5 experts: the widest operands, and groups of 16
+    c = layer_inputs(53, 64, 5, 5, 272, 144)
+    for dtype, weights in ((BF16, "fp8"), (FP16, "fp8"), (BF16, "bf16")):
+        print(f"layer: 64 tokens to an expert {dtype} {weights}", flush=True)
+        _check_layer(layer_inputs(53, 64, 5, 5, 272, 144, weights), dtype)
 
 
 LAYERS = [(1, 1, 1, 16, 16), (1, 2, 4, 128, 32), (1, 9, 16, 272, 144), (2, 3, 16, 128, 256), (5, 4, 6, 144, 112),

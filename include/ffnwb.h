@@ -485,7 +485,7 @@ typedef struct moe_quant_fp8_desc {
   int32_t dtype;             /* of x: FFNWB_DT_FP16, _BF16 or _FP32 */
   int32_t reserved0;         /* must be 0 */
   int64_t num_rows;          /* R >= 0 */
-  int64_t hidden;            /* H in (0, 2^20]; R * ceil(H / 128) < 2^30 */
+  int64_t hidden;            /* H in (0, 2^20]; R * ceil(H / 128) <= 2^28 - 16 */
   int64_t x_row_stride;      /* bytes, a multiple of the element size; 0 = H * element size */
   int64_t q_row_stride;      /* bytes; 0 = H */
   int64_t scale_row_stride;  /* elements; 0 = ceil(H / 128) */
@@ -501,7 +501,8 @@ typedef struct moe_quant_fp8_desc {
 
 /* Validates *d and returns the workspace size (0) (host only).  Errors:
    FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes, x, q or scale NULL), FFNWB_ERR_PARAM_INVALID (dtype,
-   sizes, a stride below its row or above 2^40, x not aligned to its element size, reserved0 != 0). */
+   sizes, a stride below its row or above 2^40 (above 2^60 / R for more than 2^20 rows), x not
+   aligned to its element size, reserved0 != 0). */
 int moe_quant_fp8_workspace_size(const moe_quant_fp8_desc* d, size_t* ws_bytes);
 
 /* Validates again, then enqueues the quantising on `stream` (one launch). */
@@ -561,8 +562,9 @@ typedef struct moe_grouped_matmul_fp8_desc {
 /* Validates *d and returns the workspace size in bytes (host only).  Errors:
    FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes or a required array NULL), FFNWB_ERR_PARAM_INVALID
    (a code, range, multiple or alignment above violated, a stride below its row or above
-   2^32, more than 2^24 tiles of output; group_list given without
-   num_groups or the other way round; num_experts != 1 without a group_list). */
+   2^32; group_list given without num_groups or the other way round; num_experts != 1 without
+   a group_list; more tiles of output than the 2^22 - 8 workgroups of a launch, which is never
+   so while (ceil(R / 64) + num_groups) * ceil(F / 16), F = N without SwiGLU, is no more). */
 int moe_grouped_matmul_fp8_workspace_size(const moe_grouped_matmul_fp8_desc* d, size_t* ws_bytes);
 
 /* Validates again, then enqueues the product on `stream`. */
@@ -619,8 +621,8 @@ typedef struct moe_layer_desc {
 /* Validates *d and returns the workspace size in bytes (host only).  Errors:
    FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes or a required array NULL), FFNWB_ERR_PARAM_INVALID
    (a code, range, multiple or alignment above violated, a stride below its row or above
-   2^40, min(T K, E) * F / 16 of 2^23 - 1 or more; scales of weights given with
-   BF16 weights, or missing with e4m3 ones). */
+   2^40; min(T K, E) * F / 16 of 2^23 - 1 or more; scales of weights given with BF16
+   weights, or missing with e4m3 ones). */
 int moe_layer_workspace_size(const moe_layer_desc* d, size_t* ws_bytes);
 
 /* Validates again, then enqueues the layer on `stream`. */

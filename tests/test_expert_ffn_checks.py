@@ -109,6 +109,47 @@ def test_invalid_parameters(name, over):
     assert getattr(F.lib(), name)(ctypes.byref(MAKE[name](**over)), None, 0, None) == F.FFNWB_ERR_PARAM_INVALID
 
 
+@pytest.mark.parametrize("name,most,past", [
+    ("moe_quant_fp8", dict(num_rows=(1 << 28) - 16, hidden=128), dict(num_rows=(1 << 28) - 15, hidden=128)),
+    ("moe_quant_fp8", dict(num_rows=32767, hidden=1 << 20, x_row_stride=1 << 40), dict(num_rows=32768, hidden=1 << 20)),
+    ("moe_quant_fp8", dict(num_rows=1 << 27, hidden=128, x_row_stride=1 << 33), dict(num_rows=1 << 27, hidden=128, x_row_stride=(1 << 33) + 2)),
+    # the widest tiles are 256 x 256 (16-bit results) and 128 x 256 (FP32)
+    ("moe_grouped_matmul_fp8", dict(num_rows=1 << 24, out_features=(1 << 14) - 256), dict(num_rows=1 << 24, out_features=1 << 14)),
+    ("moe_grouped_matmul_fp8", dict(num_rows=1 << 23, out_features=(1 << 14) - 256, out_dtype=3),
+     dict(num_rows=1 << 23, out_features=1 << 14, out_dtype=3)),
+    # rows too far apart for the tiles: 64 x 16
+    ("moe_grouped_matmul_fp8", dict(num_rows=1 << 24, out_features=240, x_row_stride=1 << 32),
+     dict(num_rows=1 << 24, out_features=256, x_row_stride=1 << 32)),
+    ("moe_layer", dict(num_tokens=64, slots=64, num_experts=4096, inter_size=(2047) * 16),
+     dict(num_tokens=64, slots=64, num_experts=4096, inter_size=2048 * 16)),
+])
+def test_largest_sizes(name, most, past):
+    if name == "moe_grouped_matmul_fp8":
+        most, past = ({**o, "num_groups": 1} for o in (most, past))
+    assert _ws(name, MAKE[name](**most))[0] == F.FFNWB_OK
+    assert _ws(name, MAKE[name](**past))[0] == F.FFNWB_ERR_PARAM_INVALID
+
+
+def test_a_call_whose_widest_tiles_fit_is_never_refused():
+    # (ceil(R / 64) + num_groups) * ceil(F / 16) up to the workgroups of a launch, whatever the times expected
+    for groups in (1, 300, 8192):
+        for f in (16, 512, 1 << 12, 1 << 17):
+            rows = min(((1 << 22) - 8) // (f // 16) - groups, 1 << 18) * 64
+            if rows <= 0:
+                continue
+            for over in (dict(out_features=f), dict(out_features=f, out_dtype=3), dict(out_features=2 * f, epilogue=1),
+                         dict(out_features=2 * f, epilogue=1, out_dtype=6)):
+                for stride in (0, 1 << 30):
+                    d = _matmul(num_rows=rows, num_groups=groups, num_experts=64, in_features=128, x_row_stride=stride, **over)
+                    assert _ws("moe_grouped_matmul_fp8", d)[0] == F.FFNWB_OK, (groups, f, over, stride)
+
+
+def test_calls_on_the_cpu_do_not_run():
+    for make in (_quant_call, _matmul_call, _layer_call):
+        with pytest.raises(ValueError, match="GPU"):
+            make().run()
+
+
 def test_workspace_is_checked_before_any_device_work():
     for name, over in (("moe_grouped_matmul_fp8", dict(num_groups=2000)),
                        ("moe_grouped_matmul_fp8", dict(epilogue=1, out_features=64, out_dtype=6)), ("moe_layer", {})):

@@ -10,6 +10,7 @@ import unpermute_ffnwb_batching_amd as F
 from _expert import (FP8, canary, close, dev, fp8, host, layer_inputs, layer_reference, matmul_inputs, matmul_reference,
                      quantised_close, untouched)
 from oracle import expert_ffn as O
+from unpermute_ffnwb_batching_amd.hip_events import HipEvent
 
 pytestmark = pytest.mark.gpu
 
@@ -223,6 +224,136 @@ def test_no_rows():
                        torch.zeros(2, 32, 64, device="cuda", dtype=BF16), torch.zeros(2, 64, 16, device="cuda", dtype=BF16)
                        )["y"].shape == (0, 64)
     torch.cuda.synchronize()
+
+
+def _sampled(c, groups, picks, epilogue, narrow):
+    # the picked rows' values, each with its own expert's weights
+    ends = np.cumsum([0] + [n for _, n in groups])
+    want, off = [], []
+    for r in picks:
+        e = groups[int(np.searchsorted(ends, r, side="right")) - 1][0]
+        one = dict(x=c["x"][r:r + 1], xs=c["xs"][r:r + 1], w=c["w"][e:e + 1], ws=c["ws"][e:e + 1])
+        v, o, _ = matmul_reference(one, None, epilogue, narrow)
+        want.append(v)
+        off.append(o)
+    return np.concatenate(want), np.concatenate(off)
+
+
+# many rows: the largest tiles, K that ends inside a block, odd widths, more than 4096 tiles (whose
+# list a launch of its own makes)
+LARGE = [
+    (1100, 272, 8208, BF16, "none", 1), (2304, 400, 1001, BF16, "none", 3), (2304, 400, 1001, FP32, "none", 3),
+    (5000, 144, 4128, FP16, "swiglu", 7), (5000, 144, 4128, FP32, "swiglu", 7), (5000, 144, 4128, FP8, "swiglu", 7),
+    (40000, 128, 4096, BF16, "none", 32), (40000, 128, 8192, FP8, "swiglu", 32), (30000, 16, 8191, FP32, "none", 40),
+]
+
+
+@pytest.mark.parametrize("rows,k,n,dtype,epilogue,experts", LARGE)
+def test_large_products(rows, k, n, dtype, epilogue, experts):
+    rng = np.random.default_rng(rows + n)
+    c = matmul_inputs(rows + k, rows, k, n, experts)
+    cut = np.sort(rng.integers(0, rows, experts - 1))
+    groups = [(int(e), int(m)) for e, m in enumerate(np.diff([0, *cut, rows]))]
+    swiglu, f = epilogue == "swiglu", n // 2 if epilogue == "swiglu" else n
+    out = {"y": canary((rows, f + 7 if dtype != FP8 else f), dtype)[:, :f]}
+    if dtype == FP8:
+        out["y_scale"] = canary((rows, -(-f // 128)), FP32)
+    print(f"product {rows} x {k} x {n} {dtype} {epilogue}, {experts} experts", flush=True)
+    got = F.moe_grouped_matmul_fp8(fp8(c["x"]), dev(c["xs"]), fp8(c["w"]), dev(c["ws"]), out_dtype=dtype, out=out,
+                                   group_list=dev(np.array(groups, np.int64)), epilogue=F.FFNWB_EPI_SWIGLU if swiglu else F.FFNWB_EPI_NONE)
+    torch.cuda.synchronize()
+    picks = np.unique(np.concatenate([[0, rows - 1], cut[:4], rng.integers(0, rows, 20)]))
+    want, off = _sampled(c, groups, picks, epilogue, dtype in (BF16, FP16))
+    at = torch.from_numpy(picks).cuda()
+    if dtype == FP8:
+        quantised_close(got["y"].view(torch.uint8)[at].view(FP8), got["y_scale"][at], want, off)
+    else:
+        close(got["y"][at], want, off, dtype)
+        whole = out["y"]._base.view(dtype).reshape(rows, f + 7)
+        assert untouched(whole[:, f:])
+
+
+@pytest.mark.parametrize("rows", [5, 40, 300, 1500])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_nan_stays_in_its_rows_and_columns(rows, dtype):
+    # K ends 16 into a block: what a tile reads past it are the next row's first columns, or the gap
+    # between rows; both hold NaN here
+    k, n, bad_row, bad_col = 272, 272, rows // 2, 130
+    c = matmul_inputs(61, rows, k, n, 2)
+    gaps = np.full((rows, 400), 0x7F, np.uint8)
+    gaps[:, :k] = c["x"]
+    gaps[bad_row, :k] = 0xFF
+    c["w"][1, bad_col] = 0x7F
+    c["w"][0] = 0x7F                            # an expert without rows
+    x = fp8(gaps)[:, :k]
+    print(f"NaN: {rows} rows {dtype}", flush=True)
+    y = F.moe_grouped_matmul_fp8(x, dev(c["xs"]), fp8(c["w"]), dev(c["ws"]), group_list=torch.tensor([[0, 0], [1, rows]], device="cuda"),
+                                 out_dtype=dtype)["y"]
+    torch.cuda.synchronize()
+    nan = np.zeros((rows, n), bool)
+    nan[bad_row], nan[:, bad_col] = True, True
+    got = torch.isnan(y).cpu().numpy()
+    assert (got == nan).all()
+    clean = dict(c, w=np.where(c["w"][1:] == 0x7F, 0, c["w"][1:]), ws=c["ws"][1:])
+    want, off, _ = matmul_reference(clean, None, "none", dtype == BF16)
+    keep_rows, keep_cols = np.arange(rows) != bad_row, np.arange(n) != bad_col
+    close(y[dev(keep_rows)][:, dev(keep_cols)], want[keep_rows][:, keep_cols], off[keep_rows][:, keep_cols], dtype)
+
+
+@pytest.mark.parametrize("tokens", [3, 20])
+def test_layer_nan_stays_with_its_token_and_expert(tokens):
+    c = layer_inputs(62, tokens, 2, 6, 272, 144)
+    c["ids"] = np.stack([[1, 3 if t % 2 else 4] for t in range(tokens)]).astype(np.int32)
+    c["w13"][0], c["w2"][0], c["w13"][2], c["w2"][2], c["w13"][5], c["w2"][5] = (0x7F,) * 6   # nobody's experts
+    xt = dev(c["x"], BF16)
+    wide = torch.full((tokens, 400), float("nan"), dtype=BF16, device="cuda")
+    wide[:, :272] = xt
+    wide[1] = float("nan")
+    args = dict(w13_scale=dev(c["w13s"]), w2_scale=dev(c["w2s"]), expert_scales=dev(c["scales"]))
+    print(f"layer: NaN in one of {tokens} tokens", flush=True)
+    y = F.moe_layer(wide[:, :272], dev(c["ids"]), fp8(c["w13"]), fp8(c["w2"]), **args)["y"]
+    c4 = dict(c, w2=c["w2"].copy())
+    c4["w2"][4, 17] = 0x7F                     # one column of one expert, of the even tokens
+    y4 = F.moe_layer(xt, dev(c["ids"]), fp8(c4["w13"]), fp8(c4["w2"]), **args)["y"]
+    torch.cuda.synchronize()
+    for e in (0, 2, 5):
+        c["w13"][e], c["w2"][e] = 0, 0
+    want, off = layer_reference(c, xt)
+    keep = np.arange(tokens) != 1
+    assert bool(torch.isnan(y[1]).all())
+    close(y[dev(keep)], want[keep], off[keep], BF16)
+    nan = np.zeros((tokens, 272), bool)
+    nan[::2, 17] = True
+    assert (torch.isnan(y4).cpu().numpy() == nan).all()
+    close(y4[1::2], want[1::2], off[1::2], BF16)
+
+
+def test_quant_of_the_most_rows():
+    # 2^28 - 16 rows of one element: the largest grid
+    rows = (1 << 28) - 16
+    x = torch.arange(rows, device="cuda", dtype=torch.int32).remainder_(2001).sub_(1000).to(FP16)[:, None]
+    print("quant: 2^28 - 16 rows", flush=True)
+    out = F.moe_quant_fp8(x)
+    torch.cuda.synchronize()
+    want, scales = O.quantise_rows(x[:2001].float().cpu().numpy())
+    whole = rows // 2001 * 2001
+    q = out["q"].view(torch.uint8)
+    for t, w in ((q, dev(want)), (out["scale"], dev(scales))):
+        assert bool((t[:whole].view(-1, 2001) == w.view(1, 2001)).all())
+        assert torch.equal(t[whole:], w[:rows - whole])
+
+
+def test_empty_calls_record_their_events():
+    e = [(HipEvent(), HipEvent()) for _ in range(3)]
+    F.moe_quant_fp8(torch.zeros(0, 64, device="cuda"), ev_quant=e[0])
+    F.moe_grouped_matmul_fp8(torch.zeros(0, 64, device="cuda", dtype=torch.uint8).view(FP8), torch.zeros(0, 1, device="cuda"),
+                             torch.zeros(32, 64, device="cuda", dtype=torch.uint8).view(FP8), torch.zeros(1, 1, device="cuda"),
+                             ev_matmul=e[1])
+    F.moe_layer(torch.zeros(0, 64, device="cuda", dtype=BF16), torch.zeros(0, 2, device="cuda", dtype=torch.int32),
+                torch.zeros(2, 32, 64, device="cuda", dtype=BF16), torch.zeros(2, 64, 16, device="cuda", dtype=BF16), ev_layer=e[2])
+    torch.cuda.synchronize()
+    for b, end in e:
+        assert 0.0 <= b.elapsed_ms(end) < 1000.0
 
 
 def test_rows_past_4_gib():

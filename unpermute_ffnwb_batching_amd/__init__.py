@@ -829,6 +829,7 @@ class _Call:
     def run(self, stream=None):
         """Enqueue the call on ``stream`` (default: the current stream of the tensors' device)."""
         index = self._device.index
+        _req(self._device.type == "cuda", f"the tensors are on {self._device}, not on a GPU")
         if stream is None:
             raw = torch._C._cuda_getCurrentRawStream(index)   # no Stream object in a serving loop's path
         else:

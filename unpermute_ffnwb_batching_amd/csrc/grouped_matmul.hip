@@ -435,24 +435,25 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     p->ntiles = tile ? (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256) : (p->F + 15) / 16;
     return p->mtiles * p->ntiles;
   };
+  auto quant_parts = [&](int64_t bm) { return (bm * fb + kMqThreads / 16 - 1) / (kMqThreads / 16); };
   // The kernel and the rows of its tiles: the least of the times expected.  Over 400 random sizes
   // (1 to 65536 rows, K and N to 8192, 0 to 256 groups) the choice is 3% slower than the best of
   // the shapes on average; a fixed rule (the largest tile that the groups fill and that gives
   // every CU one) was 15%.  256 rows of x, and the gate rows of w, have to be inside the 32-bit
   // offsets of the tile kernel.
   const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
+  const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup
   double best = 0;
   int64_t best_bm = 0;
   for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {  // negative: direct
     if (bm > 0 && (!near || (bm == 256 && !fast))) continue;
+    if (shape(bm > 0, bm > 0 ? bm : -bm) > most || (quant && bm < 0 && p->mtiles * quant_parts(p->bm) > most)) continue;
     const double t = expected_us(p->R, p->N, p->K, p->F, d->num_groups, swiglu, quant, fast, bm > 0, bm > 0 ? bm : -bm);
     if (best_bm == 0 || t < best) best = t, best_bm = bm;
   }
+  if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
   shape(best_bm > 0, best_bm > 0 ? best_bm : -best_bm);
-  // one dimension of the grid: fewer than 2^32 threads of at most 1024 a workgroup
-  if (p->mtiles * p->ntiles > (int64_t{1} << 22) - 8) return FFNWB_ERR_PARAM_INVALID;
-  p->quant_parts = (p->bm * fb + kMqThreads / 16 - 1) / (kMqThreads / 16);
-  if (quant && !p->tile && p->mtiles * p->quant_parts > (int64_t{1} << 22) - 8) return FFNWB_ERR_PARAM_INVALID;
+  p->quant_parts = quant_parts(p->bm);
   p->ws_bytes = 0;
   Carve c;
   // The list in every workgroup costs each about 1 us, two to a CU at a time; the launch 4 us.
@@ -505,7 +506,7 @@ static bool launch_tile(const MmArgs& a, const MatmulPlan& p, hipStream_t s, voi
 }
 
 int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan& p, void* ws, hipStream_t s) {
-  if (p.R == 0) return FFNWB_OK;
+  if (p.R == 0) return record_event(d->ev_matmul_begin, s) && record_event(d->ev_matmul_end, s) ? FFNWB_OK : FFNWB_ERR_RUNTIME;
   const bool quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
   MmArgs a{};
   a.rows = static_cast<int32_t>(p.R), a.K = p.K, a.N = p.N, a.F = p.F;

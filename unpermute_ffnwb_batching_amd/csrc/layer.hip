@@ -662,7 +662,7 @@ static bool launch_t(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void
 }
 
 int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStream_t s) {
-  if (p.T == 0) return FFNWB_OK;
+  if (p.T == 0) return record_event(d->ev_layer_begin, s) && record_event(d->ev_layer_end, s) ? FFNWB_OK : FFNWB_ERR_RUNTIME;
   LayerArgs a{};
   a.T = static_cast<int32_t>(p.T), a.K = static_cast<int32_t>(p.K), a.E = static_cast<int32_t>(p.E);
   a.H = static_cast<int32_t>(p.H), a.F = static_cast<int32_t>(p.F);

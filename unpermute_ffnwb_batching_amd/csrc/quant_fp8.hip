@@ -2,16 +2,17 @@
 //
 // A block of 128 elements is taken by 16 lanes, 8 elements each: one 16-byte load per lane of
 // 16-bit rows (two of FP32 rows), a maximum over the 16 lanes, 8 quotients, one 8-byte store.
-// Blocks are numbered row by row, so a wave's 4 blocks of one round are adjacent in memory
-// whatever the row length.
+// Blocks are numbered row by row, so a wave's 4 blocks are adjacent in memory whatever the row
+// length.  Bound by memory: 4608 rows of 7168 BF16 take 19.7 us, 100 MB at 5.1 TB/s (a plain copy
+// moves 4.8); the quotients by multiplication and FMA instead of division were worth 26%, and two
+// or four blocks to a thread's lane group, one after another, gained nothing.
 #include "fp8_block.hpp"
 #include "internal.hpp"
 
 namespace ffnwb {
 
 constexpr int kQThreads = 256;
-constexpr int kQGroups = kQThreads / 16;  // blocks a workgroup takes per round
-constexpr int kQRounds = 1;
+constexpr int kQGroups = kQThreads / 16;  // blocks a workgroup takes
 
 struct QuantArgs {
   int64_t rows, hidden;
@@ -49,28 +50,24 @@ __global__ __launch_bounds__(kQThreads) void quant_fp8_kernel(QuantArgs a) {
     rows = n < 0 ? 0 : n < rows ? n : rows;
   }
   const uint32_t lane16 = threadIdx.x % 16;
-  const uint32_t base = blockIdx.x * (kQGroups * kQRounds) + threadIdx.x / 16;
+  const uint32_t u = blockIdx.x * kQGroups + threadIdx.x / 16;
+  const uint32_t row = u / a.nblk, b = u - row * a.nblk;
+  const int64_t h0 = static_cast<int64_t>(b) * kBlk + lane16 * 8;
+  const bool in = row < rows && h0 < a.hidden;
+  float f[8] = {};
+  if (in) load8<T, kVec>(a.x + static_cast<int64_t>(row) * a.xs, h0, a.hidden, f);
+  uint32_t lo, hi;
+  const float s = quant_block(f, lo, hi);
+  if (!in) return;
+  char* q = a.q + static_cast<int64_t>(row) * a.qs + h0;
+  if constexpr (kVec) {
+    *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
+  } else {
 #pragma unroll
-  for (int r = 0; r < kQRounds; ++r) {
-    const uint32_t u = base + r * kQGroups;
-    const uint32_t row = u / a.nblk, b = u - row * a.nblk;
-    const int64_t h0 = static_cast<int64_t>(b) * kBlk + lane16 * 8;
-    const bool in = row < rows && h0 < a.hidden;
-    float f[8] = {};
-    if (in) load8<T, kVec>(a.x + static_cast<int64_t>(row) * a.xs, h0, a.hidden, f);
-    uint32_t lo, hi;
-    const float s = quant_block(f, lo, hi);
-    if (!in) continue;
-    char* q = a.q + static_cast<int64_t>(row) * a.qs + h0;
-    if constexpr (kVec) {
-      *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (h0 + i < a.hidden) q[i] = static_cast<char>((i < 4 ? lo >> (8 * i) : hi >> (8 * i - 32)) & 0xffu);
-    }
-    if (lane16 == 0) a.scale[static_cast<int64_t>(row) * a.ss + b] = s;
+    for (int i = 0; i < 8; ++i)
+      if (h0 + i < a.hidden) q[i] = static_cast<char>((i < 4 ? lo >> (8 * i) : hi >> (8 * i - 32)) & 0xffu);
   }
+  if (lane16 == 0) a.scale[static_cast<int64_t>(row) * a.ss + b] = s;
 }
 
 // ------------------------------------------------------------------ host side
@@ -81,11 +78,13 @@ int plan_quant_fp8(const moe_quant_fp8_desc* d) {
   if (d->dtype != FFNWB_DT_FP16 && d->dtype != FFNWB_DT_BF16 && d->dtype != FFNWB_DT_FP32) return FFNWB_ERR_PARAM_INVALID;
   if (d->hidden <= 0 || d->hidden > (int64_t{1} << 20) || d->num_rows < 0) return FFNWB_ERR_PARAM_INVALID;
   const int64_t elt = d->dtype == FFNWB_DT_FP32 ? 4 : 2, nblk = (d->hidden + kBlk - 1) / kBlk;
-  if (d->num_rows >= (int64_t{1} << 30) / nblk) return FFNWB_ERR_PARAM_INVALID;
+  // one dimension of the grid: fewer than 2^32 threads, 16 to a block of elements
+  if (d->num_rows > ((int64_t{1} << 28) - kQGroups) / nblk) return FFNWB_ERR_PARAM_INVALID;
   if (d->x_row_stride != 0 && (d->x_row_stride < d->hidden * elt || d->x_row_stride % elt != 0)) return FFNWB_ERR_PARAM_INVALID;
   if (d->q_row_stride != 0 && d->q_row_stride < d->hidden) return FFNWB_ERR_PARAM_INVALID;
   if (d->scale_row_stride != 0 && d->scale_row_stride < nblk) return FFNWB_ERR_PARAM_INVALID;
-  const int64_t far = int64_t{1} << 40;  // row * stride stays inside 64 bits
+  // row * stride * 4 bytes stays inside 64 bits
+  const int64_t far = d->num_rows > (1 << 20) ? (int64_t{1} << 60) / d->num_rows : int64_t{1} << 40;
   if (d->x_row_stride > far || d->q_row_stride > far || d->scale_row_stride > far) return FFNWB_ERR_PARAM_INVALID;
   if (reinterpret_cast<uintptr_t>(d->x) % elt != 0) return FFNWB_ERR_PARAM_INVALID;
   return FFNWB_OK;
@@ -111,11 +110,11 @@ int launch_quant_fp8(const moe_quant_fp8_desc* d, hipStream_t s) {
   a.q = static_cast<char*>(d->q);
   a.scale = d->scale;
   const int64_t units = d->num_rows * a.nblk;
-  if (units == 0) return FFNWB_OK;
-  const uint32_t grid = static_cast<uint32_t>((units + kQGroups * kQRounds - 1) / (kQGroups * kQRounds));
+  void *b = d->ev_quant_begin, *e = d->ev_quant_end;
+  if (units == 0) return record_event(b, s) && record_event(e, s) ? FFNWB_OK : FFNWB_ERR_RUNTIME;
+  const uint32_t grid = static_cast<uint32_t>((units + kQGroups - 1) / kQGroups);
   const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | static_cast<uintptr_t>(a.xs)) & 15) == 0 &&
                    ((reinterpret_cast<uintptr_t>(a.q) | static_cast<uintptr_t>(a.qs) | static_cast<uintptr_t>(a.hidden)) & 7) == 0;
-  void *b = d->ev_quant_begin, *e = d->ev_quant_end;
   const bool ok = d->dtype == FFNWB_DT_FP16   ? launch_t<TF16>(a, vec, grid, s, b, e)
                   : d->dtype == FFNWB_DT_BF16 ? launch_t<TBF16>(a, vec, grid, s, b, e)
                                               : launch_t<TF32>(a, vec, grid, s, b, e);

@@ -553,8 +553,9 @@ typedef struct moe_grouped_matmul_fp8_desc {
   void* y;                   /* [R, N] (SwiGLU: [R, F]) of out_dtype */
   float* y_scale;            /* [R, ceil(F / 128)] (FFNWB_DT_FP8_E4M3 only) */
 
-  /* Optional timing hooks (hipEvent_t) around the product's kernel, as in
-     ffnwb_batching_desc. */
+  /* Optional timing hooks (hipEvent_t): `begin` at the product's kernel, `end` at the
+     completion of the call's last kernel (the same one, unless the product is split over K or
+     quantised after it), as in ffnwb_batching_desc. */
   void* ev_matmul_begin;
   void* ev_matmul_end;
 } moe_grouped_matmul_fp8_desc;

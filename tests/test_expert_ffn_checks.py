@@ -152,7 +152,8 @@ def test_calls_on_the_cpu_do_not_run():
 
 def test_workspace_is_checked_before_any_device_work():
     for name, over in (("moe_grouped_matmul_fp8", dict(num_groups=2000)),
-                       ("moe_grouped_matmul_fp8", dict(epilogue=1, out_features=64, out_dtype=6)), ("moe_layer", {})):
+                       ("moe_grouped_matmul_fp8", dict(num_rows=520, in_features=8192, out_features=1024, epilogue=1, out_dtype=6)),
+                       ("moe_layer", {})):
         d = MAKE[name](**over)
         st, n = _ws(name, d)
         assert st == 0 and n > 0

@@ -273,6 +273,45 @@ def test_large_products(rows, k, n, dtype, epilogue, experts):
         assert untouched(whole[:, f:])
 
 
+# few tiles and a long K, which is split: parts that do not divide it, odd widths, rows behind
+SPLIT = [(128, 7168, 1000, BF16, "none", 0), (128, 7184, 1001, FP32, "none", 0), (300, 6160, 333, FP16, "none", 0),
+         (520, 4112, 1504, FP32, "swiglu", 0), (260, 8192, 1056, BF16, "swiglu", 0), (330, 8000, 800, FP8, "swiglu", 0),
+         (1000, 8192, 1056, FP8, "swiglu", 3), (260, 8000, 1000, BF16, "none", 2), (200, 12304, 600, FP32, "none", 2)]
+
+
+@pytest.mark.parametrize("rows,k,n,dtype,epilogue,experts", SPLIT)
+def test_products_split_over_k(rows, k, n, dtype, epilogue, experts):
+    c = matmul_inputs(rows + k + n, rows, k, n, max(experts, 1))
+    swiglu, f = epilogue == "swiglu", n // 2 if epilogue == "swiglu" else n
+    groups = None if experts == 0 else [(e, (rows - 9) // experts) for e in range(experts)] + [(experts, 4)]
+    out = {"y": canary((rows, f + 5), dtype)[:, :f]}
+    if dtype == FP8:
+        out["y_scale"] = canary((rows, -(-f // 128) + 1), FP32)[:, :-1]
+    call = F.GroupedMatmulFp8Call(fp8(c["x"]), dev(c["xs"]), fp8(c["w"]), dev(c["ws"]), out_dtype=dtype, out=out,
+                                  group_list=None if groups is None else dev(np.array(groups, np.int64)),
+                                  epilogue=F.FFNWB_EPI_SWIGLU if swiglu else F.FFNWB_EPI_NONE)
+    assert call.ws_bytes >= 2 * rows * n * 4, "this size is not split"
+    print(f"split product {rows} x {k} x {n} {dtype} {epilogue}, {experts} experts", flush=True)
+    call.run()
+    torch.cuda.synchronize()
+    want, off, written = matmul_reference(c, groups, epilogue, dtype in (BF16, FP16))
+    w = dev(written)
+    if dtype == FP8:
+        quantised_close(out["y"].view(torch.uint8)[w].view(FP8), out["y_scale"][w], want[written], off[written])
+        assert untouched(out["y_scale"].contiguous().view(torch.uint8)[~w])
+    else:
+        close(out["y"][w], want[written], off[written], dtype)
+    assert untouched(out["y"].contiguous().view(torch.uint8)[~w])
+    whole = out["y"]._base.view(torch.uint8).reshape(rows, -1)
+    assert untouched(whole[:, f * out["y"].element_size():])
+    first = {key: t.clone() for key, t in out.items()}
+    for _ in range(10):
+        call.run()
+    torch.cuda.synchronize()
+    for key, t in out.items():
+        assert torch.equal(first[key].view(torch.uint8), t.contiguous().view(torch.uint8))
+
+
 @pytest.mark.parametrize("rows", [5, 40, 300, 1500])
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 def test_nan_stays_in_its_rows_and_columns(rows, dtype):

@@ -109,6 +109,8 @@ def _calls(seed):
     gl = torch.tensor([[0, 40], [2, 130], [3, 1], [5, 100]], device="cuda")
     x = dev(rng.normal(size=(100, 700)).astype(np.float32), BF16)
     few = layer_inputs(seed + 2, 3, 2, 6, 128, 640)
+    lm = matmul_inputs(seed + 3, 192, 7168, 700)   # split over K
+    long = (fp8(lm["x"]), dev(lm["xs"]), fp8(lm["w"]), dev(lm["ws"]))
 
     def layer(c):
         return F.LayerCall(dev(c["x"], BF16), dev(c["ids"]), fp8(c["w13"]), fp8(c["w2"]), w13_scale=dev(c["w13s"]),
@@ -120,7 +122,7 @@ def _calls(seed):
             F.GroupedMatmulFp8Call(*args, group_list=gl, epilogue=F.FFNWB_EPI_SWIGLU, out_dtype=FP8,
                                    out={"y": canary((300, 144), FP8), "y_scale": canary((300, 2), FP32)}),
             F.GroupedMatmulFp8Call(*args, group_list=gl, out={"y": canary((300, 288), BF16)}),
-            layer(lc), layer(few)]
+            F.GroupedMatmulFp8Call(*long, out={"y": canary((192, 700), BF16)}), layer(lc), layer(few)]
 
 
 def _outputs(calls):
@@ -142,7 +144,7 @@ def test_calls_on_streams_at_once():
     again = _calls(91)
     streams = [torch.cuda.Stream() for _ in again]
     torch.cuda.synchronize()
-    print("five calls on five streams", flush=True)
+    print("six calls on six streams", flush=True)
     for _ in range(5):
         for c, s in zip(again, streams):
             c.run(s)

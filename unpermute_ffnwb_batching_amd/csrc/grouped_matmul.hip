@@ -15,6 +15,8 @@ struct MmArgs {
   int32_t rows;
   int32_t kb, nb;              // 128-blocks along K and N
   int32_t ntiles;              // column tiles
+  int32_t parts, part_blocks;  // parts of K, each a workgroup's, and 128-blocks of a part
+  int64_t part_bytes;          // between the results of two parts
   int32_t ngroups, nexperts;
   bool vec;                    // four adjacent outputs are one aligned store
   int32_t unit;                // rows of y are whole aligned units of 16 or 4 bytes, or elements (0)
@@ -314,41 +316,65 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm_direct_kernel(MmArgs 
 
 namespace ffnwb {
 
-// ------------------------------------------------------------------ quantising a product
+// ------------------------------------------------------------------ joining a product
 //
-// For the products whose column tiles are narrower than a block: SwiGLU results h [R, F] in
-// FP32 to e4m3 rows.  16 lanes take a block, as in moe_quant_fp8; a workgroup takes 16 blocks of
-// a row tile, so that rows of no expert stay as they were.
+// For products whose tiles do not hold whole results: those split over K (FP32 sums [parts][R][N
+// rounded up to 8]), and SwiGLU results of the direct kernel (FP32 h [R][F]) on their way to e4m3 rows,
+// whose blocks are wider than its column tiles.  16 lanes take 128 outputs of a row, as in
+// moe_quant_fp8; a workgroup takes 16 such blocks of a row tile, so that rows of no expert stay as
+// they were.  The parts are added in order: the same bits on every run.
 
-constexpr int kMqThreads = 256;
+constexpr int kJoinThreads = 256;
 
-__global__ __launch_bounds__(kMqThreads) void mm_quant_kernel(MmArgs a, const float* h, int32_t bm) {
+template <class T, bool kSwiglu, bool kQuant>
+__global__ __launch_bounds__(kJoinThreads) void mm_join_kernel(MmArgs a, const float* sums, int64_t pitch, int32_t parts, int32_t bm) {
   const int32_t fb = static_cast<int32_t>((a.F + kBlk - 1) / kBlk);
   RowTile rt;
-  int32_t part;
-  if (!find_tile(a, bm, rt, part)) return;
-  const int32_t u = part * (kMqThreads / 16) + threadIdx.x / 16;
+  int32_t group;
+  if (!find_tile(a, bm, rt, group)) return;
+  const int32_t u = group * (kJoinThreads / 16) + threadIdx.x / 16;
   const int32_t i = u / fb, b = u - i * fb;
   const int64_t row = rt.row0 + i, f0 = static_cast<int64_t>(b) * kBlk + threadIdx.x % 16 * 8;
-  const bool in = i < rt.rows && f0 < a.F;  // F is a multiple of 16
-  float f[8] = {};
-  if (in) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(h + row * a.F + f0);
-    const f32x4 v0 = p[0], v1 = p[1];
+  const bool in = i < rt.rows && f0 < a.F;
+  auto sum = [&](int64_t n, float (&f)[8]) {  // columns n .. n + 7
+    const float* p = sums + row * pitch + n;
+    f32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int32_t s = 0; s < parts; ++s, p += a.rows * pitch) {
+      v0 += reinterpret_cast<const f32x4*>(p)[0];
+      v1 += reinterpret_cast<const f32x4*>(p)[1];
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = v0[j], f[4 + j] = v1[j];
-  }
-  uint32_t lo, hi;
-  const float s = quant_block(f, lo, hi);
-  if (!in) return;
-  char* q = a.y + row * a.ys + f0;
-  if (((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.ys)) & 7) == 0) {
-    *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
-  } else {
+  };
+  float f[8] = {};
+  if (in) {
+    sum(f0, f);
+    if constexpr (kSwiglu) {
+      float up[8];
+      sum(a.F + f0, up);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = static_cast<char>((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
+      for (int j = 0; j < 8; ++j) f[j] = swiglu(f[j], up[j]);
+    }
   }
-  if (threadIdx.x % 16 == 0) a.y_scale[row * a.yss + b] = s;
+  if constexpr (kQuant) {  // F is a multiple of 16
+    uint32_t lo, hi;
+    const float s = quant_block(f, lo, hi);
+    if (!in) return;
+    char* q = a.y + row * a.ys + f0;
+    if (((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(a.ys)) & 7) == 0) {
+      *reinterpret_cast<u32x2*>(q) = u32x2{lo, hi};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = static_cast<char>((j < 4 ? lo >> (8 * j) : hi >> (8 * j - 32)) & 0xffu);
+    }
+    if (threadIdx.x % 16 == 0) a.y_scale[row * a.yss + b] = s;
+  } else {
+    if (!in) return;
+    char* y = a.y + row * a.ys;
+    store4<T>(y, f0, a.F, f32x4{f[0], f[1], f[2], f[3]}, a.vec);
+    store4<T>(y, f0 + 4, a.F, f32x4{f[4], f[5], f[6], f[7]}, a.vec);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -367,30 +393,31 @@ static int direct_waves(int64_t tiles, int64_t kb, int64_t bm) {
 
 // Microseconds that a product takes with the given kernel and tile rows: rounds of workgroups
 // that fit the chip together, times what one needs for its blocks of K; the figures (us per
-// block and round) are measured.  A group's last tile is counted as 0.7 of one.
+// block and round) are measured.  A group's last tile is counted as 0.57 of one.
 static double expected_us(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t groups, bool swiglu, bool quant, bool fast,
-                          bool tile, int64_t bm) {
+                          bool tile, int64_t bm, int64_t parts) {
   const int64_t kb = (K + 127) / 128, some = groups < rows ? groups : rows;
-  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.7 * some : static_cast<double>((rows + bm - 1) / bm);
+  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.57 * some : static_cast<double>((rows + bm - 1) / bm);
   auto rounds = [](double wgs, int64_t together) { return wgs <= together ? 1.0 : __builtin_ceil(wgs / together); };
   if (tile) {
-    const double tiles = mt * ((F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
-    double us = fast ? (bm == 256 ? 2.3 : bm == 128 ? 1.3 : 0.93) : (bm == 128 ? 2.15 : 1.35);
+    const double tiles = parts > 1 ? mt * ((N + 255) / 256) * parts : mt * ((F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
+    const double join = parts > 1 ? 3.7 + parts * rows * N * 8 / 5700e3 : 0.0;  // a launch, sums written and read
+    double us = fast ? (bm == 256 ? 1.8 : bm == 128 ? 1.36 : 0.93) : (bm == 128 ? 1.82 : 1.31);
     int64_t together = kCus;
     if (bm == 32) {  // two to a CU
-      us = fast ? (tiles > kCus ? 1.0 : 0.72) : (tiles > kCus ? 1.8 : 1.3);
+      us = fast ? (tiles > kCus ? 1.28 : 0.69) : (tiles > kCus ? 1.82 : 0.88);
       together = 2 * kCus;
     }
-    return 3.0 + rounds(tiles, together) * (kb * us + 2.8);
+    return 4.0 + rounds(tiles, together) * ((kb + parts - 1) / parts * us + 2.3) + join;
   }
   const int64_t nt = (F + 15) / 16;
   const int waves = direct_waves(((rows + bm - 1) / bm + some) * nt, kb, bm);
   // waves of a CU by the kernels' registers
   const int fit = bm == 16 ? (swiglu ? 20 : 28) : bm == 32 ? (swiglu ? 12 : 20) : (swiglu ? 8 : 12);
-  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 2.0 : 1.3) * (bm == 64 ? 1.3 : 1.0);
-  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus : kCus) * ((kb + waves - 1) / waves * us + 0.7);
-  const double weights = mt * N * K / 9000e3;  // read again for every row tile, from L2
-  return 3.0 + (work > weights ? work : weights) + (quant ? 3.0 : 0.0);
+  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 1.85 : 1.33) * (bm == 64 ? 1.63 : bm == 32 ? 1.18 : 1.0);
+  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus : kCus) * ((kb + waves - 1) / waves * us + 0.6);
+  const double weights = mt * N * K / 5250e3;  // read again for every row tile, from L2
+  return 4.0 + (work > weights ? work : weights) + (quant ? 2.3 : 0.0);
 }
 
 int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
@@ -429,31 +456,45 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t groups = d->group_list != nullptr ? d->num_groups : 1;
   const bool fast = !quant && d->out_dtype != FFNWB_DT_FP32;
-  auto shape = [&](bool tile, int64_t bm) {
-    p->tile = tile, p->bm = bm;
-    p->mtiles = (p->R + bm - 1) / bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
-    p->ntiles = tile ? (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256) : (p->F + 15) / 16;
-    return p->mtiles * p->ntiles;
+  auto shape = [&](int64_t bm, int64_t parts) {  // negative bm: direct; the result: workgroups, of the larger launch
+    p->tile = bm > 0, p->bm = bm > 0 ? bm : -bm;
+    p->part_blocks = (p->kb + parts - 1) / parts;
+    p->parts = (p->kb + p->part_blocks - 1) / p->part_blocks;
+    p->mtiles = (p->R + p->bm - 1) / p->bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
+    p->ntiles = !p->tile ? (p->F + 15) / 16 : p->parts > 1 ? (p->N + 255) / 256 * p->parts : (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+    p->join = p->parts > 1 || (quant && !p->tile);
+    p->join_groups = (p->bm * fb + kJoinThreads / 16 - 1) / (kJoinThreads / 16);
+    return p->mtiles * (p->join && p->join_groups > p->ntiles ? p->join_groups : p->ntiles);
   };
-  auto quant_parts = [&](int64_t bm) { return (bm * fb + kMqThreads / 16 - 1) / (kMqThreads / 16); };
-  // The kernel and the rows of its tiles: the least of the times expected.  Over 400 random sizes
-  // (1 to 65536 rows, K and N to 8192, 0 to 256 groups) the choice is 3% slower than the best of
-  // the shapes on average; a fixed rule (the largest tile that the groups fill and that gives
-  // every CU one) was 15%.  256 rows of x, and the gate rows of w, have to be inside the 32-bit
-  // offsets of the tile kernel.
+  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  Over
+  // 420 random sizes (1 to 16384 rows, K and N to 8192, 0 to 256 groups) the choice is 1.5% slower
+  // than the best of the shapes on average; a fixed rule (the largest tile that the groups fill
+  // and that gives every CU one) was 15%.  Parts are what fills the chip with a long K and few tiles:
+  // 256 rows by 2048 columns over 7168 take 39.9 us in the best shape without and 17.7 us in 8 parts,
+  // 128 by 8192 over 8192 45.5 and 24.3 us; with 1536 columns over 1536 they cost 0.2 to 3 us.  256 rows of x, and the gate rows of w, have to be
+  // inside the 32-bit offsets of the tile kernel.
   const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
   const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup
   double best = 0;
-  int64_t best_bm = 0;
-  for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {  // negative: direct
+  int64_t best_bm = 0, best_parts = 1;
+  auto consider = [&](int64_t bm, int64_t parts) {
+    if (shape(bm, parts) > most) return;
+    const double t = expected_us(p->R, p->N, p->K, p->F, d->num_groups, swiglu, quant, fast, p->tile, p->bm, p->parts);
+    if (best_bm == 0 || t < best) best = t, best_bm = bm, best_parts = p->parts;
+  };
+  for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {
     if (bm > 0 && (!near || (bm == 256 && !fast))) continue;
-    if (shape(bm > 0, bm > 0 ? bm : -bm) > most || (quant && bm < 0 && p->mtiles * quant_parts(p->bm) > most)) continue;
-    const double t = expected_us(p->R, p->N, p->K, p->F, d->num_groups, swiglu, quant, fast, bm > 0, bm > 0 ? bm : -bm);
-    if (best_bm == 0 || t < best) best = t, best_bm = bm;
+    consider(bm, 1);
+    if (bm < 0 || bm == 256) continue;
+    // parts that fill the chip once, or half of it
+    const int64_t last = d->num_groups < p->R ? d->num_groups : p->R, tiles = ((p->R + bm - 1) / bm + last * 6 / 10) * ((p->N + 255) / 256);
+    const int64_t fill = (bm == 32 ? 2 : 1) * kCus / (tiles > 0 ? tiles : 1);
+    for (const int64_t parts : {fill, fill / 2})
+      if (parts > 1) consider(bm, parts < p->kb / 2 ? parts : p->kb / 2 > 1 ? p->kb / 2 : 1);
   }
   if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
-  shape(best_bm > 0, best_bm > 0 ? best_bm : -best_bm);
-  p->quant_parts = quant_parts(p->bm);
+  shape(best_bm, best_parts);
+  p->pitch = p->parts > 1 ? (p->N + 7) / 8 * 8 : p->F;
   p->ws_bytes = 0;
   Carve c;
   // The list in every workgroup costs each about 1 us, two to a CU at a time; the launch 4 us.
@@ -462,7 +503,7 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     c.take<int32_t>(1);
     c.take<int4>(static_cast<size_t>(p->mtiles));
   }
-  if (quant && !p->tile) c.take<float>(static_cast<size_t>(p->R * p->F));
+  if (p->join) c.take<float>(static_cast<size_t>(p->parts * p->R * p->pitch));
   p->ws_bytes = c.off;
   return FFNWB_OK;
 }
@@ -494,10 +535,9 @@ static bool launch_tile_shape(const MmArgs& a, const MatmulPlan& p, hipStream_t 
   return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles)), dim3(S::kThreads), S::kLds, s, b, e, a);
 }
 
-template <class T, int EPI, bool kQuant = false>
+template <class T, int EPI, bool kQuant = false, bool kFast = !kQuant && T::kBytes == 2>
 static bool launch_tile(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
-  constexpr bool kFast = !kQuant && T::kBytes == 2;
-  if constexpr (kFast) {
+  if constexpr (T::kBytes == 2) {
     if (p.bm == 256) return launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 8>(a, p, s, b, e);
   }
   return p.bm == 128  ? launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 4>(a, p, s, b, e)
@@ -507,11 +547,10 @@ static bool launch_tile(const MmArgs& a, const MatmulPlan& p, hipStream_t s, voi
 
 int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan& p, void* ws, hipStream_t s) {
   if (p.R == 0) return record_event(d->ev_matmul_begin, s) && record_event(d->ev_matmul_end, s) ? FFNWB_OK : FFNWB_ERR_RUNTIME;
-  const bool quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
   MmArgs a{};
   a.rows = static_cast<int32_t>(p.R), a.K = p.K, a.N = p.N, a.F = p.F;
   a.xs = p.xs, a.xss = p.xss, a.ys = p.ys, a.yss = p.yss;
-  a.kb = static_cast<int32_t>(p.kb), a.nb = static_cast<int32_t>(p.nb), a.ntiles = static_cast<int32_t>(p.ntiles);
+  a.kb = static_cast<int32_t>(p.kb), a.nb = static_cast<int32_t>(p.nb);
   a.ngroups = static_cast<int32_t>(d->num_groups), a.nexperts = static_cast<int32_t>(d->num_experts);
   a.groups = d->group_list;
   a.x = static_cast<const char*>(d->x), a.x_scale = d->x_scale;
@@ -526,46 +565,66 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
     if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
     a.table = table, a.count = count;
   }
-  const int64_t quad = 4 * out_size(d->out_dtype);
-  a.vec = ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(p.ys)) & (quad - 1)) == 0;
-  const uint64_t all = reinterpret_cast<uintptr_t>(a.y) | static_cast<uint64_t>(p.ys) | static_cast<uint64_t>(p.F * (quad / 4));
-  a.unit = (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 0;
   void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
-  if (p.tile) {
-    bool ok;
-    if (d->epilogue == FFNWB_EPI_SWIGLU) {
-      ok = quant                           ? launch_tile<TF32, FFNWB_EPI_SWIGLU, true>(a, p, s, b, e)
-           : d->out_dtype == FFNWB_DT_FP16 ? launch_tile<TF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
-           : d->out_dtype == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
-                                           : launch_tile<TF32, FFNWB_EPI_SWIGLU>(a, p, s, b, e);
-    } else {
-      ok = d->out_dtype == FFNWB_DT_FP16   ? launch_tile<TF16, FFNWB_EPI_NONE>(a, p, s, b, e)
-           : d->out_dtype == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_NONE>(a, p, s, b, e)
-                                           : launch_tile<TF32, FFNWB_EPI_NONE>(a, p, s, b, e);
-    }
-    return ok ? FFNWB_OK : FFNWB_ERR_RUNTIME;
-  }
-  float* h = quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
-  if (quant) a.y = reinterpret_cast<char*>(h), a.ys = p.F * 4, a.vec = true;
-  bool ok;
-  if (d->epilogue == FFNWB_EPI_SWIGLU) {
-    ok = d->out_dtype == FFNWB_DT_FP16   ? launch_direct<TF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
-         : d->out_dtype == FFNWB_DT_BF16 ? launch_direct<TBF16, FFNWB_EPI_SWIGLU>(a, p, s, b, e)
-                                         : launch_direct<TF32, FFNWB_EPI_SWIGLU>(a, p, s, b, e);
+  // the product: results, or sums for the join
+  const int32_t dt = p.join ? static_cast<int32_t>(FFNWB_DT_FP32) : d->out_dtype;
+  MmArgs m = a;
+  m.ntiles = static_cast<int32_t>(p.ntiles);
+  m.parts = static_cast<int32_t>(p.parts), m.part_blocks = static_cast<int32_t>(p.part_blocks), m.part_bytes = p.R * p.pitch * 4;
+  float* sums = nullptr;
+  if (p.join) {
+    sums = c.take<float>(static_cast<size_t>(p.parts * p.R * p.pitch));
+    m.y = reinterpret_cast<char*>(sums), m.ys = p.pitch * 4;
+    m.vec = true, m.unit = 16;  // the units of a row's end may run into the rest of its pitch
+    if (p.parts > 1) m.F = p.N;
   } else {
-    ok = d->out_dtype == FFNWB_DT_FP16   ? launch_direct<TF16, FFNWB_EPI_NONE>(a, p, s, b, e)
-         : d->out_dtype == FFNWB_DT_BF16 ? launch_direct<TBF16, FFNWB_EPI_NONE>(a, p, s, b, e)
-                                         : launch_direct<TF32, FFNWB_EPI_NONE>(a, p, s, b, e);
+    const uint64_t at = reinterpret_cast<uintptr_t>(a.y) | static_cast<uint64_t>(p.ys), elt = static_cast<uint64_t>(out_size(dt));
+    m.vec = (at & (4 * elt - 1)) == 0;
+    m.unit = ((at | p.F * elt) & 15) == 0 ? 16 : ((at | p.F * elt) & 3) == 0 ? 4 : 0;
   }
-  if (!ok) return FFNWB_ERR_RUNTIME;
-  if (quant) {
-    a.y = static_cast<char*>(d->y), a.ys = p.ys;
-    a.ntiles = static_cast<int32_t>(p.quant_parts);
-    hipLaunchKernelGGL(mm_quant_kernel, dim3(tile_grid(p.mtiles * p.quant_parts)), dim3(kMqThreads), 0, s, a, h,
-                       static_cast<int32_t>(p.bm));
-    if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
+  void* product_end = p.join ? nullptr : e;
+  const bool swiglu = d->epilogue == FFNWB_EPI_SWIGLU, quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
+  bool ok;
+  if (p.parts > 1) {
+    ok = out_size(d->out_dtype) == 2 ? launch_tile<TF32, FFNWB_EPI_NONE, false, true>(m, p, s, b, product_end)
+                                     : launch_tile<TF32, FFNWB_EPI_NONE>(m, p, s, b, product_end);
+  } else if (p.tile && swiglu) {
+    ok = quant                ? launch_tile<TF32, FFNWB_EPI_SWIGLU, true>(m, p, s, b, e)
+         : dt == FFNWB_DT_FP16 ? launch_tile<TF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)
+         : dt == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)
+                               : launch_tile<TF32, FFNWB_EPI_SWIGLU>(m, p, s, b, e);
+  } else if (p.tile) {
+    ok = dt == FFNWB_DT_FP16   ? launch_tile<TF16, FFNWB_EPI_NONE>(m, p, s, b, e)
+         : dt == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_NONE>(m, p, s, b, e)
+                               : launch_tile<TF32, FFNWB_EPI_NONE>(m, p, s, b, e);
+  } else if (swiglu) {
+    ok = dt == FFNWB_DT_FP16   ? launch_direct<TF16, FFNWB_EPI_SWIGLU>(m, p, s, b, product_end)
+         : dt == FFNWB_DT_BF16 ? launch_direct<TBF16, FFNWB_EPI_SWIGLU>(m, p, s, b, product_end)
+                               : launch_direct<TF32, FFNWB_EPI_SWIGLU>(m, p, s, b, product_end);
+  } else {
+    ok = dt == FFNWB_DT_FP16   ? launch_direct<TF16, FFNWB_EPI_NONE>(m, p, s, b, e)
+         : dt == FFNWB_DT_BF16 ? launch_direct<TBF16, FFNWB_EPI_NONE>(m, p, s, b, e)
+                               : launch_direct<TF32, FFNWB_EPI_NONE>(m, p, s, b, e);
   }
-  return FFNWB_OK;
+  if (ok && p.join) {
+    a.ntiles = static_cast<int32_t>(p.join_groups);
+    const int64_t quad = 4 * out_size(d->out_dtype);
+    a.vec = ((reinterpret_cast<uintptr_t>(a.y) | static_cast<uintptr_t>(p.ys)) & (quad - 1)) == 0;
+    const int64_t pitch = p.pitch;
+    const int32_t parts = m.parts, bm = static_cast<int32_t>(p.bm);
+    auto join = [&](auto kernel) {
+      return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.join_groups)), dim3(kJoinThreads), 0, s, nullptr, e, a, sums, pitch, parts, bm);
+    };
+    ok = quant && p.parts == 1                     ? join(mm_join_kernel<TF32, false, true>)
+         : quant                                   ? join(mm_join_kernel<TF32, true, true>)
+         : swiglu && d->out_dtype == FFNWB_DT_FP16 ? join(mm_join_kernel<TF16, true, false>)
+         : swiglu && d->out_dtype == FFNWB_DT_BF16 ? join(mm_join_kernel<TBF16, true, false>)
+         : swiglu                                  ? join(mm_join_kernel<TF32, true, false>)
+         : d->out_dtype == FFNWB_DT_FP16           ? join(mm_join_kernel<TF16, false, false>)
+         : d->out_dtype == FFNWB_DT_BF16           ? join(mm_join_kernel<TBF16, false, false>)
+                                                   : join(mm_join_kernel<TF32, false, false>);
+  }
+  return ok ? FFNWB_OK : FFNWB_ERR_RUNTIME;
 }
 
 }  // namespace ffnwb

@@ -131,8 +131,11 @@ struct MatmulPlan {
   int64_t xs = 0, xss = 0, ys = 0, yss = 0;    // row strides: bytes, elements, bytes, elements
   bool tile = false;                           // through LDS, else straight to registers
   int64_t bm = 0;                              // rows of a tile
-  int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles
-  int64_t quant_parts = 0;                     // workgroups that quantise a row tile
+  int64_t parts = 1, part_blocks = 0;          // parts of K, and 128-blocks of each
+  int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles (times the parts)
+  bool join = false;                           // FP32 sums, joined by a launch of its own
+  int64_t pitch = 0;                           // elements of a row of sums
+  int64_t join_groups = 0;                     // workgroups that join a row tile
   bool table = false;                          // row tiles listed by a launch of their own
   size_t ws_bytes = 0;
 };

@@ -92,6 +92,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
   RowTile rt;
   int32_t c;
   if (!find_tile(a, S::kBM, rt, c)) return;
+  // this workgroup's part of K: kb blocks from block k0 on, all of them unless the product is split
+  const int32_t part = c % a.parts, k0 = part * a.part_blocks, kb = min(a.kb - k0, a.part_blocks);
+  c /= a.parts;
   const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), r = lane % 16, g = lane / 16;
   const int32_t wm = wave / WN, wn = wave % WN;
   const int64_t c0 = static_cast<int64_t>(c) * (kSwiglu ? 128 : 256);  // first output column
@@ -108,8 +111,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
   // Copy j of a wave takes 8 rows, one chunk per lane: 32-bit offsets from the tile's first rows
   // (256 rows of x, and of w as far as the up columns, are below 2^32 bytes in this kernel).
   const int64_t w0 = weight_row(0);
-  const Buffer xbuf = make_buffer(a.x + rt.row0 * a.xs, (rt.rows - 1) * a.xs + a.K);
-  const Buffer wbuf = make_buffer(a.w + (static_cast<int64_t>(rt.expert) * a.N + w0) * a.K, (a.N - w0) * a.K);
+  const int64_t kfirst = static_cast<int64_t>(k0) * kBlk;
+  const Buffer xbuf = make_buffer(a.x + rt.row0 * a.xs + kfirst, (rt.rows - 1) * a.xs + a.K - kfirst);
+  const Buffer wbuf = make_buffer(a.w + (static_cast<int64_t>(rt.expert) * a.N + w0) * a.K + kfirst, (a.N - w0) * a.K - kfirst);
   const uint32_t chunk = ((lane % 8) ^ (lane / 8)) * 16;
   uint32_t xsrc[S::kXCopies], wsrc[S::kWCopies];
 #pragma unroll
@@ -130,10 +134,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
     for (int j = 0; j < S::kWCopies; ++j) copy16_to_lds(wbuf, wsrc[j], b * kBlk, to + (j * WM * WN + wave) * 1024);
   };
   // A short last block: the chunks past K (of the next row, or not there) become zeros.
-  const int32_t full = static_cast<int32_t>(a.K % kBlk) / 16;
+  const int32_t full = k0 + kb == a.kb ? static_cast<int32_t>(a.K % kBlk) / 16 : 0;
   auto clear_tail = [&] {
-    char* xb = lds + ((a.kb - 1) & 1) * S::kBM * kBlk;
-    char* wb = lds + 2 * S::kBM * kBlk + ((a.kb - 1) & 1) * 256 * kBlk;
+    char* xb = lds + ((kb - 1) & 1) * S::kBM * kBlk;
+    char* wb = lds + 2 * S::kBM * kBlk + ((kb - 1) & 1) * 256 * kBlk;
     for (int32_t i = threadIdx.x; i < S::kRows * (8 - full); i += S::kThreads) {
       const int32_t row = i / (8 - full), ch = full + i % (8 - full);
       char* at = row < S::kBM ? xb + row * kBlk : wb + (row - S::kBM) * kBlk;
@@ -149,11 +153,11 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
 #pragma unroll
   for (int j = 0; j < S::kScaleLoads; ++j) {
     const int32_t i = (j * S::kThreads + static_cast<int32_t>(threadIdx.x)) / S::kScaleRuns;
-    scp[j] = i < S::kBM ? a.x_scale + (rt.row0 + min(i, rt.rows - 1)) * a.xss
-                        : a.w_scale + (static_cast<int64_t>(rt.expert) * a.nb + weight_row(min(i - S::kBM, 15) * 16) / kBlk) * a.kb;
+    scp[j] = i < S::kBM ? a.x_scale + (rt.row0 + min(i, rt.rows - 1)) * a.xss + k0
+                        : a.w_scale + k0 + (static_cast<int64_t>(rt.expert) * a.nb + weight_row(min(i - S::kBM, 15) * 16) / kBlk) * a.kb;
   }
   auto scales_load = [&](int32_t b0) {
-    const int32_t b = min(b0 + static_cast<int32_t>(threadIdx.x) % S::kScaleRuns, a.kb - 1);
+    const int32_t b = min(b0 + static_cast<int32_t>(threadIdx.x) % S::kScaleRuns, kb - 1);
 #pragma unroll
     for (int j = 0; j < S::kScaleLoads; ++j) scr[j] = scp[j][b];
   };
@@ -170,17 +174,17 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
   fetch_w(0);
   scales_load(0);
   scales_store(0);
-  if (a.kb > 1) fetch_w(1);
-  copies_done<S::kWCopies>(a.kb > 1);
+  if (kb > 1) fetch_w(1);
+  copies_done<S::kWCopies>(kb > 1);
 
   // Step b: x of block b + 1 is fetched from its start; the waves take their fragments of w into
   // registers, which frees that buffer for block b + 2.  So w has two steps to arrive and x one.
   f32x4 tot[MF][NF] = {};
-  for (int32_t b = 0; b < a.kb; ++b) {
+  for (int32_t b = 0; b < kb; ++b) {
     const int32_t turn = b % S::kScaleRuns, next = b - turn + S::kScaleRuns;
-    if (turn == S::kScaleRuns - 2 && next < a.kb) scales_store(next);
-    if (turn == 0 && next < a.kb) scales_load(next);
-    if (b + 1 < a.kb) fetch_x(b + 1);
+    if (turn == S::kScaleRuns - 2 && next < kb) scales_store(next);
+    if (turn == 0 && next < kb) scales_load(next);
+    if (b + 1 < kb) fetch_x(b + 1);
     else if (full != 0) clear_tail();
     const char* xb = lds + (b & 1) * S::kBM * kBlk;
     const char* wb = lds + 2 * S::kBM * kBlk + (b & 1) * 256 * kBlk;
@@ -207,7 +211,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
 #pragma unroll
     for (int i = 0; i < MF; ++i) xs[i] = scb[(wm * MF + i) * 16 + r];
     if constexpr (MF > 1) read_x(1);
-    if (b + 2 < a.kb) {
+    if (b + 2 < kb) {
       lds_barrier();  // every wave has its fragments of w
       fetch_w(b + 2);
     }
@@ -259,7 +263,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
     scale(MF - 1);
-    copies_done<S::kWCopies>(b + 2 < a.kb);
+    copies_done<S::kWCopies>(b + 2 < kb);
   }
 
   // Results go through LDS, so that memory sees whole lines: a matrix result is 16 rows by 4
@@ -310,9 +314,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
   constexpr int kPartRows = S::kBM / kParts;
   static_assert(kParts == 1 || WM == 2, "a part is the rows of some of the waves");
 #pragma unroll
-  for (int part = 0; part < kParts; ++part) {
-    if (part > 0) __syncthreads();
-    if (kParts == 1 || wm == part) {
+  for (int half = 0; half < kParts; ++half) {
+    if (half > 0) __syncthreads();
+    if (kParts == 1 || wm == half) {
 #pragma unroll
       for (int i = 0; i < MF; ++i) {
         const int32_t row = ((kParts == 1 ? wm * MF : 0) + i) * 16 + r;
@@ -335,9 +339,9 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
       }
     }
     __syncthreads();
-    const int32_t rows = min(rt.rows - part * kPartRows, kPartRows);
+    const int32_t rows = min(rt.rows - half * kPartRows, kPartRows);
     const int32_t bytes = static_cast<int32_t>(min(limit - c0, int64_t{kCols})) * kElt;  // of a row
-    char* y = a.y + (rt.row0 + part * kPartRows) * a.ys + c0 * kElt;
+    char* y = a.y + part * a.part_bytes + (rt.row0 + half * kPartRows) * a.ys + c0 * kElt;
     if (a.unit == 16) copy_out<16, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
     else if (a.unit == 4) copy_out<4, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
     else copy_out<kElt, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);

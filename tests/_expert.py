@@ -32,8 +32,8 @@ def product_error(k):
 
 
 def dropped_bits(x, xs, w, ws):
-    """[R, N]: what the e4m3 matrix instructions may drop, for values x [R, K] and one expert's w [N, K]."""
-    a, b = np.abs(O.widen_rows(x, xs)), np.abs(O.widen_weights(w, ws))
+    """[R, N]: what the e4m3 matrix instructions may drop, for codes x [R, K] and one expert's w [N, K]."""
+    a, b = np.abs(O.widen_rows(O.e4m3_values(x), xs)), np.abs(O.widen_weights(O.e4m3_values(w), ws))
     k = a.shape[1] // 8
     b = np.nan_to_num(b).reshape(b.shape[0], k, 8).astype(np.float32)
     rows = [(np.nan_to_num(r).reshape(1, k, 8).astype(np.float32) * b).max(2).sum(1) for r in a]

@@ -244,6 +244,9 @@ def _sampled(c, groups, picks, epilogue, narrow):
 LARGE = [
     (1100, 272, 8208, BF16, "none", 1), (2304, 400, 1001, BF16, "none", 3), (2304, 400, 1001, FP32, "none", 3),
     (5000, 144, 4128, FP16, "swiglu", 7), (5000, 144, 4128, FP32, "swiglu", 7), (5000, 144, 4128, FP8, "swiglu", 7),
+    # a last round of tiles that is at most half full, whose tiles are halved
+    (3000, 2048, 7168, BF16, "none", 1), (5000, 1040, 4096, FP32, "none", 1), (6100, 528, 4128, FP8, "swiglu", 5),
+    (20000, 272, 1024, FP16, "none", 8),
     (40000, 128, 4096, BF16, "none", 32), (40000, 128, 8192, FP8, "swiglu", 32), (30000, 16, 8191, FP32, "none", 40),
 ]
 
@@ -262,7 +265,7 @@ def test_large_products(rows, k, n, dtype, epilogue, experts):
     got = F.moe_grouped_matmul_fp8(fp8(c["x"]), dev(c["xs"]), fp8(c["w"]), dev(c["ws"]), out_dtype=dtype, out=out,
                                    group_list=dev(np.array(groups, np.int64)), epilogue=F.FFNWB_EPI_SWIGLU if swiglu else F.FFNWB_EPI_NONE)
     torch.cuda.synchronize()
-    picks = np.unique(np.concatenate([[0, rows - 1], cut[:4], rng.integers(0, rows, 20)]))
+    picks = np.unique(np.concatenate([[0, rows - 1], cut[:4], rng.integers(0, rows, 20), np.arange(rows - 390, rows, 13)]))
     want, off = _sampled(c, groups, picks, epilogue, dtype in (BF16, FP16))
     at = torch.from_numpy(picks).cuda()
     if dtype == FP8:

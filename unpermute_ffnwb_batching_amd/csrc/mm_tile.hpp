@@ -82,16 +82,11 @@ __device__ __forceinline__ void copy_out(const char* lds, char* y, int64_t strid
 
 // kFast: e4m3 matrix instructions; else the operands are widened to BF16 (see fp8_block.hpp).
 template <class T, int EPI, bool kQuant, bool kFast, int WM, int WN, int MF>
-__global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
+__device__ __forceinline__ void mm_tile(const MmArgs& a, const RowTile& rt, int32_t c, char* lds) {
   using S = TileShape<WM, WN, MF>;
   constexpr bool kSwiglu = EPI == FFNWB_EPI_SWIGLU;
   constexpr int NF = S::kNF;
-  extern __shared__ __align__(16) char lds[];
   float* xsl = reinterpret_cast<float*>(lds + 2 * S::kRows * kBlk);  // [2][kScaleRuns][kScales]
-
-  RowTile rt;
-  int32_t c;
-  if (!find_tile(a, S::kBM, rt, c)) return;
   // this workgroup's part of K: kb blocks from block k0 on, all of them unless the product is split
   const int32_t part = c % a.parts, k0 = part * a.part_blocks, kb = min(a.kb - k0, a.part_blocks);
   c /= a.parts;
@@ -346,6 +341,24 @@ __global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
     else if (a.unit == 4) copy_out<4, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
     else copy_out<kElt, kPitch, S::kThreads>(lds, y, a.ys, rows, bytes);
   }
+}
+
+// Tiles of at most half the rows (the last one of a group, the halves of find_tile) take half the
+// fragments.
+template <class T, int EPI, bool kQuant, bool kFast, int WM, int WN, int MF>
+__global__ __launch_bounds__(WM* WN* kWave) void mm_tile_kernel(MmArgs a) {
+  extern __shared__ __align__(16) char lds[];
+  constexpr int kBM = TileShape<WM, WN, MF>::kBM;
+  RowTile rt;
+  int32_t c;
+  if (!find_tile<(MF >= kHalvedFragments)>(a, kBM, rt, c)) return;
+  if constexpr (MF >= kHalvedFragments) {
+    if (rt.rows <= kBM / 2) {
+      mm_tile<T, EPI, kQuant, kFast, WM, WN, MF / 2>(a, rt, c, lds);
+      return;
+    }
+  }
+  mm_tile<T, EPI, kQuant, kFast, WM, WN, MF>(a, rt, c, lds);
 }
 
 }  // namespace ffnwb

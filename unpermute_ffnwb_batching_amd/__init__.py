@@ -811,7 +811,8 @@ def _row_bytes(t):
 
 
 class _Call:
-    """A descriptor with its outputs and workspace, launched on the tensors' own device."""
+    """A descriptor with its outputs and workspace, launched on the tensors' own device.  Runs of
+    one call share both, so runs that may overlap (on two streams, in two graphs) need a call each."""
 
     def _bind(self, name, desc, device, out, keep, workspace, ws_bytes):
         if workspace is None and ws_bytes:

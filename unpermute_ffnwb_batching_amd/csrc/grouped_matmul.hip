@@ -405,46 +405,42 @@ constexpr int64_t kCus = 256;
 
 static int64_t out_size(int32_t dt) { return dt == FFNWB_DT_FP32 ? 4 : dt == FFNWB_DT_FP8_E4M3 ? 1 : 2; }
 
-// Waves of a direct workgroup: at least one block of K each, two where there are enough
-// workgroups to fill the chip.
+// Waves of a direct workgroup: a block of K for each, four at most where there are enough
+// workgroups to fill the chip.  (Four for a single block, three of them idle, took 12% longer on
+// average over 136 sizes with K up to 384, up to twice as long.)
 static int direct_waves(int64_t tiles, int64_t kb, int64_t bm) {
-  int waves = 4;
-  while (waves < (bm == 16 ? 16 : 8) && waves * 2 <= kb && tiles * waves < kCus * 16) waves *= 2;
+  int waves = 1;
+  while (waves < (bm == 16 ? 16 : 8) && waves * 2 <= kb && (waves < 4 || tiles * waves < kCus * 16)) waves *= 2;
   return waves;
 }
 
 // Microseconds that a product takes with the given kernel and tile rows: rounds of workgroups
 // that fit the chip together, times what one needs for its blocks of K; the figures (us per
-// block and round) are measured.  A group's last tile is counted as 0.57 of one.
+// block and round) are measured.  A group's last tile is counted as 0.58 of one.
 static double expected_us(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t groups, bool swiglu, bool quant, bool fast,
                           bool tile, int64_t bm, int64_t parts) {
   const int64_t kb = (K + 127) / 128, some = groups < rows ? groups : rows;
-  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.57 * some : static_cast<double>((rows + bm - 1) / bm);
+  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.58 * some : static_cast<double>((rows + bm - 1) / bm);
   auto rounds = [](double wgs, int64_t together) { return wgs <= together ? 1.0 : __builtin_ceil(wgs / together); };
-  // a last round that is at most half full takes tiles of half the rows, in about 0.6 of the time
-  auto tile_rounds = [&](double wgs, int64_t together) {
-    const double r = rounds(wgs, together);
-    return bm >= 128 && wgs / together <= r - 0.5 ? r - 0.4 : r;
-  };
   if (tile) {
     const double tiles = parts > 1 ? mt * ((N + 255) / 256) * parts : mt * ((F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
-    const double join = parts > 1 ? 3.7 + parts * rows * N * 8 / 5700e3 : 0.0;  // a launch, sums written and read
-    double us = fast ? (bm == 256 ? 1.8 : bm == 128 ? 1.36 : 0.93) : (bm == 128 ? 1.82 : 1.31);
+    const double join = parts > 1 ? 4.1 + parts * rows * N * 8 / 5430e3 : 0.0;  // a launch, sums written and read
+    double us = fast ? (bm == 256 ? 1.53 : bm == 128 ? 0.98 : 0.79) : (bm == 128 ? 1.63 : 1.21);
     int64_t together = kCus;
     if (bm == 32) {  // two to a CU
-      us = fast ? (tiles > kCus ? 1.28 : 0.69) : (tiles > kCus ? 1.82 : 0.88);
+      us = fast ? (tiles > kCus ? 1.2 : 0.65) : (tiles > kCus ? 1.68 : 0.83);
       together = 2 * kCus;
     }
-    return 4.0 + tile_rounds(tiles, together) * ((kb + parts - 1) / parts * us + 2.3) + join;
+    return 2.8 + rounds(tiles, together) * ((kb + parts - 1) / parts * us + 2.7) + join;
   }
   const int64_t nt = (F + 15) / 16;
   const int waves = direct_waves(((rows + bm - 1) / bm + some) * nt, kb, bm);
   // waves of a CU by the kernels' registers
   const int fit = bm == 16 ? (swiglu ? 20 : 28) : bm == 32 ? (swiglu ? 12 : 20) : (swiglu ? 8 : 12);
-  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 1.85 : 1.33) * (bm == 64 ? 1.63 : bm == 32 ? 1.18 : 1.0);
-  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus : kCus) * ((kb + waves - 1) / waves * us + 0.6);
-  const double weights = mt * N * K / 5250e3;  // read again for every row tile, from L2
-  return 4.0 + (work > weights ? work : weights) + (quant ? 2.3 : 0.0);
+  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 1.74 : 1.33) * (bm == 64 ? 1.63 : bm == 32 ? 1.27 : 1.0);
+  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus : kCus) * ((kb + waves - 1) / waves * us + 0.7);
+  const double weights = mt * N * K / 5120e3;  // read again for every row tile, from L2
+  return 2.8 + (work > weights ? work : weights) + (quant ? 3.6 : 0.0);
 }
 
 int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
@@ -494,7 +490,7 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     return p->mtiles * (p->join && p->join_groups > p->ntiles ? p->join_groups : p->ntiles);
   };
   // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  Over
-  // 420 random sizes (1 to 16384 rows, K and N to 8192, 0 to 256 groups) the choice is 1.5% slower
+  // 480 random sizes (1 to 16384 rows, K and N to 8192, 0 to 256 groups) the choice is 1.9% slower
   // than the best of the shapes on average; a fixed rule (the largest tile that the groups fill
   // and that gives every CU one) was 15%.  Parts are what fills the chip with a long K and few tiles:
   // 256 rows by 2048 columns over 7168 take 39.9 us in the best shape without and 17.7 us in 8 parts,

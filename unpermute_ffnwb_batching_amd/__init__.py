@@ -163,6 +163,25 @@ def _record_on(tensors, stream, alloc_stream):
             t.record_stream(stream)
 
 
+class _Prepared:
+    """A call with its tensors bound."""
+
+    _marked = frozenset()   # streams (raw handles) that the call's tensors are marked as used by
+    workspace = None
+
+    def _mark_used(self, stream):
+        """Mark the call's tensors as used by ``stream``, which the caller named: inputs, and outputs
+        the caller passed, may have been made on any other, and dropping them right after the call
+        must not let the allocator hand their memory out before that work ends.  Once per
+        stream: the call holds the tensors, and a mark lasts as long as the memory."""
+        if stream is None or stream.cuda_stream in self._marked:
+            return
+        self._marked |= {stream.cuda_stream}
+        for t in (self.workspace, *self._keep, *self.out.values()):
+            if t is not None and t.numel() > 0:
+                t.record_stream(stream)
+
+
 # ----------------------------------------------------------------------------- argument checks
 # The C descriptors carry raw pointers and sizes only, so the shapes, element types and
 # layouts of the tensors behind them are checked here before any call is built.
@@ -225,7 +244,7 @@ def _row_stride_bytes(t):
     return t.stride(0) * t.element_size() if t.dim() >= 2 else 0
 
 
-class BatchingCall:
+class BatchingCall(_Prepared):
     """A prepared ffnwb_batching call: descriptor, outputs and workspace bound once.
 
     ``token_data`` is a device tensor whose dim-0 rows are the Y slots (any element
@@ -264,7 +283,6 @@ class BatchingCall:
             out["err_count"] = torch.empty(1, **i32)
         self.out = out
         self._keep = [token_data, expert_ids, mask, layer_ids, session_ids, micro_batch_ids, token_scale]
-        self._alloc_stream = _alloc_stream(dev)
 
         d = BatchingDesc()
         d.A, d.BS, d.K1, d.H = A, BS, K1, H
@@ -309,7 +327,7 @@ class BatchingCall:
                                   _stream_handle(stream))
         if st != FFNWB_OK:
             raise FfnwbError(st, "ffnwb_batching")
-        _record_on([ws, *self.out.values()], stream, self._alloc_stream)
+        self._mark_used(stream)
         return self.out
 
 
@@ -370,7 +388,7 @@ def ffnwb_batching_ctx_workspace_size(desc):
     return n.value
 
 
-class BatchingCtxCall:
+class BatchingCtxCall(_Prepared):
     """A prepared ffnwb_batching_ctx call.
 
     ``schedule_context`` is a device tensor holding the 1024 context bytes (8-byte
@@ -409,7 +427,6 @@ class BatchingCtxCall:
             out["ctx_status"] = torch.empty(1, **i32)
         self.out = out
         self._keep = [schedule_context]
-        self._alloc_stream = _alloc_stream(dev)
 
         d = BatchingCtxDesc()
         d.A, d.BS, d.K1, d.H = A, BS, K1, H
@@ -446,7 +463,7 @@ class BatchingCtxCall:
                                       _stream_handle(stream))
         if st != FFNWB_OK:
             raise FfnwbError(st, "ffnwb_batching_ctx")
-        _record_on([self.workspace, *self.out.values()], stream, self._alloc_stream)
+        self._mark_used(stream)
         return self.out
 
 
@@ -470,7 +487,7 @@ def moe_unpermute_workspace_size(desc):
     return n.value
 
 
-class UnpermuteCall:
+class UnpermuteCall(_Prepared):
     """A prepared moe_unpermute call.
 
     ``permuted_tokens`` [rows, H] (fp16 / bf16 / fp32), ``sorted_indices`` int32 [N],
@@ -567,6 +584,7 @@ class UnpermuteCall:
         st = lib().moe_unpermute_noalloc(ctypes.byref(self.desc), _stream_handle(stream))
         if st != FFNWB_OK:
             raise FfnwbError(st, "moe_unpermute_noalloc")
+        self._mark_used(stream)
         return self.out
 
     def set_reduce_events(self, begin, end):
@@ -578,7 +596,7 @@ class UnpermuteCall:
                                  _stream_handle(stream))
         if st != FFNWB_OK:
             raise FfnwbError(st, "moe_unpermute")
-        _record_on([self.workspace, *self.out.values()], stream, self._alloc_stream)
+        self._mark_used(stream)
         if self.aux_stream is not None:
             # the sort's workspace and outputs are also used on the auxiliary stream
             _record_on([self.workspace, self.out.get("out_index"), self.out.get("permute_token_id")],
@@ -612,7 +630,7 @@ def moe_permute_workspace_size(desc):
     return n.value
 
 
-class PermuteCall:
+class PermuteCall(_Prepared):
     """A prepared moe_permute call.
 
     ``tokens`` [T, H] (fp16 / bf16 / fp32 / int8 / uint8; rows may be strided),
@@ -646,7 +664,6 @@ class PermuteCall:
         self.out = out
         rm = routing_map.view(torch.uint8) if routing_map.dtype in (torch.bool, torch.int8) else routing_map
         self._keep = [tokens, rm]
-        self._alloc_stream = _alloc_stream(dev)
         d = PermuteDesc()
         d.dtype = _ANY_CODE.get(tokens.dtype, -1)
         d.padded_mode = int(bool(padded_mode))
@@ -678,7 +695,7 @@ class PermuteCall:
                                _stream_handle(stream))
         if st != FFNWB_OK:
             raise FfnwbError(st, "moe_permute")
-        _record_on([self.workspace, *self.out.values()], stream, self._alloc_stream)
+        self._mark_used(stream)
         return self.out
 
 
@@ -702,7 +719,7 @@ def moe_update_expert_workspace_size(desc):
     return n.value
 
 
-class UpdateExpertCall:
+class UpdateExpertCall(_Prepared):
     """A prepared moe_update_expert call.  ``expert_ids`` [BS, K] int32 / int64,
     ``eplb_table`` [E, F] int32, optional ``expert_scales`` [BS, K] (float16, bfloat16
     or float32) with ``pruning_threshold`` [K] or [1, K] float32, and optional
@@ -746,7 +763,6 @@ class UpdateExpertCall:
             out["err_count"] = torch.empty(1, dtype=torch.int32, device=dev)
         self.out = out
         self._keep = [expert_ids, eplb_table, expert_scales, pruning_threshold, active_mask]
-        self._alloc_stream = _alloc_stream(dev)
         d = UpdateExpertDesc()
         d.bs, d.k, d.moe_expert_num, d.table_cols = BS, K, E, Fc
         d.local_rank_id, d.world_size, d.balance_mode = int(local_rank_id), int(world_size), int(balance_mode)
@@ -780,7 +796,7 @@ class UpdateExpertCall:
         st = lib().moe_update_expert(ctypes.byref(self.desc), None, ctypes.c_size_t(0), _stream_handle(stream))
         if st != FFNWB_OK:
             raise FfnwbError(st, "moe_update_expert")
-        _record_on(list(self.out.values()), stream, self._alloc_stream)
+        self._mark_used(stream)
         return self.out
 
 
@@ -810,7 +826,7 @@ def _row_bytes(t):
     return _row_elems(t) * t.element_size()
 
 
-class _Call:
+class _Call(_Prepared):
     """A descriptor with its outputs and workspace, launched on the tensors' own device.  Runs of
     one call share both, so runs that may overlap (on two streams, in two graphs) need a call each."""
 
@@ -843,9 +859,10 @@ class _Call:
                 st = self._fn(*self._args, raw)
         if st != FFNWB_OK:
             raise FfnwbError(st, self._name)
-        if raw != self._alloc_raw:
-            _record_on([self.workspace, *self._keep, *self.out.values()],
-                       stream if stream is not None else torch.cuda.current_stream(index), self._alloc_stream)
+        if stream is not None:
+            self._mark_used(stream)
+        elif raw != self._alloc_raw:   # prepared under another stream than the present one
+            self._mark_used(torch.cuda.current_stream(index))
         return self.out
 
 

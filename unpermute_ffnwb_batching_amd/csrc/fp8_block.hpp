@@ -32,9 +32,10 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
 }
 
 // x / s rounded to nearest for the values of one block, |x / s| <= 448.  r = RN(1/s), q0 =
-// RN(x r); the residual x - q0 s is exact in one FMA, and RN(q0 + residual r) is the quotient
+// RN(x r); the residual q0 s - x is exact in one FMA, and RN(q0 - residual r) is the quotient
 // (the last step of division by Newton's iteration, Markstein 1990): 3 operations where the
-// division takes about 10.  Equal to the division on 4e7 operands, half of them within 3
+// division takes about 10.  With the residual taken this way round, x = -0 gives -0: its residual is +0,
+// and -0 - (+0) stays -0, where -0 + (+0) would be +0.  Equal to the division on 4e7 operands, half of them within 3
 // steps of a midpoint of e4m3, the only place where the last bit could matter.  Residuals must
 // not underflow: quotients below 2^-11 are 0 in e4m3, so s >= 2^-80 is ample; s <= 2^100 keeps
 // r normal.  Other blocks, those with infinities and NaN among them, divide.
@@ -45,7 +46,7 @@ __device__ __forceinline__ void block_quotients(float (&x)[N], float s) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float q0 = x[i] * r;
-      x[i] = __builtin_fmaf(__builtin_fmaf(-q0, s, x[i]), r, q0);
+      x[i] = __builtin_fmaf(-__builtin_fmaf(q0, s, -x[i]), r, q0);
     }
   } else {
 #pragma unroll

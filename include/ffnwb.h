@@ -626,6 +626,17 @@ typedef struct moe_layer_desc {
    weights, or missing with e4m3 ones). */
 int moe_layer_workspace_size(const moe_layer_desc* d, size_t* ws_bytes);
 
+/* Which kernels a call of *d runs, for reports and tests (host only; the errors of
+   moe_layer_workspace_size). */
+typedef struct moe_layer_plan_info {
+  int32_t up_tokens;         /* 16 or 64: the most tokens of an expert that launch 1 is compiled for */
+  int32_t up_waves;          /* waves that share the columns of H of a tile of launch 1: 1, 4 or 8 */
+  int32_t lane_routing;      /* 1: every wave of launch 1 finds its expert among up to 64 slots; 0: through LDS */
+  int32_t down_parts;        /* workgroups that share the experts of a column tile of launch 2 */
+} moe_layer_plan_info;
+
+int moe_layer_plan(const moe_layer_desc* d, moe_layer_plan_info* info);
+
 /* Validates again, then enqueues the layer on `stream`. */
 int moe_layer(const moe_layer_desc* d, void* workspace, size_t ws_bytes, void* stream);
 

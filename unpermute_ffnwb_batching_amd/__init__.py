@@ -13,7 +13,7 @@ The names mirror the C ABI:
 * ``moe_update_expert_workspace_size`` / ``moe_update_expert``
 * ``moe_quant_fp8_workspace_size`` / ``moe_quant_fp8``
 * ``moe_grouped_matmul_fp8_workspace_size`` / ``moe_grouped_matmul_fp8``
-* ``moe_layer_workspace_size`` / ``moe_layer``
+* ``moe_layer_workspace_size`` / ``moe_layer_plan`` / ``moe_layer``
 * ``ffnwb_status_string``, ``ffnwb_abi_version``
 
 ``ffnwb_batching``, ``moe_unpermute`` and the other ``moe_`` calls take torch tensors,
@@ -40,7 +40,8 @@ from ._abi import (FFNWB_OK, FFNWB_ERR_PARAM_NULLPTR, FFNWB_ERR_PARAM_INVALID,  
                    FFNWB_CTX_BYTES, FFNWB_CTX_SHAPE, FFNWB_CTX_POLLING, FFNWB_CTX_POINTER,
                    FFNWB_CTX_BUFFER, FFNWB_DT_INT32, FFNWB_DT_INT64, BatchingDesc, BatchingCtxDesc,
                    UnpermuteDesc, PermuteDesc, UpdateExpertDesc, FFNWB_DT_FP8_E4M3, FFNWB_FP8_BLOCK,
-                   FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc)
+                   FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc,
+                   LayerPlanInfo)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libffnwb.so")
 _lib = None
@@ -81,6 +82,9 @@ def lib():
             getattr(L, name + "_desc_size").restype = sz
             if getattr(L, name + "_desc_size")() != ctypes.sizeof(desc):
                 raise RuntimeError("libffnwb descriptor layout does not match the Python binding")
+        for name, desc, info in (("moe_layer_plan", LayerDesc, LayerPlanInfo),):
+            getattr(L, name).argtypes = [ctypes.POINTER(desc), ctypes.POINTER(info)]
+            getattr(L, name).restype = ctypes.c_int
         for f in ("ffnwb_batching_workspace_size", "ffnwb_batching", "ffnwb_batching_ctx_workspace_size",
                   "ffnwb_batching_ctx", "moe_unpermute_workspace_size",
                   "moe_unpermute", "moe_unpermute_noalloc", "moe_permute_workspace_size", "moe_permute", "moe_update_expert_workspace_size",
@@ -884,6 +888,18 @@ def moe_grouped_matmul_fp8_workspace_size(desc):
 
 def moe_layer_workspace_size(desc):
     return _workspace_size("moe_layer", desc)
+
+
+def _plan(name, desc, info):
+    st = getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(info))
+    if st != FFNWB_OK:
+        raise FfnwbError(st, name)
+    return {f: getattr(info, f) for f, _ in info._fields_}
+
+
+def moe_layer_plan(desc):
+    """Which kernels a call runs: dict(up_tokens, up_waves, lane_routing, down_parts)."""
+    return _plan("moe_layer_plan", desc, LayerPlanInfo())
 
 
 class QuantFp8Call(_Call):

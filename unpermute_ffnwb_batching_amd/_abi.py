@@ -124,6 +124,10 @@ class GroupedMatmulFp8Desc(ctypes.Structure):
     ]
 
 
+class LayerPlanInfo(ctypes.Structure):
+    _fields_ = [("up_tokens", _i32), ("up_waves", _i32), ("lane_routing", _i32), ("down_parts", _i32)]
+
+
 class LayerDesc(ctypes.Structure):
     _fields_ = [
         ("dtype", _i32), ("weight_dtype", _i32), ("id_dtype", _i32), ("scale_dtype", _i32),

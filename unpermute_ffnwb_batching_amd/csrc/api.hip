@@ -195,6 +195,16 @@ int moe_layer_workspace_size(const moe_layer_desc* d, size_t* ws_bytes) {
   return FFNWB_OK;
 }
 
+int moe_layer_plan(const moe_layer_desc* d, moe_layer_plan_info* info) {
+  if (info == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  LayerPlan p;
+  const int st = plan_layer(d, &p);
+  if (st != FFNWB_OK) return st;
+  *info = moe_layer_plan_info{static_cast<int32_t>(p.up_tokens), static_cast<int32_t>(p.split), p.lanes ? 1 : 0,
+                              static_cast<int32_t>(p.parts)};
+  return FFNWB_OK;
+}
+
 int moe_layer(const moe_layer_desc* d, void* workspace, size_t ws_bytes, void* stream) {
   LayerPlan p;
   const int st = plan_layer(d, &p);

@@ -148,7 +148,9 @@ struct LayerPlan {
   int64_t xs = 0, ys = 0, is = 0, ss = 0, ms = 0;  // row strides: bytes, bytes, elements
   int64_t ranks = 0;                               // most distinct experts: min(T * K, E)
   int64_t groups = 0;                              // most groups of up to 16 tokens of one expert
+  int64_t up_tokens = 16;                          // tokens that the first launch's kernel is compiled for
   int64_t split = 4;                               // waves of a tile of the first launch
+  bool lanes = true;                               // its slots are one to a lane
   int64_t parts = 1;                               // workgroups of a column tile of the second launch
   size_t ws_bytes = 0;
 };

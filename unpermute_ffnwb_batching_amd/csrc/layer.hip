@@ -33,6 +33,7 @@ struct LayerArgs {
   int32_t ctiles;             // 16-column tiles of F
   int32_t groups_max;         // most groups of launch 2
   int32_t id64;
+  bool lanes;                 // at most 64 slots: one to a lane
   int32_t scale_dtype;
   int64_t xs, ys, is, ss, ms;
   const char* x;
@@ -368,7 +369,7 @@ __global__ __launch_bounds__((kSplit == 1 ? 4 : kSplit) * kWave) void layer_up_k
   const int32_t c = (static_cast<int32_t>(blockIdx.x) - 1 - rank * per) * (kSplit == 1 ? 4 : 1) +
                     (kSplit == 1 ? static_cast<int32_t>(threadIdx.x / kWave) : 0);
   const int32_t lane = threadIdx.x % kWave;
-  if (blockIdx.x != 0 && a.T * a.K <= kWave) {
+  if (blockIdx.x != 0 && a.lanes) {
     // Up to 64 slots are one to a lane, and every wave finds the workgroup's expert (the rank-th
     // in the order of the slots) by itself: two barriers and a pass through LDS less.
     int32_t* list = lists[threadIdx.x / kWave];
@@ -613,6 +614,8 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
   // Launch 1: four waves to a tile, eight where the tiles are few and H is long; a tile to each
   // wave where H has fewer blocks than four.
   const int64_t hb = (p->H + 127) / 128;
+  p->up_tokens = p->T <= 16 ? 16 : 64;
+  p->lanes = n <= kWave;
   p->split = hb < 4 ? 1 : hb >= 16 && p->ranks * (p->F / 16) < 1024 ? 8 : 4;
   Carve c;
   if (n > 0) {
@@ -658,7 +661,7 @@ static bool launch_up(const LayerArgs& a, const LayerPlan& p, hipStream_t s, voi
 
 template <class T, bool kFp8>
 static bool launch_t(const LayerArgs& a, const LayerPlan& p, hipStream_t s, void* begin, void* end) {
-  if (!(p.T <= 16 ? launch_up<T, kFp8, 16>(a, p, s, begin) : launch_up<T, kFp8, 64>(a, p, s, begin))) return false;
+  if (!(p.up_tokens == 16 ? launch_up<T, kFp8, 16>(a, p, s, begin) : launch_up<T, kFp8, 64>(a, p, s, begin))) return false;
   const size_t lds = (kDownWaves * p.T * 16 + 2 * p.groups + 1 + 2 * p.T * p.K) * 4;
   allow_large_lds(reinterpret_cast<const void*>(layer_down_kernel<T, kFp8>), lds);
   return launch_bound(layer_down_kernel<T, kFp8>, dim3(static_cast<uint32_t>(p.H / 16 * p.parts)), dim3(kDownWaves * kWave), lds, s, nullptr,
@@ -673,6 +676,7 @@ int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStrea
   a.hb = (a.H + kBlk - 1) / kBlk, a.fb = (a.F + kBlk - 1) / kBlk, a.nb13 = (2 * a.F + kBlk - 1) / kBlk;
   a.ctiles = a.F / 16;
   a.groups_max = static_cast<int32_t>(p.groups);
+  a.lanes = p.lanes;
   a.id64 = d->id_dtype == FFNWB_DT_INT64;
   a.scale_dtype = d->scale_dtype;
   a.xs = p.xs, a.ys = p.ys, a.is = p.is, a.ss = p.ss, a.ms = p.ms;

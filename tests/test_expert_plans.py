@@ -34,3 +34,12 @@ def test_layer_first_launch_with_many_tiles():
     # experts x inter / 16 from 1024 on: four waves to a tile whatever H
     assert _layer_plan(1, 8, 256, 7168, 2032)["up_waves"] == 8
     assert _layer_plan(1, 8, 256, 7168, 2048)["up_waves"] == 4
+
+
+def test_layer_second_launch():
+    # the sizes that the rule's comment names, and its limits
+    assert _layer_plan(5, 8, 23, 576, 1024, bf16=True)["down_parts"] == 12
+    assert _layer_plan(1, 6, 16, 2944, 496)["down_parts"] == 1
+    assert _layer_plan(64, 8, 64, 4080, 1024)["down_parts"] == 2     # 255 column tiles
+    assert _layer_plan(64, 8, 64, 4096, 1024)["down_parts"] == 1     # 256
+    assert _layer_plan(64, 8, 64, 64, 2048)["down_parts"] == 32

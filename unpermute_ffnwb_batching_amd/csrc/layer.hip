@@ -627,8 +627,10 @@ int plan_layer(const moe_layer_desc* d, LayerPlan* p) {
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
     c.take<uint16_t>(static_cast<size_t>(n * p->F));
     // Launch 2 has H / 16 column tiles: below 256 their blocks of F are split over several
-    // workgroups each, as long as every wave may have two (at most 32 workgroups).  One token's 6
-    // experts of hidden 2944 and inter 496: 102 us by one workgroup a tile, 17 us by two.
+    // workgroups each, as long as every wave may have two (at most 32 workgroups).  5 tokens with 8 of 23
+    // experts, hidden 576, inter 1024, BF16: 51 us by one workgroup a tile, 27 us by the 12 it gets.  One
+    // token's 6 experts, hidden 2944, inter 496, whose waves have 3 blocks each: 14.1 us by the one it gets, 15.3 by
+    // two.  Over 92 random layers the choice is 3% slower than the best count on average, 19% at most.
     const int64_t tiles = p->H / 16, blocks = p->groups * ((p->F + 127) / 128);
     p->parts = tiles >= 256 ? 1 : 512 / tiles < 32 ? 512 / tiles : 32;
     if (p->parts > blocks / (2 * kDownWaves)) p->parts = blocks / (2 * kDownWaves);

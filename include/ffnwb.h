@@ -568,6 +568,18 @@ typedef struct moe_grouped_matmul_fp8_desc {
    so while (ceil(R / 64) + num_groups) * ceil(F / 16), F = N without SwiGLU, is no more). */
 int moe_grouped_matmul_fp8_workspace_size(const moe_grouped_matmul_fp8_desc* d, size_t* ws_bytes);
 
+/* Which kernels a call of *d runs, for reports and tests (host only; the errors of
+   moe_grouped_matmul_fp8_workspace_size). */
+typedef struct moe_grouped_matmul_fp8_plan_info {
+  int32_t lds_tiles;         /* 1: tiles of 256 columns through LDS; 0: 16 columns straight to registers */
+  int32_t tile_rows;         /* 32, 64, 128 or 256; 16, 32 or 64 */
+  int32_t e4m3_products;     /* 1: e4m3 matrix instructions; 0: operands widened to 16 bits */
+  int32_t k_parts;           /* parts of K, added by a launch of their own when more than one */
+  int32_t listed;            /* 1: the row tiles are listed by a launch of their own */
+} moe_grouped_matmul_fp8_plan_info;
+
+int moe_grouped_matmul_fp8_plan(const moe_grouped_matmul_fp8_desc* d, moe_grouped_matmul_fp8_plan_info* info);
+
 /* Validates again, then enqueues the product on `stream`. */
 int moe_grouped_matmul_fp8(const moe_grouped_matmul_fp8_desc* d, void* workspace, size_t ws_bytes, void* stream);
 

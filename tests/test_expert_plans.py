@@ -5,8 +5,11 @@ import ctypes
 
 import pytest
 
+import test_gpu_layer_forms
+import test_gpu_product_forms
 import unpermute_ffnwb_batching_amd as F
-from test_expert_ffn_checks import _layer
+from test_expert_ffn_checks import _layer, _matmul
+from test_gpu_product_forms import BF16, FORMS, FP8, FP16, FP32
 
 
 def _layer_plan(T, K, E, H, inter, bf16=False):
@@ -43,3 +46,48 @@ def test_layer_second_launch():
     assert _layer_plan(64, 8, 64, 4080, 1024)["down_parts"] == 2     # 255 column tiles
     assert _layer_plan(64, 8, 64, 4096, 1024)["down_parts"] == 1     # 256
     assert _layer_plan(64, 8, 64, 64, 2048)["down_parts"] == 32
+
+
+@pytest.mark.parametrize("size,form", test_gpu_layer_forms.FORMS, ids=str)
+def test_the_layers_gpu_tests_reach_their_forms(size, form):
+    p = _layer_plan(*size)
+    assert (p["up_tokens"], p["up_waves"], p["lane_routing"]) == form
+
+
+def test_product_plan_refuses_what_the_call_refuses():
+    info = F.GroupedMatmulFp8PlanInfo()
+    plan = F.lib().moe_grouped_matmul_fp8_plan
+    assert plan(None, ctypes.byref(info)) == F.FFNWB_ERR_PARAM_NULLPTR
+    assert plan(ctypes.byref(_matmul()), None) == F.FFNWB_ERR_PARAM_NULLPTR
+    assert plan(ctypes.byref(_matmul(in_features=24)), ctypes.byref(info)) == F.FFNWB_ERR_PARAM_INVALID
+    with pytest.raises(F.FfnwbError):
+        F.moe_grouped_matmul_fp8_plan(_matmul(num_experts=0))
+
+
+def _product_plan(size, dtype, epilogue, **over):
+    rows, k, n, experts = size
+    groups = test_gpu_product_forms._groups(rows, experts)
+    over.update(dict(group_list=None, num_groups=0, num_experts=1) if groups is None else
+                dict(num_groups=len(groups), num_experts=4))
+    return F.moe_grouped_matmul_fp8_plan(_matmul(
+        num_rows=rows, in_features=k, out_features=n, epilogue=int(epilogue == "swiglu"), x_row_stride=k + 48,
+        out_dtype={FP16: 0, BF16: 1, FP32: 3, FP8: 6}[dtype], **over))
+
+
+@pytest.mark.parametrize("size,dtype,epilogue,kernel,how", FORMS, ids=test_gpu_product_forms._ids)
+def test_the_products_gpu_tests_reach_their_kernels(size, dtype, epilogue, kernel, how):
+    test_gpu_product_forms.check_form(_product_plan(size, dtype, epilogue), size, dtype, epilogue, kernel, how)
+
+
+def test_every_kernel_of_the_products_has_a_size():
+    # direct: 3 heights, results of 3 types, plain and SwiGLU, and e4m3 ones; tiles: 16-bit results of 4 heights, plain
+    # and SwiGLU, FP32 ones of 3, e4m3 ones of 3; split: 3 heights of all of them
+    have = {(kernel, dtype, epilogue, "split" in how) for _, dtype, epilogue, kernel, how in FORMS}
+    for epilogue in ("none", "swiglu"):
+        for dtype in (BF16, FP16, FP32) + ((FP8,) if epilogue == "swiglu" else ()):
+            for rows in (16, 32, 64):
+                assert (f"direct{rows}", dtype, epilogue, False) in have
+            for rows in (32, 64, 128) + ((256,) if dtype in (BF16, FP16) else ()):
+                assert (f"tiles{rows}", dtype, epilogue, False) in have
+                if rows < 256:
+                    assert (f"tiles{rows}", dtype, epilogue, True) in have

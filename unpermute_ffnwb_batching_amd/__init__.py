@@ -12,7 +12,7 @@ The names mirror the C ABI:
 * ``moe_permute_workspace_size`` / ``moe_permute``
 * ``moe_update_expert_workspace_size`` / ``moe_update_expert``
 * ``moe_quant_fp8_workspace_size`` / ``moe_quant_fp8``
-* ``moe_grouped_matmul_fp8_workspace_size`` / ``moe_grouped_matmul_fp8``
+* ``moe_grouped_matmul_fp8_workspace_size`` / ``moe_grouped_matmul_fp8_plan`` / ``moe_grouped_matmul_fp8``
 * ``moe_layer_workspace_size`` / ``moe_layer_plan`` / ``moe_layer``
 * ``ffnwb_status_string``, ``ffnwb_abi_version``
 
@@ -41,7 +41,7 @@ from ._abi import (FFNWB_OK, FFNWB_ERR_PARAM_NULLPTR, FFNWB_ERR_PARAM_INVALID,  
                    FFNWB_CTX_BUFFER, FFNWB_DT_INT32, FFNWB_DT_INT64, BatchingDesc, BatchingCtxDesc,
                    UnpermuteDesc, PermuteDesc, UpdateExpertDesc, FFNWB_DT_FP8_E4M3, FFNWB_FP8_BLOCK,
                    FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc,
-                   LayerPlanInfo)
+                   GroupedMatmulFp8PlanInfo, LayerPlanInfo)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libffnwb.so")
 _lib = None
@@ -82,7 +82,8 @@ def lib():
             getattr(L, name + "_desc_size").restype = sz
             if getattr(L, name + "_desc_size")() != ctypes.sizeof(desc):
                 raise RuntimeError("libffnwb descriptor layout does not match the Python binding")
-        for name, desc, info in (("moe_layer_plan", LayerDesc, LayerPlanInfo),):
+        for name, desc, info in (("moe_grouped_matmul_fp8_plan", GroupedMatmulFp8Desc, GroupedMatmulFp8PlanInfo),
+                                 ("moe_layer_plan", LayerDesc, LayerPlanInfo)):
             getattr(L, name).argtypes = [ctypes.POINTER(desc), ctypes.POINTER(info)]
             getattr(L, name).restype = ctypes.c_int
         for f in ("ffnwb_batching_workspace_size", "ffnwb_batching", "ffnwb_batching_ctx_workspace_size",
@@ -895,6 +896,11 @@ def _plan(name, desc, info):
     if st != FFNWB_OK:
         raise FfnwbError(st, name)
     return {f: getattr(info, f) for f, _ in info._fields_}
+
+
+def moe_grouped_matmul_fp8_plan(desc):
+    """Which kernels a call runs: dict(lds_tiles, tile_rows, e4m3_products, k_parts, listed)."""
+    return _plan("moe_grouped_matmul_fp8_plan", desc, GroupedMatmulFp8PlanInfo())
 
 
 def moe_layer_plan(desc):

@@ -124,6 +124,10 @@ class GroupedMatmulFp8Desc(ctypes.Structure):
     ]
 
 
+class GroupedMatmulFp8PlanInfo(ctypes.Structure):
+    _fields_ = [("lds_tiles", _i32), ("tile_rows", _i32), ("e4m3_products", _i32), ("k_parts", _i32), ("listed", _i32)]
+
+
 class LayerPlanInfo(ctypes.Structure):
     _fields_ = [("up_tokens", _i32), ("up_waves", _i32), ("lane_routing", _i32), ("down_parts", _i32)]
 

@@ -178,6 +178,16 @@ int moe_grouped_matmul_fp8_workspace_size(const moe_grouped_matmul_fp8_desc* d, 
   return FFNWB_OK;
 }
 
+int moe_grouped_matmul_fp8_plan(const moe_grouped_matmul_fp8_desc* d, moe_grouped_matmul_fp8_plan_info* info) {
+  if (info == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  MatmulPlan p;
+  const int st = plan_grouped_matmul(d, &p);
+  if (st != FFNWB_OK) return st;
+  *info = moe_grouped_matmul_fp8_plan_info{p.tile ? 1 : 0, static_cast<int32_t>(p.bm), p.fast ? 1 : 0,
+                                           static_cast<int32_t>(p.parts), p.table ? 1 : 0};
+  return FFNWB_OK;
+}
+
 int moe_grouped_matmul_fp8(const moe_grouped_matmul_fp8_desc* d, void* workspace, size_t ws_bytes, void* stream) {
   MatmulPlan p;
   const int st = plan_grouped_matmul(d, &p);

@@ -517,6 +517,7 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   }
   if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
   shape(best_bm, best_parts);
+  p->fast = p->tile && fast;
   p->pitch = p->parts > 1 ? (p->N + 7) / 8 * 8 : p->F;
   p->ws_bytes = 0;
   Carve c;
@@ -611,8 +612,8 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
   const bool swiglu = d->epilogue == FFNWB_EPI_SWIGLU, quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
   bool ok;
   if (p.parts > 1) {
-    ok = out_size(d->out_dtype) == 2 ? launch_tile<TF32, FFNWB_EPI_NONE, false, true>(m, p, s, b, product_end)
-                                     : launch_tile<TF32, FFNWB_EPI_NONE>(m, p, s, b, product_end);
+    ok = p.fast ? launch_tile<TF32, FFNWB_EPI_NONE, false, true>(m, p, s, b, product_end)
+                : launch_tile<TF32, FFNWB_EPI_NONE>(m, p, s, b, product_end);
   } else if (p.tile && swiglu) {
     ok = quant                ? launch_tile<TF32, FFNWB_EPI_SWIGLU, true>(m, p, s, b, e)
          : dt == FFNWB_DT_FP16 ? launch_tile<TF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)

@@ -9,7 +9,7 @@ import test_gpu_layer_forms
 import test_gpu_product_forms
 import unpermute_ffnwb_batching_amd as F
 from test_expert_ffn_checks import _layer, _matmul
-from test_gpu_product_forms import BF16, FORMS, FP8, FP16, FP32
+from test_gpu_product_forms import BF16, EXACT_FORMS, FORMS, FP8, FP16, FP32
 
 
 def _layer_plan(T, K, E, H, inter, bf16=False):
@@ -64,19 +64,35 @@ def test_product_plan_refuses_what_the_call_refuses():
         F.moe_grouped_matmul_fp8_plan(_matmul(num_experts=0))
 
 
-def _product_plan(size, dtype, epilogue, **over):
+def _product_plan(size, dtype, epilogue, exact=False, **over):
     rows, k, n, experts = size
     groups = test_gpu_product_forms._groups(rows, experts)
     over.update(dict(group_list=None, num_groups=0, num_experts=1) if groups is None else
                 dict(num_groups=len(groups), num_experts=4))
     return F.moe_grouped_matmul_fp8_plan(_matmul(
-        num_rows=rows, in_features=k, out_features=n, epilogue=int(epilogue == "swiglu"), x_row_stride=k + 48,
+        num_rows=rows, in_features=k, out_features=n, epilogue=int(epilogue == "swiglu") + (F.FFNWB_EPI_EXACT if exact else 0), x_row_stride=k + 48,
         out_dtype={FP16: 0, BF16: 1, FP32: 3, FP8: 6}[dtype], **over))
 
 
 @pytest.mark.parametrize("size,dtype,epilogue,kernel,how", FORMS, ids=test_gpu_product_forms._ids)
 def test_the_products_gpu_tests_reach_their_kernels(size, dtype, epilogue, kernel, how):
     test_gpu_product_forms.check_form(_product_plan(size, dtype, epilogue), size, dtype, epilogue, kernel, how)
+
+
+@pytest.mark.parametrize("size,dtype,epilogue,kernel,how", EXACT_FORMS, ids=test_gpu_product_forms._ids)
+def test_the_exact_products_gpu_tests_reach_their_kernels(size, dtype, epilogue, kernel, how):
+    plan = _product_plan(size, dtype, epilogue, exact=True)
+    test_gpu_product_forms.check_form(plan, size, dtype, epilogue, kernel, how, exact=True)
+
+
+def test_exact_is_a_flag_of_the_epilogue():
+    for epilogue, ok in ((0, True), (1, True), (2, False), (512, False), (-1, False), (-256, False)):
+        d = _matmul(epilogue=epilogue | F.FFNWB_EPI_EXACT)
+        st = F.lib().moe_grouped_matmul_fp8_plan(ctypes.byref(d), ctypes.byref(F.GroupedMatmulFp8PlanInfo()))
+        assert st == (F.FFNWB_OK if ok else F.FFNWB_ERR_PARAM_INVALID), epilogue
+    # e4m3 results still need SwiGLU
+    d = _matmul(epilogue=F.FFNWB_EPI_EXACT, out_dtype=6)
+    assert F.lib().moe_grouped_matmul_fp8_plan(ctypes.byref(d), ctypes.byref(F.GroupedMatmulFp8PlanInfo())) == F.FFNWB_ERR_PARAM_INVALID
 
 
 def test_every_kernel_of_the_products_has_a_size():
@@ -89,5 +105,7 @@ def test_every_kernel_of_the_products_has_a_size():
                 assert (f"direct{rows}", dtype, epilogue, False) in have
             for rows in (32, 64, 128) + ((256,) if dtype in (BF16, FP16) else ()):
                 assert (f"tiles{rows}", dtype, epilogue, False) in have
+                if dtype in (BF16, FP16) and rows < 256:
+                    assert any(f[1:4] == (dtype, epilogue, f"tiles{rows}") and "split" not in f[4] for f in EXACT_FORMS)
                 if rows < 256:
                     assert (f"tiles{rows}", dtype, epilogue, True) in have

@@ -40,7 +40,7 @@ from ._abi import (FFNWB_OK, FFNWB_ERR_PARAM_NULLPTR, FFNWB_ERR_PARAM_INVALID,  
                    FFNWB_CTX_BYTES, FFNWB_CTX_SHAPE, FFNWB_CTX_POLLING, FFNWB_CTX_POINTER,
                    FFNWB_CTX_BUFFER, FFNWB_DT_INT32, FFNWB_DT_INT64, BatchingDesc, BatchingCtxDesc,
                    UnpermuteDesc, PermuteDesc, UpdateExpertDesc, FFNWB_DT_FP8_E4M3, FFNWB_FP8_BLOCK,
-                   FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc,
+                   FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, FFNWB_EPI_EXACT, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc,
                    GroupedMatmulFp8PlanInfo, LayerPlanInfo)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libffnwb.so")
@@ -960,11 +960,13 @@ class GroupedMatmulFp8Call(_Call):
     order; None: one dense product (E = 1, ``w`` and ``w_scale`` may also be 2-D).
     ``epilogue`` FFNWB_EPI_NONE or FFNWB_EPI_SWIGLU (N = 2 F, gate rows then up rows).
     ``out_dtype`` float16 / bfloat16 / float32, or float8_e4m3fn with SwiGLU, which also
-    returns ``y_scale``.  K must be a multiple of 16, F too.
+    returns ``y_scale``.  K must be a multiple of 16, F too.  ``exact``: 16-bit results are
+    FP32 sums rounded once, at every size; by default large products with 16-bit results use the e4m3
+    matrix instructions, twice as fast, which drop low bits of products beside much larger ones.
     """
 
     def __init__(self, x, x_scale, w, w_scale, *, group_list=None, epilogue=FFNWB_EPI_NONE, out_dtype=torch.bfloat16,
-                 out=None, workspace=None, ev_matmul=None):
+                 exact=False, out=None, workspace=None, ev_matmul=None):
         _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [R, K]")
         dev = x.device
         _check_rows(x, "x", dev, (_FP8,))
@@ -983,7 +985,8 @@ class GroupedMatmulFp8Call(_Call):
                  "group_list must be [G, 2]")
             _check_tensor(group_list, "group_list", dev, (torch.int64,))
         _req(out_dtype in _OUT_CODE, f"out_dtype {out_dtype} is not float16, bfloat16, float32 or float8_e4m3fn")
-        cols = N // 2 if epilogue == FFNWB_EPI_SWIGLU else N
+        epilogue = int(epilogue) | (FFNWB_EPI_EXACT if exact else 0)
+        cols = N // 2 if epilogue & ~FFNWB_EPI_EXACT == FFNWB_EPI_SWIGLU else N
         out = dict(out or {})
         want = {"y": ((R, cols), out_dtype)}
         if out_dtype == _FP8:
@@ -996,7 +999,7 @@ class GroupedMatmulFp8Call(_Call):
             if k not in out:
                 out[k] = torch.empty(shape, dtype=dtype, device=dev)
         d = GroupedMatmulFp8Desc()
-        d.epilogue, d.out_dtype = int(epilogue), _OUT_CODE[out_dtype]
+        d.epilogue, d.out_dtype = epilogue, _OUT_CODE[out_dtype]
         d.num_rows, d.in_features, d.out_features, d.num_experts = R, K, N, E
         d.num_groups = group_list.shape[0] if group_list is not None else 0
         d.x_row_stride, d.x_scale_stride = _row_bytes(x), _row_elems(x_scale)

@@ -24,6 +24,7 @@ FFNWB_DT_FP8_E4M3 = 6
 FFNWB_FP8_BLOCK = 128
 FFNWB_EPI_NONE = 0
 FFNWB_EPI_SWIGLU = 1
+FFNWB_EPI_EXACT = 256
 
 FFNWB_CTX_BYTES = 1024
 FFNWB_CTX_SHAPE = 1

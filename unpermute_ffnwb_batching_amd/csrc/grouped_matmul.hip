@@ -446,9 +446,10 @@ static double expected_us(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t
 int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   if (d == nullptr || d->x == nullptr || d->x_scale == nullptr || d->w == nullptr || d->w_scale == nullptr || d->y == nullptr)
     return FFNWB_ERR_PARAM_NULLPTR;
-  const bool quant = d->out_dtype == FFNWB_DT_FP8_E4M3, swiglu = d->epilogue == FFNWB_EPI_SWIGLU;
+  const int32_t epilogue = d->epilogue & ~FFNWB_EPI_EXACT;
+  const bool quant = d->out_dtype == FFNWB_DT_FP8_E4M3, swiglu = epilogue == FFNWB_EPI_SWIGLU;
   if (quant && d->y_scale == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
-  if (d->epilogue != FFNWB_EPI_NONE && !swiglu) return FFNWB_ERR_PARAM_INVALID;
+  if (epilogue != FFNWB_EPI_NONE && !swiglu) return FFNWB_ERR_PARAM_INVALID;
   if (d->out_dtype != FFNWB_DT_FP16 && d->out_dtype != FFNWB_DT_BF16 && d->out_dtype != FFNWB_DT_FP32 && !(quant && swiglu))
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t big = int64_t{1} << 18;
@@ -478,7 +479,9 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
       reinterpret_cast<uintptr_t>(d->y) % elt != 0)
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t groups = d->group_list != nullptr ? d->num_groups : 1;
-  const bool fast = !quant && d->out_dtype != FFNWB_DT_FP32;
+  // The e4m3 instructions drop bits (fp8_block.hpp), mostly far below the rounding to 16 bits; FP32
+  // results and the scales of e4m3 ones would show it, and a caller can refuse it.
+  const bool fast = !quant && d->out_dtype != FFNWB_DT_FP32 && (d->epilogue & FFNWB_EPI_EXACT) == 0;
   auto shape = [&](int64_t bm, int64_t parts) {  // negative bm: direct; the result: workgroups, of the larger launch
     p->tile = bm > 0, p->bm = bm > 0 ? bm : -bm;
     p->part_blocks = (p->kb + parts - 1) / parts;
@@ -517,6 +520,7 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   }
   if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
   shape(best_bm, best_parts);
+  p->swiglu = swiglu;
   p->fast = p->tile && fast;
   p->pitch = p->parts > 1 ? (p->N + 7) / 8 * 8 : p->F;
   p->ws_bytes = 0;
@@ -561,14 +565,20 @@ static bool launch_tile_shape(const MmArgs& a, const MatmulPlan& p, hipStream_t 
   return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles + more)), dim3(S::kThreads), S::kLds, s, b, e, a);
 }
 
-template <class T, int EPI, bool kQuant = false, bool kFast = !kQuant && T::kBytes == 2>
+template <class T, int EPI, bool kQuant = false, bool kFast = false>
 static bool launch_tile(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
-  if constexpr (T::kBytes == 2) {
+  if constexpr (T::kBytes == 2 && kFast) {
     if (p.bm == 256) return launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 8>(a, p, s, b, e);
   }
   return p.bm == 128  ? launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 4>(a, p, s, b, e)
          : p.bm == 64 ? launch_tile_shape<T, EPI, kQuant, kFast, 2, 4, 2>(a, p, s, b, e)
                       : launch_tile_shape<T, EPI, kQuant, kFast, 1, 4, 2>(a, p, s, b, e);
+}
+
+// 16-bit results.
+template <class T, int EPI>
+static bool launch_tile16(const MmArgs& a, const MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  return p.fast ? launch_tile<T, EPI, false, true>(a, p, s, b, e) : launch_tile<T, EPI>(a, p, s, b, e);
 }
 
 int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan& p, void* ws, hipStream_t s) {
@@ -609,19 +619,19 @@ int launch_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, const MatmulPlan
     m.unit = ((at | p.F * elt) & 15) == 0 ? 16 : ((at | p.F * elt) & 3) == 0 ? 4 : 0;
   }
   void* product_end = p.join ? nullptr : e;
-  const bool swiglu = d->epilogue == FFNWB_EPI_SWIGLU, quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
+  const bool swiglu = p.swiglu, quant = d->out_dtype == FFNWB_DT_FP8_E4M3;
   bool ok;
   if (p.parts > 1) {
     ok = p.fast ? launch_tile<TF32, FFNWB_EPI_NONE, false, true>(m, p, s, b, product_end)
                 : launch_tile<TF32, FFNWB_EPI_NONE>(m, p, s, b, product_end);
   } else if (p.tile && swiglu) {
     ok = quant                ? launch_tile<TF32, FFNWB_EPI_SWIGLU, true>(m, p, s, b, e)
-         : dt == FFNWB_DT_FP16 ? launch_tile<TF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)
-         : dt == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)
+         : dt == FFNWB_DT_FP16 ? launch_tile16<TF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)
+         : dt == FFNWB_DT_BF16 ? launch_tile16<TBF16, FFNWB_EPI_SWIGLU>(m, p, s, b, e)
                                : launch_tile<TF32, FFNWB_EPI_SWIGLU>(m, p, s, b, e);
   } else if (p.tile) {
-    ok = dt == FFNWB_DT_FP16   ? launch_tile<TF16, FFNWB_EPI_NONE>(m, p, s, b, e)
-         : dt == FFNWB_DT_BF16 ? launch_tile<TBF16, FFNWB_EPI_NONE>(m, p, s, b, e)
+    ok = dt == FFNWB_DT_FP16   ? launch_tile16<TF16, FFNWB_EPI_NONE>(m, p, s, b, e)
+         : dt == FFNWB_DT_BF16 ? launch_tile16<TBF16, FFNWB_EPI_NONE>(m, p, s, b, e)
                                : launch_tile<TF32, FFNWB_EPI_NONE>(m, p, s, b, e);
   } else if (swiglu) {
     ok = dt == FFNWB_DT_FP16   ? launch_direct<TF16, FFNWB_EPI_SWIGLU>(m, p, s, b, product_end)

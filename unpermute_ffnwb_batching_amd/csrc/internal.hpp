@@ -131,6 +131,7 @@ struct MatmulPlan {
   int64_t xs = 0, xss = 0, ys = 0, yss = 0;    // row strides: bytes, elements, bytes, elements
   bool tile = false;                           // through LDS, else straight to registers
   int64_t bm = 0;                              // rows of a tile
+  bool swiglu = false;
   bool fast = false;                           // e4m3 matrix instructions (tiles only)
   int64_t parts = 1, part_blocks = 0;          // parts of K, and 128-blocks of each
   int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles (times the parts)

@@ -33,7 +33,6 @@ struct LayerArgs {
   int32_t ctiles;             // 16-column tiles of F
   int32_t groups_max;         // most groups of launch 2
   int32_t id64;
-  bool lanes;                 // at most 64 slots: one to a lane
   int32_t scale_dtype;
   int64_t xs, ys, is, ss, ms;
   const char* x;
@@ -369,7 +368,7 @@ __global__ __launch_bounds__((kSplit == 1 ? 4 : kSplit) * kWave) void layer_up_k
   const int32_t c = (static_cast<int32_t>(blockIdx.x) - 1 - rank * per) * (kSplit == 1 ? 4 : 1) +
                     (kSplit == 1 ? static_cast<int32_t>(threadIdx.x / kWave) : 0);
   const int32_t lane = threadIdx.x % kWave;
-  if (blockIdx.x != 0 && a.lanes) {
+  if (blockIdx.x != 0 && a.T * a.K <= kWave) {
     // Up to 64 slots are one to a lane, and every wave finds the workgroup's expert (the rank-th
     // in the order of the slots) by itself: two barriers and a pass through LDS less.
     int32_t* list = lists[threadIdx.x / kWave];
@@ -678,7 +677,6 @@ int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStrea
   a.hb = (a.H + kBlk - 1) / kBlk, a.fb = (a.F + kBlk - 1) / kBlk, a.nb13 = (2 * a.F + kBlk - 1) / kBlk;
   a.ctiles = a.F / 16;
   a.groups_max = static_cast<int32_t>(p.groups);
-  a.lanes = p.lanes;
   a.id64 = d->id_dtype == FFNWB_DT_INT64;
   a.scale_dtype = d->scale_dtype;
   a.xs = p.xs, a.ys = p.ys, a.is = p.is, a.ss = p.ss, a.ms = p.ms;

@@ -606,7 +606,8 @@ int moe_grouped_matmul_fp8(const moe_grouped_matmul_fp8_desc* d, void* workspace
  * Products with weights stand for the weight times its 128 x 128 block's scale.  Ids outside
  * [0, E) (the -1 of moe_update_expert) and inactive slots take no part; a token without any
  * gets a row of zeros.  Activations keep the 16-bit type of x, h is held to 16 significant
- * bits, sums in FP32, and y is rounded once.
+ * bits (as the sum of two BF16 numbers, so that an infinite BF16 weight of w2 may give NaN
+ * instead of an infinity), sums in FP32, and y is rounded once.
  * ------------------------------------------------------------------------------------------ */
 typedef struct moe_layer_desc {
   int32_t dtype;             /* of x and y: FFNWB_DT_FP16 or _BF16 */

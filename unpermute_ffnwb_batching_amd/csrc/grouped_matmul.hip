@@ -153,7 +153,8 @@ __global__ __launch_bounds__(kTableThreads) void mm_table_kernel(MmArgs a, int32
 // 8 row tiles by all column tiles at a time, row tiles first, so that workgroups running
 // together share rows of x and of w.  kHalve, for tiles of which a CU holds one: where the last
 // round of tiles would leave half of the CUs idle, each of its tiles is two of half the rows (8191
-// rows by 7168 columns over 5120, 3.5 rounds of 256 x 256: 316 us without, 291 us with).
+// rows by 7168 columns over 5120, 3.5 rounds of 256 x 256: 316 us without, 291 us with, on one box;
+// 4096 by 4096 over 4096, one full round, pays 0.8 of 68 us for the test).
 constexpr int32_t kXcds = 8, kXcdCus = 32;
 constexpr int kHalvedFragments = 4;  // least row fragments of a wave whose tiles are halved
 
@@ -217,7 +218,7 @@ __device__ __forceinline__ void store4(char* row, int64_t n, int64_t end, const 
 // rows by 16 columns (SwiGLU: 16 gate and the 16 up columns that go with them); its waves take
 // the 128-column blocks of K in turn, straight from memory to registers, a wave's next block
 // ahead of its present one, and their totals are added in wave order.  One row by 4096 columns
-// over 7168 takes 7.3 us, 4.0 TB/s of weights (a copy moves 4.8): three dependent loads (group,
+// over 7168 takes 7.5 us, 3.9 TB/s of weights (a copy moves 4.8): three dependent loads (group,
 // operands, scales), then the join of 16 waves.  With 64 columns and 4 waves to a workgroup
 // it was 16.2 us: too few loads on their way.
 
@@ -414,9 +415,11 @@ static int direct_waves(int64_t tiles, int64_t kb, int64_t bm) {
   return waves;
 }
 
-// Microseconds that a product takes with the given kernel and tile rows: rounds of workgroups
-// that fit the chip together, times what one needs for its blocks of K; the figures (us per
-// block and round) are measured.  A group's last tile is counted as 0.58 of one.
+// Microseconds that a product takes with the given kernel and tile rows, as far as the choice
+// between them needs it: rounds of workgroups that fit the chip together, times what one needs for
+// its blocks of K.  The figures are fitted to the times of whole calls, and are not those of the
+// parts (a round of 256-row tiles takes 15 us besides its blocks, the fit says 5.5).  A group's last tile is
+// counted as 0.58 of one.  The launch that lists the row tiles is not counted.
 static double expected_us(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t groups, bool swiglu, bool quant, bool fast,
                           bool tile, int64_t bm, int64_t parts) {
   const int64_t kb = (K + 127) / 128, some = groups < rows ? groups : rows;
@@ -492,13 +495,15 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
     p->join_groups = (p->bm * fb + kJoinThreads / 16 - 1) / (kJoinThreads / 16);
     return p->mtiles * (p->join && p->join_groups > p->ntiles ? p->join_groups : p->ntiles);
   };
-  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  Over
-  // 480 random sizes (1 to 16384 rows, K and N to 8192, 0 to 256 groups) the choice is 1.9% slower
-  // than the best of the shapes on average; a fixed rule (the largest tile that the groups fill
-  // and that gives every CU one) was 15%.  Parts are what fills the chip with a long K and few tiles:
-  // 256 rows by 2048 columns over 7168 take 39.9 us in the best shape without and 17.7 us in 8 parts,
-  // 128 by 8192 over 8192 45.5 and 24.3 us; with 1536 columns over 1536 they cost 0.2 to 3 us.  256 rows of x, and the gate rows of w, have to be
-  // inside the 32-bit offsets of the tile kernel.
+  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  On 220
+  // random sizes that the fit has not seen (1 to 16384 rows, K and N to 8192, 0 to 256 groups) the
+  // choice is 3.6% slower than the best of the shapes on average, more than 10% in 22 of them and 1.7
+  // times at worst; a fixed rule (the largest tile that the groups fill and that gives every CU one)
+  // was 15%.  Parts are what fills the chip with a long K and few tiles: 256 rows by 2048 columns over
+  // 7168 take 39.9 us in the best shape without and 17.7 us in 8 parts, 128 by 8192 over 8192 45.5 and
+  // 24.3 us; with 1536 columns over 1536 they cost 0.2 to 3 us.  256 rows of x, and the gate rows of
+  // w, have to be inside the 32-bit offsets of the tile kernel.  Tiles of 256 rows are for e4m3
+  // instructions alone: with widened operands a wave has 67 to 76 registers too few for them.
   const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
   const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup
   double best = 0;
@@ -525,7 +530,9 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   p->pitch = p->parts > 1 ? (p->N + 7) / 8 * 8 : p->F;
   p->ws_bytes = 0;
   Carve c;
-  // The list in every workgroup costs each about 1 us, two to a CU at a time; the launch 4 us.
+  // The list in every workgroup costs each about 1 us, two to a CU at a time; the launch 3 to 5 us with
+  // 128 or 256 groups.  A thread writes the tiles of a group one after another, though: 13119 rows of two groups by 78 columns over 80 take 22 us, in 820 row tiles of 16, where 64-row
+  // tiles without the launch would take 6.4.
   p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > 16 * kCus));
   if (p->table) {
     c.take<int32_t>(1);

@@ -14,9 +14,10 @@
 // as much accuracy as the rounding of y itself, FP16 could overflow, and the second product is
 // free while the weights are being read.
 //
-// Bound by memory: 16 tokens with 9 of 257 experts (hidden 7168, inter 1024) take 425 us, 5.1 TB/s;
-// 64 with 8 of 64 in BF16 (4096, 1024) 326 us, 4.9; one token with 9 (7168, 2048) 81 us, 4.7.  A
-// toy layer takes 10 us, the two launches.
+// Bound by memory: 16 tokens with 9 of 256 experts (hidden 7168, inter 1024) take 432 us, 5.0 TB/s;
+// 64 with 8 of 64 in BF16 (4096, 1024) 327 us, 4.9; one token with 9 (7168, 2048) 79 us, 4.8.  64
+// tokens with 8 of 64 in e4m3 (4096, 1024) take 253 us, 3.2 TB/s.  A toy layer takes 10 us, the two
+// launches.
 #include "fp8_block.hpp"
 #include "internal.hpp"
 

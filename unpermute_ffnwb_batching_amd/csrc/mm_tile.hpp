@@ -8,12 +8,14 @@
 // 16 rows a matrix operand reads at once over all banks.  The lanes of a copy write adjacent LDS
 // addresses, so the permutation is applied to the addresses they read.
 //
-// What bounds it, measured on 256 rows: a step takes 1.75 us; its copies alone (64 KB a CU) 1.7,
-// its arithmetic alone 1.5 (2.86 PFLOP/s, the card's own limit for these instructions).  With weights
-// fetched one step ahead instead of two, 128 rows took 16% and 64 rows 19% longer.  Filling
-// the buffers and storing the results are 16 us a round of tiles.  8191 rows by 7168 columns over
-// 5120: 291 us, 2.07 PFLOP/s.  Widened operands (FP32 and e4m3 results): 131072 rows by 2048 over
-// 4096 2240 us, 0.98 PFLOP/s; there the arithmetic alone takes 2170, without the conversions 1835.
+// What bounds it, measured on 256 rows: a step takes 1.64 to 1.73 us (4096 rows by 4096 columns, one
+// round of tiles, over 1024 to 8192); its copies alone (64 KB a CU) 1.7, its arithmetic alone 1.5
+// (2.86 PFLOP/s; a library's e4m3 product of 16384^3, without scales, runs at 3.1).  With weights
+// fetched one step ahead instead of two, 128 rows took 16% and 64 rows 19% longer.  Besides its steps
+// a call of one round takes 15 us: the launch, filling the buffers, storing the results.  8191 rows by
+// 7168 columns over 5120: 297 to 304 us, 2.0 PFLOP/s.  Widened operands (FP32, e4m3 and exact results):
+// the same product 530 us, 131072 rows by 2048 over 4096 2210 to 2250 us, 0.99 PFLOP/s; there the
+// arithmetic alone takes 2170, without the conversions 1835.
 // 256 groups of 17 rows (32-row tiles, two workgroups to a CU) run at 5.4 TB/s of weights.
 #pragma once
 

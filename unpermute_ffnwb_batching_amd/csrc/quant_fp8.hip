@@ -3,8 +3,9 @@
 // A block of 128 elements is taken by 16 lanes, 8 elements each: one 16-byte load per lane of
 // 16-bit rows (two of FP32 rows), a maximum over the 16 lanes, 8 quotients, one 8-byte store.
 // Blocks are numbered row by row, so a wave's 4 blocks are adjacent in memory whatever the row
-// length.  Bound by memory: 4608 rows of 7168 BF16 take 19.7 us, 100 MB at 5.1 TB/s (a plain copy
-// moves 4.8); the quotients by multiplication and FMA instead of division were worth 26%, and two
+// length.  Bound by memory: 4377 rows of 7168 BF16 take 19.7 us, 95 MB at 4.8 TB/s, which is what a
+// plain copy moves; rows whose width or alignment allows no wide access go element by element, 4608
+// of 7167 in 49 us.  The quotients by multiplication and FMA instead of division were worth 26%, and two
 // or four blocks to a thread's lane group, one after another, gained nothing.
 #include "fp8_block.hpp"
 #include "internal.hpp"

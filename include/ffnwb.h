@@ -36,6 +36,12 @@
  *                      with SwiGLU and the quantising of its result.
  *   moe_layer       -- the whole expert layer (both products, SwiGLU, the weighted sum
  *                      over a token's experts) for at most 64 tokens.
+ *   moe_rmsnorm_quant -- the norm before the experts: the residual's addition, the
+ *                      root-mean-square norm, and INT8 or e4m3 rows with their scales.
+ *   moe_quant_int8  -- rows to INT8 with an FP32 scale for each row, as the batching's INT8
+ *                      mode carries them.
+ *   moe_grouped_matmul_int8 -- the experts' products on such rows, with a scale for each
+ *                      token and each weight channel.
  *
  * Conventions shared by every entry point
  *   - All array pointers are DEVICE pointers owned by the caller.  The library
@@ -84,7 +90,8 @@ extern "C" {
 /* Element types. 0..2 are the batching page's tokenDtype values. */
 #define FFNWB_DT_FP16 0
 #define FFNWB_DT_BF16 1
-#define FFNWB_DT_INT8 2 /* batching: INT8 data with an FP32 dynamic scale per row; permute: 1-byte elements */
+#define FFNWB_DT_INT8 2 /* batching and the INT8 operators: INT8 data with an FP32 dynamic scale per row;
+                           permute: 1-byte elements */
 #define FFNWB_DT_FP32 3 /* unpermute and permute */
 #define FFNWB_DT_INT32 4 /* moe_update_expert ids */
 #define FFNWB_DT_INT64 5 /* moe_update_expert ids */
@@ -665,6 +672,174 @@ int moe_layer_plan(const moe_layer_desc* d, moe_layer_plan_info* info);
 /* Validates again, then enqueues the layer on `stream`. */
 int moe_layer(const moe_layer_desc* d, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Rows to INT8 with a scale for each row: the rows of the batching's INT8 mode and the input of
+ * moe_grouped_matmul_int8.
+ *
+ * For row i:
+ *   scale[i] = max(a / 127, 2^-126), a = the largest |x| of the row (FP32 division, rounded to
+ *              nearest)
+ *   q[i, h]  = the whole number nearest to x[i, h] / scale[i] (the FP32 quotient, rounded to
+ *              nearest; then to a whole number, ties to even), in [-127, 127].
+ * A row holding a NaN gets scale NaN and zeros; one holding an infinity (and no NaN) gets scale
+ * inf and zeros, so every value it stands for is NaN.  Rows i >= *actual_rows are not written.
+ * The rows may be packed as the batching's token_data holds them (H bytes, then the scale):
+ * q_row_stride = H + 4, scale = q + H, scale_row_stride = (H + 4) / 4, H a multiple of 4.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct moe_quant_int8_desc {
+  int32_t dtype;             /* of x: FFNWB_DT_FP16, _BF16 or _FP32 */
+  int32_t reserved0;         /* must be 0 */
+  int64_t num_rows;          /* R in [0, 2^24] */
+  int64_t hidden;            /* H in (0, 2^20] */
+  int64_t x_row_stride;      /* bytes, a multiple of the element size; 0 = H * element size */
+  int64_t q_row_stride;      /* bytes; 0 = H */
+  int64_t scale_row_stride;  /* elements; 0 = 1 */
+  const void* x;             /* [R, H] */
+  const int64_t* actual_rows;/* [1] rows to take (clamped to [0, R]), e.g. the batching's
+                                actual_token_num; NULL = R */
+  void* q;                   /* [R, H] INT8 */
+  float* scale;              /* [R], 4-byte aligned */
+  /* Optional timing hooks (hipEvent_t) around the kernel, as in ffnwb_batching_desc. */
+  void* ev_quant_begin;
+  void* ev_quant_end;
+} moe_quant_int8_desc;
+
+/* Validates *d and returns the workspace size (0) (host only).  Errors:
+   FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes, x, q or scale NULL), FFNWB_ERR_PARAM_INVALID (dtype,
+   sizes, a stride below its row or above 2^32, x or scale not aligned to its element size,
+   reserved0 != 0). */
+int moe_quant_int8_workspace_size(const moe_quant_int8_desc* d, size_t* ws_bytes);
+
+/* Validates again, then enqueues the quantising on `stream` (one launch). */
+int moe_quant_int8(const moe_quant_int8_desc* d, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The norm before the experts: residual addition, root-mean-square norm, 8-bit rows.
+ *
+ * For row i, in FP32:
+ *   s[h] = x[i, h] + residual[i, h]               (s = x without a residual)
+ *   r    = 1 / sqrt(mean over h of s[h]^2 + epsilon)
+ *   n[h] = (s[h] * gamma[h]) * r
+ * residual_out[i] = s and y[i] = n, each rounded once to dtype; the norm takes s before that
+ * rounding, and q takes n before it:
+ *   q_dtype FFNWB_DT_INT8:     q[i], scale[i] as moe_quant_int8 makes them of n
+ *   q_dtype FFNWB_DT_FP8_E4M3: q[i], scale[i, 0 ..] as moe_quant_fp8 makes them of n
+ * A NaN or an infinity in s makes r NaN or 0, and with it n of the row NaN, or NaN in the
+ * infinity's place and 0 elsewhere.  Squares are summed in FP32: where the sum passes its range
+ * (|s| beyond 1e19 / sqrt(H)) r is 0.  Rows i >= *actual_rows are not written.
+ * residual_out may be residual itself (same address and stride): each element is read before it
+ * is written.  For packed INT8 rows see moe_quant_int8.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct moe_rmsnorm_quant_desc {
+  int32_t dtype;             /* of x, residual, residual_out and y: FFNWB_DT_FP16, _BF16 or _FP32 */
+  int32_t gamma_dtype;       /* = dtype, or FFNWB_DT_FP32 */
+  int32_t q_dtype;           /* FFNWB_DT_INT8 or FFNWB_DT_FP8_E4M3 */
+  float epsilon;             /* finite, at least 2^-126 */
+  int64_t num_rows;          /* R in [0, 2^24] */
+  int64_t hidden;            /* H in (0, 2^20] */
+  int64_t x_row_stride;      /* this and the next three: bytes, a multiple of the element size; 0 = H * element size */
+  int64_t residual_row_stride;
+  int64_t residual_out_row_stride;
+  int64_t y_row_stride;
+  int64_t q_row_stride;      /* bytes; 0 = H */
+  int64_t scale_row_stride;  /* elements; 0 = 1 (INT8) or ceil(H / 128) (e4m3) */
+
+  /* Inputs. */
+  const void* x;             /* [R, H] */
+  const void* residual;      /* [R, H] of dtype, or NULL */
+  const void* gamma;         /* [H] of gamma_dtype */
+  const int64_t* actual_rows;/* [1] rows to take (clamped to [0, R]); NULL = R */
+
+  /* Outputs. */
+  void* residual_out;        /* [R, H] of dtype: NULL exactly when residual is */
+  void* y;                   /* [R, H] of dtype, or NULL */
+  void* q;                   /* [R, H] of q_dtype */
+  float* scale;              /* [R] (INT8) or [R, ceil(H / 128)] (e4m3) */
+
+  /* Optional timing hooks (hipEvent_t) around the kernel, as in ffnwb_batching_desc. */
+  void* ev_norm_begin;
+  void* ev_norm_end;
+} moe_rmsnorm_quant_desc;
+
+/* Validates *d and returns the workspace size (0) (host only).  Errors:
+   FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes, x, gamma, q or scale NULL, or one of residual and
+   residual_out without the other), FFNWB_ERR_PARAM_INVALID (a code, size or epsilon outside the
+   set above, a stride below its row or above 2^32, a pointer not aligned to its element size,
+   residual_out = residual with another stride). */
+int moe_rmsnorm_quant_workspace_size(const moe_rmsnorm_quant_desc* d, size_t* ws_bytes);
+
+/* Validates again, then enqueues the norm on `stream` (one launch). */
+int moe_rmsnorm_quant(const moe_rmsnorm_quant_desc* d, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The experts' products on INT8 rows, with scales for each token and channel.
+ *
+ * Rows and groups as in moe_grouped_matmul_fp8 (the batching's y, dynamic_scale and group_list
+ * in INT8 mode).  For a row i of expert e:
+ *   p[i, n] = (c * x_scale[i]) * w_scale[e, n],  c = sum_k x[i, k] * w[e, n, k]
+ * c is exact (32-bit whole numbers, which K cannot overflow), then rounded to FP32.
+ * FFNWB_EPI_NONE:   y[i, n] = p[i, n], n < N.
+ * FFNWB_EPI_SWIGLU: N = 2 F (gate rows of w, then up rows),
+ *   y[i, f] = g * sigmoid(g) * u, g = p[i, f], u = p[i, F + f], f < F.
+ * y is rounded once to out_dtype; with out_dtype FFNWB_DT_INT8 (SwiGLU only) y and y_scale are
+ * the FP32 rows quantised as moe_quant_int8 does.
+ *
+ * Without a group_list (NULL, num_groups = 0, num_experts = 1) all R rows are one group.  A pair
+ * with a count <= 0 has no rows; a pair whose key lies outside [0, E) has rows, and they are left
+ * unwritten; counts past R rows are cut.  Rows of no group are left unwritten.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct moe_grouped_matmul_int8_desc {
+  int32_t epilogue;          /* FFNWB_EPI_NONE or FFNWB_EPI_SWIGLU */
+  int32_t out_dtype;         /* FFNWB_DT_FP16, _BF16, _FP32; _INT8 with SwiGLU */
+  int64_t num_rows;          /* R in [0, 2^24] */
+  int64_t in_features;       /* K in (0, 131056], a multiple of 16 */
+  int64_t out_features;      /* N in (0, 2^18], rows of one expert's w; SwiGLU: a multiple of 32 */
+  int64_t num_experts;       /* E in [1, 8192] */
+  int64_t num_groups;        /* pairs of group_list, in [1, 8192]; 0 without one */
+  int64_t x_row_stride;      /* bytes, a multiple of 16; 0 = K */
+  int64_t x_scale_stride;    /* elements between rows; 0 = 1 */
+  int64_t y_row_stride;      /* bytes, a multiple of the element size; 0 = dense */
+  int64_t y_scale_stride;    /* elements between rows; 0 = 1 */
+
+  /* Inputs. */
+  const void* x;             /* [R, K] INT8, 16-byte aligned */
+  const float* x_scale;      /* [R] */
+  const void* w;             /* [E, N, K] INT8, dense, 16-byte aligned */
+  const float* w_scale;      /* [E, N], dense */
+  const int64_t* group_list; /* [num_groups, 2] or NULL */
+
+  /* Outputs. */
+  void* y;                   /* [R, N] (SwiGLU: [R, F]) of out_dtype */
+  float* y_scale;            /* [R] (FFNWB_DT_INT8 only) */
+
+  /* Optional timing hooks (hipEvent_t): `begin` at the product's kernel, `end` at the
+     completion of the call's last kernel, as in moe_grouped_matmul_fp8_desc. */
+  void* ev_matmul_begin;
+  void* ev_matmul_end;
+} moe_grouped_matmul_int8_desc;
+
+/* Validates *d and returns the workspace size in bytes (host only).  Errors:
+   FFNWB_ERR_PARAM_NULLPTR (d, ws_bytes or a required array NULL), FFNWB_ERR_PARAM_INVALID
+   (a code, range, multiple or alignment above violated, a stride below its row or above
+   2^32; group_list given without num_groups or the other way round; num_experts != 1 without
+   a group_list; more tiles of output than the 2^22 - 8 workgroups of a launch, which is never
+   so while (ceil(R / 64) + num_groups) * max(ceil(F / 16), 16), F = N without SwiGLU, is no more). */
+int moe_grouped_matmul_int8_workspace_size(const moe_grouped_matmul_int8_desc* d, size_t* ws_bytes);
+
+/* Which kernels a call of *d runs, for reports and tests (host only; the errors of
+   moe_grouped_matmul_int8_workspace_size). */
+typedef struct moe_grouped_matmul_int8_plan_info {
+  int32_t lds_tiles;         /* 1: tiles of 256 columns through LDS; 0: 16 columns straight to registers */
+  int32_t tile_rows;         /* 32, 64, 128 or 256; 16, 32 or 64 */
+  int32_t k_parts;           /* parts of K, added by a launch of their own when more than one */
+  int32_t listed;            /* 1: the row tiles are listed by a launch of their own */
+} moe_grouped_matmul_int8_plan_info;
+
+int moe_grouped_matmul_int8_plan(const moe_grouped_matmul_int8_desc* d, moe_grouped_matmul_int8_plan_info* info);
+
+/* Validates again, then enqueues the product on `stream`. */
+int moe_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, void* workspace, size_t ws_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* ffnwb_status_string(int status);
 
@@ -680,6 +855,9 @@ size_t moe_update_expert_desc_size(void);
 size_t moe_quant_fp8_desc_size(void);
 size_t moe_grouped_matmul_fp8_desc_size(void);
 size_t moe_layer_desc_size(void);
+size_t moe_quant_int8_desc_size(void);
+size_t moe_rmsnorm_quant_desc_size(void);
+size_t moe_grouped_matmul_int8_desc_size(void);
 
 #ifdef __cplusplus
 }

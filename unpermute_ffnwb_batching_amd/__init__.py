@@ -14,12 +14,16 @@ The names mirror the C ABI:
 * ``moe_quant_fp8_workspace_size`` / ``moe_quant_fp8``
 * ``moe_grouped_matmul_fp8_workspace_size`` / ``moe_grouped_matmul_fp8_plan`` / ``moe_grouped_matmul_fp8``
 * ``moe_layer_workspace_size`` / ``moe_layer_plan`` / ``moe_layer``
+* ``moe_rmsnorm_quant_workspace_size`` / ``moe_rmsnorm_quant``
+* ``moe_quant_int8_workspace_size`` / ``moe_quant_int8``
+* ``moe_grouped_matmul_int8_workspace_size`` / ``moe_grouped_matmul_int8_plan`` / ``moe_grouped_matmul_int8``
 * ``ffnwb_status_string``, ``ffnwb_abi_version``
 
 ``ffnwb_batching``, ``moe_unpermute`` and the other ``moe_`` calls take torch tensors,
 allocate any output or workspace the caller did not pass, fill the C descriptor and
 enqueue the call on the current stream.  ``BatchingCall`` / ``UnpermuteCall`` /
-``PermuteCall`` / ``QuantFp8Call`` / ``GroupedMatmulFp8Call`` / ``LayerCall`` build the
+``PermuteCall`` / ``QuantFp8Call`` / ``GroupedMatmulFp8Call`` / ``LayerCall`` /
+``RmsNormQuantCall`` / ``QuantInt8Call`` / ``GroupedMatmulInt8Call`` build the
 descriptor once for repeated launches (serving loops, benchmarks, graph capture).
 
 The library must be built (``python -m unpermute_ffnwb_batching_amd.build``); importing
@@ -41,7 +45,8 @@ from ._abi import (FFNWB_OK, FFNWB_ERR_PARAM_NULLPTR, FFNWB_ERR_PARAM_INVALID,  
                    FFNWB_CTX_BUFFER, FFNWB_DT_INT32, FFNWB_DT_INT64, BatchingDesc, BatchingCtxDesc,
                    UnpermuteDesc, PermuteDesc, UpdateExpertDesc, FFNWB_DT_FP8_E4M3, FFNWB_FP8_BLOCK,
                    FFNWB_EPI_NONE, FFNWB_EPI_SWIGLU, FFNWB_EPI_EXACT, QuantFp8Desc, GroupedMatmulFp8Desc, LayerDesc,
-                   GroupedMatmulFp8PlanInfo, LayerPlanInfo)
+                   GroupedMatmulFp8PlanInfo, LayerPlanInfo, QuantInt8Desc, RmsNormQuantDesc, GroupedMatmulInt8Desc,
+                   GroupedMatmulInt8PlanInfo)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libffnwb.so")
 _lib = None
@@ -74,7 +79,8 @@ def lib():
         L.moe_update_expert_workspace_size.argtypes = [ctypes.POINTER(UpdateExpertDesc), ctypes.POINTER(sz)]
         L.moe_update_expert.argtypes = [ctypes.POINTER(UpdateExpertDesc), vp, sz, vp]
         for name, desc in (("moe_quant_fp8", QuantFp8Desc), ("moe_grouped_matmul_fp8", GroupedMatmulFp8Desc),
-                           ("moe_layer", LayerDesc)):
+                           ("moe_layer", LayerDesc), ("moe_quant_int8", QuantInt8Desc),
+                           ("moe_rmsnorm_quant", RmsNormQuantDesc), ("moe_grouped_matmul_int8", GroupedMatmulInt8Desc)):
             getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(desc), ctypes.POINTER(sz)]
             getattr(L, name + "_workspace_size").restype = ctypes.c_int
             getattr(L, name).argtypes = [ctypes.POINTER(desc), vp, sz, vp]
@@ -83,7 +89,8 @@ def lib():
             if getattr(L, name + "_desc_size")() != ctypes.sizeof(desc):
                 raise RuntimeError("libffnwb descriptor layout does not match the Python binding")
         for name, desc, info in (("moe_grouped_matmul_fp8_plan", GroupedMatmulFp8Desc, GroupedMatmulFp8PlanInfo),
-                                 ("moe_layer_plan", LayerDesc, LayerPlanInfo)):
+                                 ("moe_layer_plan", LayerDesc, LayerPlanInfo),
+                                 ("moe_grouped_matmul_int8_plan", GroupedMatmulInt8Desc, GroupedMatmulInt8PlanInfo)):
             getattr(L, name).argtypes = [ctypes.POINTER(desc), ctypes.POINTER(info)]
             getattr(L, name).restype = ctypes.c_int
         for f in ("ffnwb_batching_workspace_size", "ffnwb_batching", "ffnwb_batching_ctx_workspace_size",
@@ -1091,3 +1098,200 @@ def moe_layer(x, expert_ids, w13, w2, *, stream=None, **kw):
     dict(y), allocated on that stream."""
     with _on(stream):
         return LayerCall(x, expert_ids, w13, w2, **kw).run(stream)
+
+
+# ----------------------------------------------------------------------------- INT8 rows
+
+_Q_CODE = {torch.int8: FFNWB_DT_INT8, _FP8: FFNWB_DT_FP8_E4M3}
+_OUT8_CODE = {**_FLOAT_CODE, torch.int8: FFNWB_DT_INT8}
+
+
+def moe_quant_int8_workspace_size(desc):
+    return _workspace_size("moe_quant_int8", desc)
+
+
+def moe_rmsnorm_quant_workspace_size(desc):
+    return _workspace_size("moe_rmsnorm_quant", desc)
+
+
+def moe_grouped_matmul_int8_workspace_size(desc):
+    return _workspace_size("moe_grouped_matmul_int8", desc)
+
+
+def moe_grouped_matmul_int8_plan(desc):
+    """Which kernels a call runs: dict(lds_tiles, tile_rows, k_parts, listed)."""
+    return _plan("moe_grouped_matmul_int8_plan", desc, GroupedMatmulInt8PlanInfo())
+
+
+def _check_scales(t, name, device, rows):
+    """A 1-D float32 tensor of a scale for each row, any distance >= 1 apart."""
+    _check_tensor(t, name, device, (torch.float32,), (rows,), contiguous=False)
+    _req(rows <= 1 or t.stride(0) >= 1, f"{name} must not be broadcast")
+
+
+def _outputs(out, want, device):
+    """The caller's outputs checked against want {name: (shape, dtype)}, the missing ones allocated."""
+    out = dict(out or {})
+    for k, t in out.items():
+        _req(k in want, f"unknown output {k!r}")
+        shape, dtype = want[k]
+        if len(shape) == 1:
+            _check_scales(t, f"out[{k!r}]", device, shape[0])
+        else:
+            _check_rows(t, f"out[{k!r}]", device, (dtype,))
+            _req(tuple(t.shape) == shape, f"out[{k!r}] must be {shape}")
+    for k, (shape, dtype) in want.items():
+        if k not in out:
+            out[k] = torch.empty(shape, dtype=dtype, device=device)
+    return out
+
+
+class QuantInt8Call(_Call):
+    """A prepared moe_quant_int8 call.
+
+    ``x`` [R, H] (float16 / bfloat16 / float32; rows may be strided).  ``actual_rows``: an
+    int64 tensor of one element, the rows to take (the batching's ``actual_token_num``); the
+    rows behind them are left as they were.  Outputs ``q`` [R, H] int8 and ``scale`` [R]
+    float32, allocated unless given in ``out``; both may be strided, so views into packed rows
+    (H bytes, then the scale) as the batching's INT8 ``token_data`` holds them are fine.
+    """
+
+    def __init__(self, x, *, actual_rows=None, out=None, ev_quant=None):
+        _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [R, H]")
+        dev = x.device
+        _check_rows(x, "x", dev, tuple(_FLOAT_CODE))
+        R, H = x.shape
+        _req(H > 0, "x must have at least one column")
+        if actual_rows is not None:
+            _check_numel(actual_rows, "actual_rows", dev, (torch.int64,), 1)
+        out = _outputs(out, {"q": ((R, H), torch.int8), "scale": ((R,), torch.float32)}, dev)
+        d = QuantInt8Desc()
+        d.dtype = _FLOAT_CODE[x.dtype]
+        d.num_rows, d.hidden = R, H
+        d.x_row_stride, d.q_row_stride, d.scale_row_stride = _row_bytes(x), _row_bytes(out["q"]), _row_elems(out["scale"])
+        d.x, d.actual_rows, d.q, d.scale = _ptr(x), _ptr(actual_rows), _ptr(out["q"]), _ptr(out["scale"])
+        if ev_quant is not None:
+            d.ev_quant_begin, d.ev_quant_end = _event_handle(ev_quant[0]), _event_handle(ev_quant[1])
+        self._bind("moe_quant_int8", d, dev, out, [x, actual_rows], None, moe_quant_int8_workspace_size(d))
+
+
+def moe_quant_int8(x, *, stream=None, **kw):
+    """Quantise rows to INT8 with a scale for each row, once on ``stream`` (default: the
+    current stream); returns dict(q, scale), allocated on that stream."""
+    with _on(stream):
+        return QuantInt8Call(x, **kw).run(stream)
+
+
+class RmsNormQuantCall(_Call):
+    """A prepared moe_rmsnorm_quant call: residual addition, root-mean-square norm, 8-bit rows.
+
+    ``x`` [R, H] (float16 / bfloat16 / float32), ``gamma`` [H] of the same type or float32,
+    ``residual`` [R, H] of x's type or None; rows may be strided.  ``q_dtype`` int8 (``scale``
+    [R]) or float8_e4m3fn (``scale`` [R, ceil(H / 128)]).  ``actual_rows`` as in QuantFp8Call.
+    Outputs ``q``, ``scale``; ``residual_out`` [R, H] (x + residual, with a residual only);
+    ``y`` [R, H], the normed rows in x's type, if ``with_y`` or given in ``out``.
+    ``out={"residual_out": residual}`` updates the residual in place.
+    """
+
+    def __init__(self, x, gamma, *, residual=None, eps=1e-6, q_dtype=torch.int8, with_y=False, actual_rows=None,
+                 out=None, ev_norm=None):
+        _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [R, H]")
+        dev = x.device
+        _check_rows(x, "x", dev, tuple(_FLOAT_CODE))
+        R, H = x.shape
+        _req(H > 0, "x must have at least one column")
+        _check_tensor(gamma, "gamma", dev, (x.dtype, torch.float32), (H,))
+        if residual is not None:
+            _check_rows(residual, "residual", dev, (x.dtype,))
+            _req(tuple(residual.shape) == (R, H), f"residual must be {(R, H)}")
+        if actual_rows is not None:
+            _check_numel(actual_rows, "actual_rows", dev, (torch.int64,), 1)
+        _req(q_dtype in _Q_CODE, f"q_dtype {q_dtype} is not int8 or float8_e4m3fn")
+        want = {"q": ((R, H), q_dtype),
+                "scale": ((R,) if q_dtype == torch.int8 else (R, _blocks(H)), torch.float32)}
+        if residual is not None:
+            want["residual_out"] = ((R, H), x.dtype)
+        if with_y or "y" in (out or {}):
+            want["y"] = ((R, H), x.dtype)
+        out = _outputs(out, want, dev)
+        d = RmsNormQuantDesc()
+        d.dtype, d.gamma_dtype, d.q_dtype, d.epsilon = _FLOAT_CODE[x.dtype], _FLOAT_CODE[gamma.dtype], _Q_CODE[q_dtype], float(eps)
+        d.num_rows, d.hidden = R, H
+        d.x_row_stride, d.q_row_stride, d.scale_row_stride = _row_bytes(x), _row_bytes(out["q"]), _row_elems(out["scale"])
+        d.x, d.gamma, d.actual_rows, d.q, d.scale = _ptr(x), _ptr(gamma), _ptr(actual_rows), _ptr(out["q"]), _ptr(out["scale"])
+        if residual is not None:
+            d.residual, d.residual_row_stride = _ptr(residual), _row_bytes(residual)
+            d.residual_out, d.residual_out_row_stride = _ptr(out["residual_out"]), _row_bytes(out["residual_out"])
+        if "y" in out:
+            d.y, d.y_row_stride = _ptr(out["y"]), _row_bytes(out["y"])
+        if ev_norm is not None:
+            d.ev_norm_begin, d.ev_norm_end = _event_handle(ev_norm[0]), _event_handle(ev_norm[1])
+        self._bind("moe_rmsnorm_quant", d, dev, out, [x, gamma, residual, actual_rows], None,
+                   moe_rmsnorm_quant_workspace_size(d))
+
+
+def moe_rmsnorm_quant(x, gamma, *, stream=None, **kw):
+    """Run the norm with its 8-bit output once on ``stream`` (default: the current stream);
+    returns dict(q, scale) with residual_out and y where asked for, allocated on that stream."""
+    with _on(stream):
+        return RmsNormQuantCall(x, gamma, **kw).run(stream)
+
+
+class GroupedMatmulInt8Call(_Call):
+    """A prepared moe_grouped_matmul_int8 call.
+
+    ``x`` [R, K] int8 with ``x_scale`` [R] float32 (the batching's ``y`` and ``dynamic_scale``;
+    both may be strided), ``w`` [E, N, K] int8 with ``w_scale`` [E, N] float32.
+    ``group_list`` int64 [G, 2]: the {expert, row count} pairs of the batching, rows in that
+    order; None: one dense product (E = 1, ``w`` may also be [N, K] and ``w_scale`` [N]).
+    ``epilogue`` FFNWB_EPI_NONE or FFNWB_EPI_SWIGLU (N = 2 F, gate rows then up rows).
+    ``out_dtype`` float16 / bfloat16 / float32, or int8 with SwiGLU, which also returns
+    ``y_scale`` [R].  K must be a multiple of 16, F too.
+    """
+
+    def __init__(self, x, x_scale, w, w_scale, *, group_list=None, epilogue=FFNWB_EPI_NONE, out_dtype=torch.bfloat16,
+                 out=None, workspace=None, ev_matmul=None):
+        _req(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [R, K]")
+        dev = x.device
+        _check_rows(x, "x", dev, (torch.int8,))
+        R, K = x.shape
+        _check_scales(x_scale, "x_scale", dev, R)
+        _req(isinstance(w, torch.Tensor) and isinstance(w_scale, torch.Tensor), "w and w_scale must be tensors")
+        if group_list is None and w.dim() == 2 and w_scale.dim() == 1:
+            w, w_scale = w[None], w_scale[None]
+        _req(w.dim() == 3 and w.shape[2] == K, f"w must be [E, N, K={K}]")
+        E, N = w.shape[0], w.shape[1]
+        _check_tensor(w, "w", dev, (torch.int8,))
+        _check_tensor(w_scale, "w_scale", dev, (torch.float32,), (E, N))
+        if group_list is not None:
+            _req(isinstance(group_list, torch.Tensor) and group_list.dim() == 2 and group_list.shape[1] == 2,
+                 "group_list must be [G, 2]")
+            _check_tensor(group_list, "group_list", dev, (torch.int64,))
+        _req(out_dtype in _OUT8_CODE, f"out_dtype {out_dtype} is not float16, bfloat16, float32 or int8")
+        epilogue = int(epilogue)
+        cols = N // 2 if epilogue == FFNWB_EPI_SWIGLU else N
+        want = {"y": ((R, cols), out_dtype)}
+        if out_dtype == torch.int8:
+            want["y_scale"] = ((R,), torch.float32)
+        out = _outputs(out, want, dev)
+        d = GroupedMatmulInt8Desc()
+        d.epilogue, d.out_dtype = epilogue, _OUT8_CODE[out_dtype]
+        d.num_rows, d.in_features, d.out_features, d.num_experts = R, K, N, E
+        d.num_groups = group_list.shape[0] if group_list is not None else 0
+        d.x_row_stride, d.x_scale_stride, d.y_row_stride = _row_bytes(x), _row_elems(x_scale), _row_bytes(out["y"])
+        d.x, d.x_scale, d.w, d.w_scale = _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale)
+        d.group_list = _ptr(group_list)
+        d.y = _ptr(out["y"])
+        if "y_scale" in out:
+            d.y_scale, d.y_scale_stride = _ptr(out["y_scale"]), _row_elems(out["y_scale"])
+        if ev_matmul is not None:
+            d.ev_matmul_begin, d.ev_matmul_end = _event_handle(ev_matmul[0]), _event_handle(ev_matmul[1])
+        self._bind("moe_grouped_matmul_int8", d, dev, out, [x, x_scale, w, w_scale, group_list], workspace,
+                   moe_grouped_matmul_int8_workspace_size(d))
+
+
+def moe_grouped_matmul_int8(x, x_scale, w, w_scale, *, stream=None, **kw):
+    """Run the experts' INT8 products once on ``stream`` (default: the current stream);
+    returns dict(y) or, for int8 outputs, dict(y, y_scale), allocated on that stream."""
+    with _on(stream):
+        return GroupedMatmulInt8Call(x, x_scale, w, w_scale, **kw).run(stream)

@@ -143,3 +143,41 @@ class LayerDesc(ctypes.Structure):
         ("w13", _vp), ("w13_scale", _vp), ("w2", _vp), ("w2_scale", _vp), ("y", _vp),
         ("ev_layer_begin", _vp), ("ev_layer_end", _vp),
     ]
+
+
+class QuantInt8Desc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("reserved0", _i32),
+        ("num_rows", _i64), ("hidden", _i64),
+        ("x_row_stride", _i64), ("q_row_stride", _i64), ("scale_row_stride", _i64),
+        ("x", _vp), ("actual_rows", _vp), ("q", _vp), ("scale", _vp),
+        ("ev_quant_begin", _vp), ("ev_quant_end", _vp),
+    ]
+
+
+class RmsNormQuantDesc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", _i32), ("gamma_dtype", _i32), ("q_dtype", _i32), ("epsilon", ctypes.c_float),
+        ("num_rows", _i64), ("hidden", _i64),
+        ("x_row_stride", _i64), ("residual_row_stride", _i64), ("residual_out_row_stride", _i64), ("y_row_stride", _i64),
+        ("q_row_stride", _i64), ("scale_row_stride", _i64),
+        ("x", _vp), ("residual", _vp), ("gamma", _vp), ("actual_rows", _vp),
+        ("residual_out", _vp), ("y", _vp), ("q", _vp), ("scale", _vp),
+        ("ev_norm_begin", _vp), ("ev_norm_end", _vp),
+    ]
+
+
+class GroupedMatmulInt8Desc(ctypes.Structure):
+    _fields_ = [
+        ("epilogue", _i32), ("out_dtype", _i32),
+        ("num_rows", _i64), ("in_features", _i64), ("out_features", _i64), ("num_experts", _i64),
+        ("num_groups", _i64),
+        ("x_row_stride", _i64), ("x_scale_stride", _i64), ("y_row_stride", _i64), ("y_scale_stride", _i64),
+        ("x", _vp), ("x_scale", _vp), ("w", _vp), ("w_scale", _vp), ("group_list", _vp),
+        ("y", _vp), ("y_scale", _vp),
+        ("ev_matmul_begin", _vp), ("ev_matmul_end", _vp),
+    ]
+
+
+class GroupedMatmulInt8PlanInfo(ctypes.Structure):
+    _fields_ = [("lds_tiles", _i32), ("tile_rows", _i32), ("k_parts", _i32), ("listed", _i32)]

@@ -19,7 +19,7 @@ LIB = os.path.join(LIBDIR, "libffnwb.so")
 PROBE_SOURCE = "probe_copy.hip"
 PROBE_LIB = os.path.join(LIBDIR, "libffnwb_probe.so")
 SOURCES = ["api.hip", "batching.hip", "unpermute.hip", "permute.hip", "context.hip", "update_expert.hip",
-           "noalloc.hip", "quant_fp8.hip", "grouped_matmul.hip", "layer.hip"]
+           "noalloc.hip", "quant_fp8.hip", "grouped_matmul.hip", "layer.hip", "row_quant.hip", "matmul_int8.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

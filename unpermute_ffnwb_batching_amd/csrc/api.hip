@@ -55,6 +55,12 @@ size_t moe_grouped_matmul_fp8_desc_size(void) { return sizeof(moe_grouped_matmul
 
 size_t moe_layer_desc_size(void) { return sizeof(moe_layer_desc); }
 
+size_t moe_quant_int8_desc_size(void) { return sizeof(moe_quant_int8_desc); }
+
+size_t moe_rmsnorm_quant_desc_size(void) { return sizeof(moe_rmsnorm_quant_desc); }
+
+size_t moe_grouped_matmul_int8_desc_size(void) { return sizeof(moe_grouped_matmul_int8_desc); }
+
 const char* ffnwb_status_string(int status) {
   switch (status) {
     case FFNWB_OK: return "FFNWB_OK";
@@ -221,6 +227,65 @@ int moe_layer(const moe_layer_desc* d, void* workspace, size_t ws_bytes, void* s
   if (st != FFNWB_OK) return st;
   if (!workspace_ok(workspace, ws_bytes, p.ws_bytes)) return FFNWB_ERR_WORKSPACE;
   return launch_layer(d, p, workspace, static_cast<hipStream_t>(stream));
+}
+
+int moe_quant_int8_workspace_size(const moe_quant_int8_desc* d, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  const int st = plan_quant_int8(d);
+  if (st != FFNWB_OK) return st;
+  *ws_bytes = 0;
+  return FFNWB_OK;
+}
+
+int moe_quant_int8(const moe_quant_int8_desc* d, void* workspace, size_t ws_bytes, void* stream) {
+  (void)workspace;
+  (void)ws_bytes;
+  const int st = plan_quant_int8(d);
+  if (st != FFNWB_OK) return st;
+  return launch_quant_int8(d, static_cast<hipStream_t>(stream));
+}
+
+int moe_rmsnorm_quant_workspace_size(const moe_rmsnorm_quant_desc* d, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  const int st = plan_rmsnorm_quant(d);
+  if (st != FFNWB_OK) return st;
+  *ws_bytes = 0;
+  return FFNWB_OK;
+}
+
+int moe_rmsnorm_quant(const moe_rmsnorm_quant_desc* d, void* workspace, size_t ws_bytes, void* stream) {
+  (void)workspace;
+  (void)ws_bytes;
+  const int st = plan_rmsnorm_quant(d);
+  if (st != FFNWB_OK) return st;
+  return launch_rmsnorm_quant(d, static_cast<hipStream_t>(stream));
+}
+
+int moe_grouped_matmul_int8_workspace_size(const moe_grouped_matmul_int8_desc* d, size_t* ws_bytes) {
+  if (ws_bytes == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  Int8MatmulPlan p;
+  const int st = plan_grouped_matmul_int8(d, &p);
+  if (st != FFNWB_OK) return st;
+  *ws_bytes = p.ws_bytes;
+  return FFNWB_OK;
+}
+
+int moe_grouped_matmul_int8_plan(const moe_grouped_matmul_int8_desc* d, moe_grouped_matmul_int8_plan_info* info) {
+  if (info == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  Int8MatmulPlan p;
+  const int st = plan_grouped_matmul_int8(d, &p);
+  if (st != FFNWB_OK) return st;
+  *info = moe_grouped_matmul_int8_plan_info{p.tile ? 1 : 0, static_cast<int32_t>(p.bm), static_cast<int32_t>(p.parts),
+                                            p.table ? 1 : 0};
+  return FFNWB_OK;
+}
+
+int moe_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, void* workspace, size_t ws_bytes, void* stream) {
+  Int8MatmulPlan p;
+  const int st = plan_grouped_matmul_int8(d, &p);
+  if (st != FFNWB_OK) return st;
+  if (!workspace_ok(workspace, ws_bytes, p.ws_bytes)) return FFNWB_ERR_WORKSPACE;
+  return launch_grouped_matmul_int8(d, p, workspace, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

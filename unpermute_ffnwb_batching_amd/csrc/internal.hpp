@@ -160,6 +160,32 @@ struct LayerPlan {
 int plan_layer(const moe_layer_desc* d, LayerPlan* p);
 int launch_layer(const moe_layer_desc* d, const LayerPlan& p, void* ws, hipStream_t s);
 
+int plan_quant_int8(const moe_quant_int8_desc* d);
+int launch_quant_int8(const moe_quant_int8_desc* d, hipStream_t s);
+
+int plan_rmsnorm_quant(const moe_rmsnorm_quant_desc* d);
+int launch_rmsnorm_quant(const moe_rmsnorm_quant_desc* d, hipStream_t s);
+
+struct Int8MatmulPlan {
+  int64_t R = 0, K = 0, N = 0, F = 0;          // F = outputs per row
+  int64_t xs = 0, xss = 0, ys = 0, yss = 0;    // row strides: bytes, elements, bytes, elements
+  bool swiglu = false;
+  bool quant = false;                          // INT8 rows out, by a second launch
+  bool tile = false;                           // through LDS, else straight to registers
+  int64_t bm = 0;                              // rows of a tile
+  int64_t kb = 0;                              // 128-column blocks of K
+  int64_t parts = 1, part_blocks = 0;          // parts of K, and blocks of each
+  int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles (times the parts)
+  bool join = false;                           // sums or FP32 rows, finished by a launch of its own
+  int64_t pitch = 0;                           // elements of a row of them
+  int64_t join_groups = 0;                     // workgroups that finish a row tile
+  bool table = false;                          // row tiles listed by a launch of their own
+  size_t ws_bytes = 0;
+};
+
+int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPlan* p);
+int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8MatmulPlan& p, void* ws, hipStream_t s);
+
 // Widest row-copy access (16, 4 or 1 bytes) that two base addresses, two strides and the
 // row size all allow.
 inline int vec_class(uintptr_t a, uintptr_t b, int64_t s1, int64_t s2, int64_t bytes) {

@@ -1,0 +1,426 @@
+// The experts' products on INT8 rows, with a scale for each row of x and each row of w.
+//
+// As for e4m3 rows there are two kernels: few rows go straight from memory to registers
+// (mm8_direct_kernel), more rows in tiles through LDS (mm8_tile_kernel).  The scales belong to whole
+// rows, so the matrix cores carry the 32-bit totals over all of K, and the scaling is done once, at
+// the end.  What a workgroup cannot finish by itself, mm8_join_kernel (parts of K) or mm8_rows_kernel
+// (INT8 results, whose scale spans the row) does.
+#include "int8_tile.hpp"
+
+namespace ffnwb {
+
+// ------------------------------------------------------------------ direct kernel
+//
+// For few rows, where the weights are read once and latency counts.  A workgroup takes MT * 16
+// rows by 16 columns (SwiGLU: 16 gate and the 16 up columns that go with them); its waves take
+// the 128-column blocks of K in turn, straight from memory to registers, a wave's next block
+// ahead of its present one, and their totals are added in wave order.
+
+template <class T, int EPI, int MT>
+__global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Args a) {
+  constexpr int NF = EPI == FFNWB_EPI_SWIGLU ? 2 : 1;
+  extern __shared__ __align__(16) i32x4 red8[];  // [waves][NF * MT][lanes]
+  RowTile rt;
+  int32_t c;
+  if (!find_tile(a, MT * 16, rt, c)) return;
+  const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), waves = blockDim.x / kWave;
+  const int32_t r = lane % 16, g = lane / 16;
+  const int64_t n0 = int64_t{c} * 16;
+  const char* wp[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+    wp[f] = a.w + (static_cast<int64_t>(rt.expert) * a.N + min(n0 + f * a.F + r, a.N - 1)) * a.K;
+  const char* xp[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xp[i] = a.x + static_cast<int64_t>(rt.row0 + min(i * 16 + r, rt.rows - 1)) * a.xs;
+  struct Block {
+    u32x4 w[NF][2], x[MT][2];
+  } blk[2];
+  // A block's columns; past the end of K the row's last ones (no branch in the way of the loads),
+  // which `multiply` clears in x.
+  const int32_t last = static_cast<int32_t>(a.K) - 16;
+  auto load = [&](Block& v, int32_t b) {
+    if (b >= a.kb) return;
+    const int32_t k0 = min(b * kBlk + g * 16, last), k1 = min(b * kBlk + 64 + g * 16, last);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) v.w[f][0] = load16(wp[f] + k0), v.w[f][1] = load16(wp[f] + k1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) v.x[i][0] = load16(xp[i] + k0), v.x[i][1] = load16(xp[i] + k1);
+  };
+  i32x4 tot[NF][MT] = {};
+  auto multiply = [&](Block& v, int32_t b) {
+    if (b >= a.kb) return;
+    if ((b + 1) * kBlk > a.K) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (b * kBlk + h * 64 + g * 16 > last) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i) v.x[i][h] = u32x4{0, 0, 0, 0};
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) tot[f][i] = mul_int8(v.w[f][h], v.x[i][h], tot[f][i]);
+  };
+  load(blk[0], wave);
+  for (int32_t b = wave; b < a.kb; b += 2 * waves) {
+    load(blk[1], b + waves);
+    multiply(blk[0], b);
+    load(blk[0], b + 2 * waves);
+    multiply(blk[1], b + waves);
+  }
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) red8[(wave * NF * MT + f * MT + i) * kWave + lane] = tot[f][i];
+  __syncthreads();
+  for (int32_t i = wave; i < MT; i += waves) {
+    i32x4 s[NF] = {};
+    for (int32_t w = 0; w < waves; ++w)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) s[f] += red8[(w * NF * MT + f * MT + i) * kWave + lane];
+    if (i * 16 + r >= rt.rows) continue;
+    const int64_t row = rt.row0 + i * 16 + r;
+    const float xs = a.x_scale[row * a.xss];
+    f32x4 p[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) p[f] = scaled(s[f], xs, channel_scales(a, rt.expert, n0 + f * a.F + g * 4));
+    if constexpr (EPI == FFNWB_EPI_SWIGLU) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[0][j] = swiglu(p[0][j], p[1][j]);
+    }
+    store4<T>(a.y + row * a.ys, n0 + g * 4, a.F, p[0], a.vec);
+  }
+}
+
+// ------------------------------------------------------------------ joining a product
+//
+// Products split over K: whole-number sums [parts][R][N rounded up to 8], whose order does not
+// matter.  16 lanes take 128 outputs of a row; a workgroup takes 16 such blocks of a row tile, so
+// that rows of no expert stay as they were.  FP32 results on their way to INT8 go to the FP32 rows
+// that mm8_rows_kernel takes.
+
+constexpr int kJoin8Threads = 256;
+
+template <class T, bool kSwiglu>
+__global__ __launch_bounds__(kJoin8Threads) void mm8_join_kernel(Mm8Args a, const int32_t* sums, int64_t pitch, int32_t parts, int32_t bm) {
+  const int32_t fb = static_cast<int32_t>((a.F + kBlk - 1) / kBlk);
+  RowTile rt;
+  int32_t group;
+  if (!find_tile(a, bm, rt, group)) return;
+  const int32_t u = group * (kJoin8Threads / 16) + threadIdx.x / 16;
+  const int32_t i = u / fb, b = u - i * fb;
+  const int64_t row = rt.row0 + i, f0 = static_cast<int64_t>(b) * kBlk + threadIdx.x % 16 * 8;
+  if (i >= rt.rows || f0 >= a.F) return;
+  const float xs = a.x_scale[row * a.xss];
+  auto sum = [&](int64_t n, f32x4 (&f)[2]) {  // columns n .. n + 7
+    const int32_t* p = sums + row * pitch + n;
+    i32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int32_t s = 0; s < parts; ++s, p += a.rows * pitch) {
+      v0 += reinterpret_cast<const i32x4*>(p)[0];
+      v1 += reinterpret_cast<const i32x4*>(p)[1];
+    }
+    f[0] = scaled(v0, xs, channel_scales(a, rt.expert, n));
+    f[1] = scaled(v1, xs, channel_scales(a, rt.expert, n + 4));
+  };
+  f32x4 f[2];
+  sum(f0, f);
+  if constexpr (kSwiglu) {
+    f32x4 up[2];
+    sum(a.F + f0, up);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[h][j] = swiglu(f[h][j], up[h][j]);
+  }
+  char* y = a.y + row * a.ys;
+  store4<T>(y, f0, a.F, f[0], a.vec);
+  store4<T>(y, f0 + 4, a.F, f[1], a.vec);
+}
+
+// ------------------------------------------------------------------ INT8 results
+//
+// FP32 rows [R][F] to INT8, with the row's scale: a wave to a row, 4 rows of a row tile to a
+// workgroup.  C: runs of 8 elements that a lane holds; 0: the row is read twice instead.
+
+template <int C>
+__global__ __launch_bounds__(256) void mm8_rows_kernel(Mm8Args a, const float* h, int64_t pitch, int32_t bm) {
+  RowTile rt;
+  int32_t group;
+  if (!find_tile(a, bm, rt, group)) return;
+  const int32_t i = group * 4 + uniform(threadIdx.x / kWave), t = threadIdx.x % kWave;
+  if (i >= rt.rows) return;
+  const int64_t row = rt.row0 + i;
+  const char* from = reinterpret_cast<const char*>(h + row * pitch);
+  char* q = a.y + row * a.ys;
+  const int32_t F = static_cast<int32_t>(a.F);
+  float v[C > 0 ? C : 1][8] = {}, none = 0.0f;
+  uint32_t m = 0, lo, hi;
+  auto gather = [&](int32_t h0, float (&f)[8]) {
+    load_run<TF32>(from, h0, F, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+  };
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if ((j * kWave + t) * 8 < F) gather((j * kWave + t) * 8, v[j]);
+  } else {
+    for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) gather(h0, v[0]);
+  }
+  row_reduce<true>(none, m, 0);
+  const float s = row_scale(__uint_as_float(m));
+  if (t == 0) a.y_scale[row * a.yss] = s;
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int32_t h0 = (j * kWave + t) * 8;
+      if (h0 >= F) continue;
+      quant_int8(v[j], s, lo, hi);
+      store_bytes(q, h0, F, lo, hi);
+    }
+  } else {
+    for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) {
+      gather(h0, v[0]);
+      quant_int8(v[0], s, lo, hi);
+      store_bytes(q, h0, F, lo, hi);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+constexpr int64_t kCus8 = 256;
+
+static int64_t out_size8(int32_t dt) { return dt == FFNWB_DT_FP32 ? 4 : dt == FFNWB_DT_INT8 ? 1 : 2; }
+
+// Waves of a direct workgroup: a block of K for each, four at most where there are enough
+// workgroups to fill the chip.
+static int direct_waves8(int64_t tiles, int64_t kb, int64_t bm) {
+  int waves = 1;
+  while (waves < (bm == 16 ? 16 : 8) && waves * 2 <= kb && (waves < 4 || tiles * waves < kCus8 * 16)) waves *= 2;
+  return waves;
+}
+
+// Microseconds that a product takes with the given kernel and tile rows, as far as the choice
+// between them needs it.
+static double expected_us8(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t groups, bool swiglu, bool tile, int64_t bm,
+                           int64_t parts) {
+  const int64_t kb = (K + 127) / 128, some = groups < rows ? groups : rows;
+  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.58 * some : static_cast<double>((rows + bm - 1) / bm);
+  auto rounds = [](double wgs, int64_t together) { return wgs <= together ? 1.0 : __builtin_ceil(wgs / together); };
+  if (tile) {
+    const double tiles = parts > 1 ? mt * ((N + 255) / 256) * parts : mt * ((F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
+    const double join = parts > 1 ? 4.1 + parts * rows * N * 8 / 5430e3 : 0.0;  // a launch, sums written and read
+    double us = bm == 256 ? 1.53 : bm == 128 ? 0.98 : 0.79;
+    int64_t together = kCus8;
+    if (bm == 32) {  // two to a CU
+      us = tiles > kCus8 ? 1.2 : 0.65;
+      together = 2 * kCus8;
+    }
+    return 2.8 + rounds(tiles, together) * ((kb + parts - 1) / parts * us + 2.7) + join;
+  }
+  const int64_t nt = (F + 15) / 16;
+  const int waves = direct_waves8(((rows + bm - 1) / bm + some) * nt, kb, bm);
+  const int fit = bm == 16 ? (swiglu ? 20 : 28) : bm == 32 ? (swiglu ? 12 : 20) : (swiglu ? 8 : 12);
+  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 1.74 : 1.33) * (bm == 64 ? 1.63 : bm == 32 ? 1.27 : 1.0);
+  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus8 : kCus8) * ((kb + waves - 1) / waves * us + 0.7);
+  const double weights = mt * N * K / 5120e3;  // read again for every row tile, from L2
+  return 2.8 + (work > weights ? work : weights);
+}
+
+int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPlan* p) {
+  if (d == nullptr || d->x == nullptr || d->x_scale == nullptr || d->w == nullptr || d->w_scale == nullptr || d->y == nullptr)
+    return FFNWB_ERR_PARAM_NULLPTR;
+  const bool quant = d->out_dtype == FFNWB_DT_INT8, swiglu = d->epilogue == FFNWB_EPI_SWIGLU;
+  if (quant && d->y_scale == nullptr) return FFNWB_ERR_PARAM_NULLPTR;
+  if (d->epilogue != FFNWB_EPI_NONE && !swiglu) return FFNWB_ERR_PARAM_INVALID;
+  if (d->out_dtype != FFNWB_DT_FP16 && d->out_dtype != FFNWB_DT_BF16 && d->out_dtype != FFNWB_DT_FP32 && !(quant && swiglu))
+    return FFNWB_ERR_PARAM_INVALID;
+  if (d->num_rows < 0 || d->num_rows > (int64_t{1} << 24)) return FFNWB_ERR_PARAM_INVALID;
+  // K * 128 * 128 stays below 2^31
+  if (d->in_features <= 0 || d->in_features > 131056 || d->in_features % 16 != 0) return FFNWB_ERR_PARAM_INVALID;
+  if (d->out_features <= 0 || d->out_features > (int64_t{1} << 18) || (swiglu && d->out_features % 32 != 0)) return FFNWB_ERR_PARAM_INVALID;
+  if (d->num_experts < 1 || d->num_experts > kMaxExperts) return FFNWB_ERR_PARAM_INVALID;
+  if (d->group_list != nullptr ? (d->num_groups < 1 || d->num_groups > kMaxExperts)
+                               : (d->num_groups != 0 || d->num_experts != 1))
+    return FFNWB_ERR_PARAM_INVALID;
+  p->R = d->num_rows;
+  p->K = d->in_features;
+  p->N = d->out_features;
+  p->F = swiglu ? d->out_features / 2 : d->out_features;
+  p->kb = (p->K + 127) / 128;
+  const int64_t elt = out_size8(d->out_dtype);
+  p->xs = d->x_row_stride ? d->x_row_stride : p->K;
+  p->xss = d->x_scale_stride ? d->x_scale_stride : 1;
+  p->ys = d->y_row_stride ? d->y_row_stride : p->F * elt;
+  p->yss = d->y_scale_stride ? d->y_scale_stride : 1;
+  const int64_t far = int64_t{1} << 32;  // row * stride stays far inside 64 bits
+  if (p->xs < p->K || p->xs % 16 != 0 || p->xs > far || p->xss < 1 || p->xss > far) return FFNWB_ERR_PARAM_INVALID;
+  if (p->ys < p->F * elt || p->ys % elt != 0 || p->ys > far || p->yss < 1 || p->yss > far) return FFNWB_ERR_PARAM_INVALID;
+  if ((reinterpret_cast<uintptr_t>(d->x) | reinterpret_cast<uintptr_t>(d->w)) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(d->y) % elt != 0 || (reinterpret_cast<uintptr_t>(d->x_scale) | reinterpret_cast<uintptr_t>(d->w_scale)) % 4 != 0 ||
+      (quant && reinterpret_cast<uintptr_t>(d->y_scale) % 4 != 0))
+    return FFNWB_ERR_PARAM_INVALID;
+  const int64_t groups = d->group_list != nullptr ? d->num_groups : 1;
+  auto shape = [&](int64_t bm, int64_t parts) {  // negative bm: direct; the result: workgroups, of the larger launch
+    p->tile = bm > 0, p->bm = bm > 0 ? bm : -bm;
+    p->part_blocks = (p->kb + parts - 1) / parts;
+    p->parts = (p->kb + p->part_blocks - 1) / p->part_blocks;
+    p->mtiles = (p->R + p->bm - 1) / p->bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
+    p->ntiles = !p->tile ? (p->F + 15) / 16 : p->parts > 1 ? (p->N + 255) / 256 * p->parts : (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
+    p->join = p->parts > 1;
+    p->join_groups = p->join ? (p->bm * ((p->F + 127) / 128) + kJoin8Threads / 16 - 1) / (kJoin8Threads / 16) : 0;
+    int64_t most = p->join_groups > p->ntiles ? p->join_groups : p->ntiles;
+    if (quant && p->bm / 4 > most) most = p->bm / 4;
+    return p->mtiles * most;
+  };
+  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  256 rows
+  // of x, and the gate rows of w, have to be inside the 32-bit offsets of the tile kernel.
+  const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
+  const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup
+  double best = 0;
+  int64_t best_bm = 0, best_parts = 1;
+  auto consider = [&](int64_t bm, int64_t parts) {
+    if (shape(bm, parts) > most) return;
+    const double t = expected_us8(p->R, p->N, p->K, p->F, d->num_groups, swiglu, p->tile, p->bm, p->parts);
+    if (best_bm == 0 || t < best) best = t, best_bm = bm, best_parts = p->parts;
+  };
+  for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {
+    if (bm > 0 && !near) continue;
+    consider(bm, 1);
+    if (bm < 0 || bm == 256) continue;
+    // parts that fill the chip once, or half of it
+    const int64_t last = d->num_groups < p->R ? d->num_groups : p->R, tiles = ((p->R + bm - 1) / bm + last * 6 / 10) * ((p->N + 255) / 256);
+    const int64_t fill = (bm == 32 ? 2 : 1) * kCus8 / (tiles > 0 ? tiles : 1);
+    for (const int64_t parts : {fill, fill / 2})
+      if (parts > 1) consider(bm, parts < p->kb / 2 ? parts : p->kb / 2 > 1 ? p->kb / 2 : 1);
+  }
+  if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
+  shape(best_bm, best_parts);
+  p->swiglu = swiglu;
+  p->quant = quant;
+  p->pitch = (p->N + 7) / 8 * 8;
+  p->ws_bytes = 0;
+  Carve c;
+  p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > 16 * kCus8));
+  if (p->table) {
+    c.take<int32_t>(1);
+    c.take<int4>(static_cast<size_t>(p->mtiles));
+  }
+  if (p->join) c.take<int32_t>(static_cast<size_t>(p->parts * p->R * p->pitch));
+  if (p->quant) c.take<float>(static_cast<size_t>(p->R * p->F));
+  p->ws_bytes = c.off;
+  return FFNWB_OK;
+}
+
+template <class T, int EPI, int MT>
+static bool launch_direct8_rows(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  const int waves = direct_waves8(p.mtiles * p.ntiles, p.kb, p.bm);
+  const size_t lds = static_cast<size_t>(waves) * (EPI == FFNWB_EPI_SWIGLU ? 2 : 1) * MT * kWave * 16;
+  auto kernel = mm8_direct_kernel<T, EPI, MT>;
+  allow_large_lds(reinterpret_cast<const void*>(kernel), lds);
+  return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles)), dim3(static_cast<uint32_t>(waves * kWave)), lds, s, b, e, a);
+}
+
+template <class T, int EPI, int WM, int WN, int MF>
+static bool launch_tile8_shape(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  using S = Tile8Shape<WM, WN, MF>;
+  auto kernel = mm8_tile_kernel<T, EPI, WM, WN, MF>;
+  allow_large_lds(reinterpret_cast<const void*>(kernel), S::kLds);
+  // halved tiles: up to half a round of workgroups more
+  const int64_t more = MF >= kHalvedFragments ? kXcds * kXcdCus / 2 : 0;
+  return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles + more)), dim3(S::kThreads), S::kLds, s, b, e, a);
+}
+
+template <class T, int EPI>
+static bool launch_product8(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  if constexpr (!T::kWhole) {
+    if (!p.tile)
+      return p.bm == 16   ? launch_direct8_rows<typename T::Out, EPI, 1>(a, p, s, b, e)
+             : p.bm == 32 ? launch_direct8_rows<typename T::Out, EPI, 2>(a, p, s, b, e)
+                          : launch_direct8_rows<typename T::Out, EPI, 4>(a, p, s, b, e);
+  }
+  return p.bm == 256   ? launch_tile8_shape<T, EPI, 2, 4, 8>(a, p, s, b, e)
+         : p.bm == 128 ? launch_tile8_shape<T, EPI, 2, 4, 4>(a, p, s, b, e)
+         : p.bm == 64  ? launch_tile8_shape<T, EPI, 2, 4, 2>(a, p, s, b, e)
+                       : launch_tile8_shape<T, EPI, 1, 4, 2>(a, p, s, b, e);
+}
+
+int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8MatmulPlan& p, void* ws, hipStream_t s) {
+  if (p.R == 0) return record_event(d->ev_matmul_begin, s) && record_event(d->ev_matmul_end, s) ? FFNWB_OK : FFNWB_ERR_RUNTIME;
+  Mm8Args a{};
+  a.rows = static_cast<int32_t>(p.R), a.K = p.K, a.N = p.N, a.F = p.F;
+  a.xs = p.xs, a.xss = p.xss, a.ys = p.ys, a.yss = p.yss;
+  a.kb = static_cast<int32_t>(p.kb);
+  a.ngroups = static_cast<int32_t>(d->num_groups), a.nexperts = static_cast<int32_t>(d->num_experts);
+  a.groups = d->group_list;
+  a.x = static_cast<const char*>(d->x), a.x_scale = d->x_scale;
+  a.w = static_cast<const char*>(d->w), a.w_scale = d->w_scale;
+  a.y = static_cast<char*>(d->y), a.y_scale = d->y_scale;
+  const int32_t bm = static_cast<int32_t>(p.bm);
+  Carve c;
+  c.base = static_cast<char*>(ws);
+  if (p.table) {
+    int32_t* count = c.take<int32_t>(1);
+    int4* table = c.take<int4>(static_cast<size_t>(p.mtiles));
+    hipLaunchKernelGGL(mm_table_kernel<Mm8Args>, dim3(1), dim3(kTableThreads), 0, s, a, bm, table, count);
+    if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
+    a.table = table, a.count = count;
+  }
+  int32_t* sums = p.join ? c.take<int32_t>(static_cast<size_t>(p.parts * p.R * p.pitch)) : nullptr;
+  float* rows = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
+  void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
+  // results in their own type, or FP32 rows on their way to INT8
+  Mm8Args out = a;
+  const int32_t dt = p.quant ? static_cast<int32_t>(FFNWB_DT_FP32) : d->out_dtype;
+  const uint64_t elt = static_cast<uint64_t>(out_size8(dt));
+  if (p.quant) out.y = reinterpret_cast<char*>(rows), out.ys = p.F * 4;
+  const uint64_t at = reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys);
+  out.vec = (at & (4 * elt - 1)) == 0;
+  out.unit = ((at | p.F * elt) & 15) == 0 ? 16 : ((at | p.F * elt) & 3) == 0 ? 4 : 0;
+  void* out_end = p.quant ? nullptr : e;
+  // the product: results, or whole-number sums for the join
+  Mm8Args m = out;
+  m.ntiles = static_cast<int32_t>(p.ntiles);
+  m.parts = static_cast<int32_t>(p.parts), m.part_blocks = static_cast<int32_t>(p.part_blocks), m.part_bytes = p.R * p.pitch * 4;
+  bool ok;
+  if (p.join) {
+    m.y = reinterpret_cast<char*>(sums), m.ys = p.pitch * 4, m.F = p.N;
+    m.vec = true, m.unit = 16;  // the units of a row's end may run into the rest of its pitch
+    ok = launch_product8<Whole, FFNWB_EPI_NONE>(m, p, s, b, nullptr);
+    if (ok) {
+      out.ntiles = static_cast<int32_t>(p.join_groups);
+      const int32_t parts = m.parts;
+      const int64_t pitch = p.pitch;
+      auto join = [&](auto kernel) {
+        return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.join_groups)), dim3(kJoin8Threads), 0, s, nullptr, out_end, out, sums, pitch, parts, bm);
+      };
+      ok = dt == FFNWB_DT_FP16   ? (p.swiglu ? join(mm8_join_kernel<TF16, true>) : join(mm8_join_kernel<TF16, false>))
+           : dt == FFNWB_DT_BF16 ? (p.swiglu ? join(mm8_join_kernel<TBF16, true>) : join(mm8_join_kernel<TBF16, false>))
+                                 : (p.swiglu ? join(mm8_join_kernel<TF32, true>) : join(mm8_join_kernel<TF32, false>));
+    }
+  } else {
+    ok = dt == FFNWB_DT_FP16   ? (p.swiglu ? launch_product8<Scaled<TF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end) : launch_product8<Scaled<TF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end))
+         : dt == FFNWB_DT_BF16 ? (p.swiglu ? launch_product8<Scaled<TBF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end) : launch_product8<Scaled<TBF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end))
+                               : (p.swiglu ? launch_product8<Scaled<TF32>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end) : launch_product8<Scaled<TF32>, FFNWB_EPI_NONE>(m, p, s, b, out_end));
+  }
+  if (ok && p.quant) {
+    a.ntiles = bm / 4;
+    const int64_t pitch = p.F;
+    auto quant = [&](auto kernel) {
+      return launch_bound(kernel, dim3(tile_grid(p.mtiles * a.ntiles)), dim3(256), 0, s, nullptr, e, a, static_cast<const float*>(rows), pitch, bm);
+    };
+    ok = p.F <= 512    ? quant(mm8_rows_kernel<1>)
+         : p.F <= 1024 ? quant(mm8_rows_kernel<2>)
+         : p.F <= 2048 ? quant(mm8_rows_kernel<4>)
+                       : quant(mm8_rows_kernel<0>);
+  }
+  return ok ? FFNWB_OK : FFNWB_ERR_RUNTIME;
+}
+
+}  // namespace ffnwb

@@ -161,7 +161,9 @@ __global__ __launch_bounds__(256) void mm8_rows_kernel(Mm8Args a, const float* h
   float v[C > 0 ? C : 1][8] = {}, none = 0.0f;
   uint32_t m = 0, lo, hi;
   auto gather = [&](int32_t h0, float (&f)[8]) {
-    load_run<TF32>(from, h0, F, f);
+    Raw<TF32> raw;
+    load_raw<TF32, false>(from, h0, F, raw);  // F is a multiple of 16
+    widen_raw(raw, f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
   };
@@ -172,7 +174,7 @@ __global__ __launch_bounds__(256) void mm8_rows_kernel(Mm8Args a, const float* h
   } else {
     for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) gather(h0, v[0]);
   }
-  row_reduce<true>(none, m, 0);
+  row_reduce<64, false>(none, m, 0);
   const float s = row_scale(__uint_as_float(m));
   if (t == 0) a.y_scale[row * a.yss] = s;
   if constexpr (C > 0) {
@@ -181,13 +183,13 @@ __global__ __launch_bounds__(256) void mm8_rows_kernel(Mm8Args a, const float* h
       const int32_t h0 = (j * kWave + t) * 8;
       if (h0 >= F) continue;
       quant_int8(v[j], s, lo, hi);
-      store_bytes(q, h0, F, lo, hi);
+      store_bytes<false>(q, h0, F, lo, hi);
     }
   } else {
     for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) {
       gather(h0, v[0]);
       quant_int8(v[0], s, lo, hi);
-      store_bytes(q, h0, F, lo, hi);
+      store_bytes<false>(q, h0, F, lo, hi);
     }
   }
 }

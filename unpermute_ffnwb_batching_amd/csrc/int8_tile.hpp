@@ -1,13 +1,15 @@
 // Tiles of the INT8 products through LDS (matmul_int8.hip).
 //
 // A workgroup of WM x WN waves takes BM = 16 WM MF rows by 256 columns (SwiGLU: 128 gate columns
-// and the 128 up columns that go with them, half and half in every wave), 64 columns of K to a
-// step.  Both operands go from memory to LDS without passing through registers (16 bytes per
-// lane), kBuffers steps deep.  A row of a step is 64 bytes, 4 chunks of 16; chunk c of row r lies at
-// position c ^ (r / 2 % 4), which spreads the 16 rows that a matrix operand reads at once over
-// all banks.  The lanes of a copy write adjacent LDS addresses, so the permutation is applied to
-// the addresses they read.
+// and the 128 up columns that go with them, half and half in every wave), one 128-column block of K
+// per step.  Both operands go from memory to LDS without passing through registers (16 bytes per
+// lane).  A row of a block is 128 bytes, a whole line of the caches, 8 chunks of 16; chunk c of row r lies
+// at position c ^ (r % 8), which spreads the 16 rows that a matrix operand reads at once over all
+// banks.  The lanes of a copy write adjacent LDS addresses, so the permutation is applied to the
+// addresses they read.
 #pragma once
+
+#include <type_traits>
 
 #include "fp8_block.hpp"
 #include "internal.hpp"
@@ -68,28 +70,26 @@ __device__ __forceinline__ f32x4 scaled(const i32x4& c, float xs, const f32x4& w
 struct Whole { static constexpr bool kWhole = true; static constexpr int kBytes = 4; };
 template <class T> struct Scaled { static constexpr bool kWhole = false; static constexpr int kBytes = T::kBytes; using Out = T; };
 
-constexpr int kStep = 64;  // columns of K to a step
-
 template <int WM, int WN, int MF>
 struct Tile8Shape {
   static constexpr int kThreads = WM * WN * kWave;
   static constexpr int kNF = 16 / WN;              // column fragments of a wave: 256 columns in all
   static constexpr int kBM = WM * MF * 16;
-  static constexpr int kRows = kBM + 256;          // rows of a buffer, x then w
-  static constexpr int kXCopies = (kBM / 16 + WM * WN - 1) / (WM * WN), kWCopies = 256 / 16 / (WM * WN);  // of 16 rows
-  static constexpr int kBuffers = 4;
-  static constexpr int kLds = kBuffers * kRows * kStep;
-  static_assert(kBM % 16 == 0 && 256 % (16 * WM * WN) == 0, "whole copies");
+  static constexpr int kXCopies = kBM / 8 / (WM * WN), kWCopies = 256 / 8 / (WM * WN);  // of 8 rows
+  static constexpr bool kAhead = MF >= 4;          // fragments are read half a step ahead (see mm8_tile)
+  static constexpr int kXBuffers = kAhead ? 3 : 2, kWBuffers = 2;
+  static constexpr int kLds = (kXBuffers * kBM + kWBuffers * 256) * kBlk;
+  static_assert(kBM % (8 * WM * WN) == 0 && 256 % (8 * WM * WN) == 0, "every wave copies the same number of rows");
 };
 
 template <class T, int EPI, int WM, int WN, int MF>
 __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, int32_t c, char* lds) {
   using S = Tile8Shape<WM, WN, MF>;
   constexpr bool kSwiglu = EPI == FFNWB_EPI_SWIGLU;
-  constexpr int NF = S::kNF, NB = S::kBuffers, kWaves = WM * WN;
-  // this workgroup's part of K, in columns
+  constexpr int NF = S::kNF, kWaves = WM * WN;
+  // this workgroup's part of K: kb blocks, `columns` columns
   const int32_t part = c % a.parts, k0 = part * a.part_blocks * kBlk;
-  const int32_t columns = min(static_cast<int32_t>(a.K) - k0, a.part_blocks * kBlk), steps = (columns + kStep - 1) / kStep;
+  const int32_t columns = min(static_cast<int32_t>(a.K) - k0, a.part_blocks * kBlk), kb = (columns + kBlk - 1) / kBlk;
   c /= a.parts;
   const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), r = lane % 16, g = lane / 16;
   const int32_t wm = wave / WN, wn = wave % WN;
@@ -104,52 +104,129 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
       return min(c0 + q, a.N - 1);
     }
   };
-  // Copy j of a wave takes 16 rows, one chunk per lane: 32-bit offsets from the tile's first rows
+  // Copy j of a wave takes 8 rows, one chunk per lane: 32-bit offsets from the tile's first rows
   // (256 rows of x, and of w as far as the up columns, are below 2^32 bytes in this kernel).
   const int64_t w0 = weight_row(0);
   const Buffer xbuf = make_buffer(a.x + rt.row0 * a.xs + k0, (rt.rows - 1) * a.xs + a.K - k0);
   const Buffer wbuf = make_buffer(a.w + (static_cast<int64_t>(rt.expert) * a.N + w0) * a.K + k0, (a.N - w0) * a.K - k0);
-  const uint32_t chunk = ((lane % 4) ^ (lane / 8 % 4)) * 16;
+  const uint32_t chunk = ((lane % 8) ^ (lane / 8)) * 16;
   uint32_t xsrc[S::kXCopies], wsrc[S::kWCopies];
 #pragma unroll
   for (int j = 0; j < S::kXCopies; ++j)
-    xsrc[j] = chunk + static_cast<uint32_t>(min((j * kWaves + wave) % (S::kBM / 16) * 16 + lane / 4, rt.rows - 1) * a.xs);
+    xsrc[j] = chunk + static_cast<uint32_t>(min((j * kWaves + wave) * 8 + lane / 8, rt.rows - 1) * a.xs);
 #pragma unroll
   for (int j = 0; j < S::kWCopies; ++j)
-    wsrc[j] = chunk + static_cast<uint32_t>((weight_row((j * kWaves + wave) * 16 + lane / 4) - w0) * a.K);
-  // Waves that no rows of x are left for fetch the first rows once more, to where those lie: every
-  // wave has the same number of copies on its way.
-  auto fetch = [&](int32_t b) {
-    char* to = lds + b % NB * S::kRows * kStep;
+    wsrc[j] = chunk + static_cast<uint32_t>((weight_row((j * kWaves + wave) * 8 + lane / 8) - w0) * a.K);
+  char* const xlds = lds;
+  char* const wlds = lds + S::kXBuffers * S::kBM * kBlk;
+  auto fetch_x = [&](int32_t b) {
+    char* to = xlds + b % S::kXBuffers * S::kBM * kBlk;
 #pragma unroll
-    for (int j = 0; j < S::kXCopies; ++j) copy16_to_lds(xbuf, xsrc[j], b * kStep, to + (j * kWaves + wave) % (S::kBM / 16) * 1024);
-#pragma unroll
-    for (int j = 0; j < S::kWCopies; ++j) copy16_to_lds(wbuf, wsrc[j], b * kStep, to + S::kBM * kStep + (j * kWaves + wave) * 1024);
+    for (int j = 0; j < S::kXCopies; ++j) copy16_to_lds(xbuf, xsrc[j], b * kBlk, to + (j * kWaves + wave) * 1024);
   };
-  constexpr int kCopies = S::kXCopies + S::kWCopies;
+  auto fetch_w = [&](int32_t b) {
+    char* to = wlds + b % S::kWBuffers * 256 * kBlk;
 #pragma unroll
-  for (int b = 0; b < NB - 1; ++b)
-    if (b < steps) fetch(b);
+    for (int j = 0; j < S::kWCopies; ++j) copy16_to_lds(wbuf, wsrc[j], b * kBlk, to + (j * kWaves + wave) * 1024);
+  };
+  // fragments: 64 columns, the first (s = 0) or second half of a block
+  const int32_t at = r * kBlk + (g ^ (r & 7)) * 16;
+  auto read_x = [&](int32_t b, int s, int i) {
+    return *reinterpret_cast<const u32x4*>(xlds + b % S::kXBuffers * S::kBM * kBlk + (wm * MF + i) * 16 * kBlk + (at ^ (s * 64)));
+  };
+  auto read_w = [&](int32_t b, int s, int f) {
+    return *reinterpret_cast<const u32x4*>(wlds + b % S::kWBuffers * 256 * kBlk + (wn * NF + f) * 16 * kBlk + (at ^ (s * 64)));
+  };
+  // In the last block the columns past K (of the next row, or not there) count as zeros: clearing
+  // them in x is enough.
+  const int32_t left = columns - (kb - 1) * kBlk - g * 16;
+  auto clear_past = [&](int s, u32x4& v) {
+    if (left <= s * 64) v = u32x4{0, 0, 0, 0};
+  };
 
-  // Step b: once its operands have landed for every wave, which also means that every wave is done
-  // with step b - 1, the buffer of that one takes step b + NB - 1.
+  fetch_x(0);
+  fetch_w(0);
+  if (kb > 1) {
+    fetch_x(1);
+    if constexpr (S::kAhead) fetch_w(1);
+  }
   i32x4 tot[MF][NF] = {};
-  for (int32_t b = 0; b < steps; ++b) {
-    copies_done<(NB - 2) * kCopies>(b + NB - 2 < steps);
-    if (b + NB - 1 < steps) fetch(b + NB - 1);
-    const char* xb = lds + b % NB * S::kRows * kStep;
-    const char* wb = xb + S::kBM * kStep;
-    const int32_t at = r * kStep + (g ^ (r / 2 % 4)) * 16;
-    u32x4 wv[NF];
+  if constexpr (S::kAhead) {
+    // A block's two halves are multiplied from fragments read before: w's in the half before, x's two
+    // ahead.  Halfway through the first half every wave is done with block b - 1, and x of block b + 2 takes
+    // its buffer; halfway through the second, w of block b is in registers, and w of block b + 2 takes its
+    // buffer, once block b + 1 has landed for every wave.  So x has 1.5 steps to arrive and w one.
+    u32x4 wv[2][NF], xv[3];
+    copies_done<S::kXCopies + S::kWCopies>(kb > 1);
 #pragma unroll
-    for (int f = 0; f < NF; ++f) wv[f] = *reinterpret_cast<const u32x4*>(wb + (wn * NF + f) * 16 * kStep + at);
-    const bool past = b * kStep + g * 16 >= columns;  // columns past K: of the next row, or not there
+    for (int f = 0; f < NF; ++f) wv[0][f] = read_w(0, 0, f);
+    xv[0] = read_x(0, 0, 0), xv[1] = read_x(0, 0, 1);
+    auto block = [&](int32_t b, auto last) {
+      constexpr bool kLast = decltype(last)::value;
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      u32x4 xv = *reinterpret_cast<const u32x4*>(xb + (wm * MF + i) * 16 * kStep + at);
-      if (past) xv = u32x4{0, 0, 0, 0};
+      for (int n = 0; n < 2 * MF; ++n) {
+        const int s = n / MF, i = n % MF;
+        if (!kLast && n == MF / 2) {
+          lds_barrier();
+          if (b + 2 < kb) fetch_x(b + 2);
+        }
+        if (!kLast && n == MF + MF / 2) {
+          copies_done<S::kXCopies>(b + 2 < kb);
+          if (b + 2 < kb) fetch_w(b + 2);
+        }
+        if (n + 2 < 2 * MF) xv[2] = read_x(b, (n + 2) / MF, (n + 2) % MF);
+        else if (!kLast) xv[2] = read_x(b + 1, 0, n + 2 - 2 * MF);
+        if (kLast) clear_past(s, xv[0]);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) tot[i][f] = mul_int8(wv[f], xv, tot[i][f]);
+        for (int f = 0; f < NF; ++f) {
+          if (i == MF / 2) {
+            if (s == 0) wv[1][f] = read_w(b, 1, f);
+            else if (!kLast) wv[0][f] = read_w(b + 1, 0, f);
+          }
+          tot[i][f] = mul_int8(wv[s][f], xv[0], tot[i][f]);
+        }
+        xv[0] = xv[1], xv[1] = xv[2];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int32_t b = 0; b + 1 < kb; ++b) block(b, std::false_type{});
+    block(kb - 1, std::true_type{});
+  } else {
+    // w of the next block is on its way since the step before, x since the start of this one, and the
+    // fragments of w go to registers first, which frees their buffer for the block after next.
+    if (kb > 1) fetch_w(1);
+    copies_done<S::kXCopies + S::kWCopies>(kb > 1);
+    for (int32_t b = 0; b < kb; ++b) {
+      u32x4 wv[2][NF];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) wv[s][f] = read_w(b, s, f);
+      u32x4 xv[2][MF];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+          xv[s][i] = read_x(b, s, i);
+          if (b == kb - 1) clear_past(s, xv[s][i]);
+        }
+      if (b + 2 < kb) {
+        lds_barrier();  // every wave has its fragments
+        fetch_x(b + 2);
+        fetch_w(b + 2);
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+          for (int f = 0; f < NF; ++f) tot[i][f] = mul_int8(wv[s][f], xv[s][i], tot[i][f]);
+      copies_done<S::kXCopies + S::kWCopies>(b + 2 < kb);
     }
   }
   __syncthreads();

@@ -31,7 +31,6 @@ struct Mm8Args {
   int64_t part_bytes;          // between the results of two parts
   int32_t ngroups, nexperts;
   bool vec;                    // four adjacent outputs are one aligned store
-  int32_t unit;                // rows of y are whole aligned units of 16 or 4 bytes, or elements (0)
   const char* x;
   const float* x_scale;
   const char* w;
@@ -66,9 +65,28 @@ __device__ __forceinline__ f32x4 scaled(const i32x4& c, float xs, const f32x4& w
   return p;
 }
 
+// Two results as one register of a 16-bit type, a lowest.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <class T> __device__ __forceinline__ uint32_t narrow2(float a, float b);
+template <> __device__ __forceinline__ uint32_t narrow2<TBF16>(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
+template <> __device__ __forceinline__ uint32_t narrow2<TF16>(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+}
+
+// Registers of the lane groups g = lane / 16 of two fragments a, b, four columns each -> of 8
+// adjacent columns: group 0 gets a's groups 0 and 1 (a first), group 1 a's 2 and 3, groups 2 and 3
+// those of b.
+__device__ __forceinline__ void join_columns(uint32_t& a, uint32_t& b) {
+  const auto h = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  const auto q = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+  a = q[0], b = q[1];
+}
+
 // What a tile writes: whole-number sums, or scaled results of a type.
-struct Whole { static constexpr bool kWhole = true; static constexpr int kBytes = 4; };
-template <class T> struct Scaled { static constexpr bool kWhole = false; static constexpr int kBytes = T::kBytes; using Out = T; };
+struct Whole { static constexpr bool kWhole = true; };
+template <class T> struct Scaled { static constexpr bool kWhole = false; using Out = T; };
 
 template <int WM, int WN, int MF>
 struct Tile8Shape {
@@ -150,6 +168,19 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
     fetch_x(1);
     if constexpr (S::kAhead) fetch_w(1);
   }
+  // The scales of the wave's rows and columns, loaded among the last products.
+  float xs[MF];
+  f32x4 ws[NF];
+  const int64_t n0 = c0 + wn * (kSwiglu ? NF * 8 : NF * 16) + g * 4;  // the lane's first column of fragment 0
+  auto scales = [&] {
+    if constexpr (!T::kWhole) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i) xs[i] = a.x_scale[(rt.row0 + min((wm * MF + i) * 16 + r, rt.rows - 1)) * a.xss];
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        ws[f] = channel_scales(a, rt.expert, kSwiglu && f >= NF / 2 ? a.F + n0 + (f - NF / 2) * 16 : n0 + f * 16);
+    }
+  };
   i32x4 tot[MF][NF] = {};
   if constexpr (S::kAhead) {
     // A block's two halves are multiplied from fragments read before: w's in the half before, x's two
@@ -195,6 +226,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
       }
     };
     for (int32_t b = 0; b + 1 < kb; ++b) block(b, std::false_type{});
+    scales();
     block(kb - 1, std::true_type{});
   } else {
     // w of the next block is on its way since the step before, x since the start of this one, and the
@@ -229,67 +261,68 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
       copies_done<S::kXCopies + S::kWCopies>(b + 2 < kb);
     }
   }
-  __syncthreads();
+  if constexpr (!S::kAhead) scales();
 
-  // Results go through LDS, so that memory sees whole lines: a matrix result is 16 rows by 4
-  // adjacent columns per lane.  Row r of the tile is kPitch bytes, its 16-byte chunks at
-  // position c ^ (r % 8).
-  constexpr int kElt = T::kBytes;
-  constexpr int kCols = kSwiglu ? 128 : 256, kPitch = kCols * kElt;
+  // Results go from registers to memory: a lane holds 4 adjacent columns of a row, in 16-bit types 8 after
+  // an exchange between two fragments, so that a store writes 64 adjacent bytes of 16 rows.
   constexpr int OF = kSwiglu ? NF / 2 : NF;  // result fragments of a wave
   const int64_t limit = kSwiglu ? a.F : a.N;
-  // FP32 tiles of many rows are wider than the buffers: some of the waves' fragments at a time.
-  constexpr int kParts = (S::kBM * kPitch + S::kLds - 1) / S::kLds <= 1 ? 1 : (S::kBM * kPitch + S::kLds - 1) / S::kLds <= 2 ? 2 : 4;
-  constexpr int kPartF = MF / kParts, kPartRows = S::kBM / kParts;
-  static_assert(MF % kParts == 0, "a part is some of the fragments of every wave");
 #pragma unroll
-  for (int p = 0; p < kParts; ++p) {
-    if (p > 0) __syncthreads();
+  for (int i = 0; i < MF; ++i) {
+    __builtin_amdgcn_sched_barrier(0);  // one row fragment after another: few registers
+    const int32_t row = (wm * MF + i) * 16 + r;
+    char* y = a.y + part * a.part_bytes + (rt.row0 + min(row, rt.rows - 1)) * a.ys;
+    const bool in = row < rt.rows;
+    if constexpr (T::kWhole) {
 #pragma unroll
-    for (int i = 0; i < kPartF; ++i) {
-      const int32_t row = (wm * kPartF + i) * 16 + r;  // of the part
-      float xs = 0.0f;
-      if constexpr (!T::kWhole) xs = a.x_scale[(rt.row0 + min((wm * MF + p * kPartF + i) * 16 + r, rt.rows - 1)) * a.xss];
+      for (int f = 0; f < OF; ++f)  // the ends of a row may run into the rest of its pitch
+        if (in && n0 + f * 16 < limit) *reinterpret_cast<i32x4*>(y + (n0 + f * 16) * 4) = tot[i][f];
+    } else {
+      using Out = typename T::Out;
+      f32x4 v[OF];
 #pragma unroll
       for (int f = 0; f < OF; ++f) {
-        const int32_t byte = ((wn * OF + f) * 16 + g * 4) * kElt;  // of the row
-        char* to = lds + row * kPitch + ((byte / 16 ^ (row & 7)) * 16 + byte % 16);
-        const i32x4& t = tot[p * kPartF + i][f];
-        if constexpr (T::kWhole) {
-          *reinterpret_cast<i32x4*>(to) = t;
-        } else {
-          const int64_t n = c0 + (wn * OF + f) * 16 + g * 4;
-          f32x4 v = scaled(t, xs, channel_scales(a, rt.expert, n));
-          if constexpr (kSwiglu) {
-            const f32x4 up = scaled(tot[p * kPartF + i][OF + f], xs, channel_scales(a, rt.expert, a.F + n));
+        v[f] = scaled(tot[i][f], xs[i], ws[f]);
+        if constexpr (kSwiglu) {
+          const f32x4 up = scaled(tot[i][OF + f], xs[i], ws[OF + f]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = swiglu(v[j], up[j]);
+          for (int j = 0; j < 4; ++j) v[f][j] = swiglu(v[f][j], up[j]);
+        }
+      }
+      if constexpr (Out::kBytes == 4) {
+#pragma unroll
+        for (int f = 0; f < OF; ++f) {
+          const int64_t n = n0 + f * 16;
+          char* to = y + n * 4;
+          if (in && n + 4 <= limit) {
+            *reinterpret_cast<u32x4_a4*>(to) = __builtin_bit_cast(u32x4, v[f]);
+          } else if (in) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              if (n + j < limit) reinterpret_cast<float*>(to)[j] = v[f][j];
           }
-          if constexpr (kElt == 2) {
-            const float w[8] = {v[0], v[1], v[2], v[3], 0, 0, 0, 0};
-            const u32x4 h = Chunk<typename T::Out>::narrow(w);
-            *reinterpret_cast<u32x2*>(to) = u32x2{h[0], h[1]};
-          } else {
-            *reinterpret_cast<f32x4*>(to) = v;
+        }
+      } else {
+#pragma unroll
+        for (int f = 0; f < OF; f += 2) {
+          uint32_t p[2] = {narrow2<Out>(v[f][0], v[f][1]), narrow2<Out>(v[f][2], v[f][3])};
+          uint32_t q[2] = {narrow2<Out>(v[f + 1][0], v[f + 1][1]), narrow2<Out>(v[f + 1][2], v[f + 1][3])};
+          join_columns(p[0], q[0]);
+          join_columns(p[1], q[1]);
+          const int64_t n = n0 + f * 16 + g * 4;  // n0 holds 4 g, the lane's columns start at 8 g
+          char* to = y + n * 2;
+          if (in && n + 8 <= limit) {
+            *reinterpret_cast<u32x4_a1*>(to) = u32x4{p[0], p[1], q[0], q[1]};
+          } else if (in) {
+            const uint32_t w[4] = {p[0], p[1], q[0], q[1]};
+#pragma unroll
+            for (int j = 0; j < 7; ++j)
+              if (n + j < limit) reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
           }
         }
       }
     }
-    __syncthreads();
-    const int32_t bytes = static_cast<int32_t>(min(limit - c0, int64_t{kCols})) * kElt;  // of a row
-    // rows of a part: kPartF * 16 of every wave row
-#pragma unroll
-    for (int w = 0; w < (kParts == 1 ? 1 : WM); ++w) {
-      const int32_t first = kParts == 1 ? 0 : w * MF * 16 + p * kPartF * 16;
-      const int32_t rows = min(rt.rows - first, kParts == 1 ? S::kBM : kPartF * 16);
-      char* y = a.y + part * a.part_bytes + (rt.row0 + first) * a.ys + c0 * kElt;
-      const char* from = lds + (kParts == 1 ? 0 : w * kPartF * 16 * kPitch);
-      if (a.unit == 16) copy_out<16, kPitch, S::kThreads>(from, y, a.ys, rows, bytes);
-      else if (a.unit == 4) copy_out<4, kPitch, S::kThreads>(from, y, a.ys, rows, bytes);
-      else copy_out<kElt, kPitch, S::kThreads>(from, y, a.ys, rows, bytes);
-    }
   }
-  (void)kPartRows;
 }
 
 // Tiles of at most half the rows (the last one of a group, the halves of find_tile) take half the

@@ -384,7 +384,6 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
   if (p.quant) out.y = reinterpret_cast<char*>(rows), out.ys = p.F * 4;
   const uint64_t at = reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys);
   out.vec = (at & (4 * elt - 1)) == 0;
-  out.unit = ((at | p.F * elt) & 15) == 0 ? 16 : ((at | p.F * elt) & 3) == 0 ? 4 : 0;
   void* out_end = p.quant ? nullptr : e;
   // the product: results, or whole-number sums for the join
   Mm8Args m = out;
@@ -393,7 +392,6 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
   bool ok;
   if (p.join) {
     m.y = reinterpret_cast<char*>(sums), m.ys = p.pitch * 4, m.F = p.N;
-    m.vec = true, m.unit = 16;  // the units of a row's end may run into the rest of its pitch
     ok = launch_product8<Whole, FFNWB_EPI_NONE>(m, p, s, b, nullptr);
     if (ok) {
       out.ntiles = static_cast<int32_t>(p.join_groups);

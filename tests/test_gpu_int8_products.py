@@ -37,7 +37,7 @@ def check(c, groups=None, epilogue="none", out_dtype=BF16, pad=0, what=""):
     want, off, written = matmul_reference(c, groups, epilogue)
     w = dev(written)
     if out_dtype == I8:
-        quantised_close(out["y"][w], out["y_scale"][w], want[written], off[written])
+        quantised_close(out["y"][w], out["y_scale"][w], want[written], off[written], held=True)
         side = out["y_scale"]._base.view(FP32).reshape(rows, 3)
         assert untouched(side[~w]) and untouched(side[:, :1]) and untouched(side[:, 2:])
     else:
@@ -174,7 +174,7 @@ def test_quantised_rows_that_are_not_finite_or_zero():
     assert (q[3:6] == 0).all()
     keep = np.delete(np.arange(40), [3, 4])
     want, off, _ = matmul_reference(dict(c, xs=np.nan_to_num(c["xs"], posinf=0)), None, "swiglu")
-    quantised_close(out["y"][dev(keep)], out["y_scale"][dev(keep)], want[keep], off[keep])
+    quantised_close(out["y"][dev(keep)], out["y_scale"][dev(keep)], want[keep], off[keep], held=True)
 
 
 def test_no_rows():
@@ -211,3 +211,20 @@ def test_weights_past_4_gib():
     want, off, _ = matmul_reference(c)
     close(torch.cat([y[:, :8], y[:, n - 8:]], 1), want, off, FP32)
     assert bool((y[:, 8:n - 8] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [FP32, BF16, I8])
+@pytest.mark.parametrize("rows", [4, 300])
+def test_swiglu_over_its_whole_range(rows, dtype):
+    # one product a column: gates from -110 to 110 and far beyond, infinities among the scales
+    n, k = 512, 16
+    c = dict(x=np.zeros((rows, k), np.int8), xs=np.ones(rows, np.float32), w=np.zeros((1, n, k), np.int8), ws=np.ones((1, n), np.float32))
+    c["x"][:, 0], c["x"][:, 1] = 1, 3
+    c["w"][0, :256, 0], c["w"][0, 256:, 1] = np.arange(256) - 128, 1
+    c["ws"][0, :256] = 0.8671875
+    c["xs"][1] = 7.0
+    check(c, None, "swiglu", dtype, what="range of gates")
+    c["xs"][2] = np.inf                                        # gates of +-inf, NaN where the sum is 0
+    out = F.moe_grouped_matmul_int8(dev(c["x"]), dev(c["xs"]), dev(c["w"]), dev(c["ws"]), out_dtype=FP32, epilogue=F.FFNWB_EPI_SWIGLU)["y"]
+    torch.cuda.synchronize()
+    assert bool(out[2, :129].isnan().all()) and bool((out[2, 129:] == float("inf")).all())

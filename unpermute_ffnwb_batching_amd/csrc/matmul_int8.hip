@@ -82,7 +82,7 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
     for (int32_t w = 0; w < waves; ++w)
 #pragma unroll
       for (int f = 0; f < NF; ++f) s[f] += red8[(w * NF * MT + f * MT + i) * kWave + lane];
-    if (i * 16 + r >= rt.rows) continue;
+    if (i * 16 + r >= rt.rows) continue;  // the four lanes of a row together
     const int64_t row = rt.row0 + i * 16 + r;
     const float xs = a.x_scale[row * a.xss];
     f32x4 p[NF];
@@ -90,9 +90,13 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
     for (int f = 0; f < NF; ++f) p[f] = scaled(s[f], xs, channel_scales(a, rt.expert, n0 + f * a.F + g * 4));
     if constexpr (EPI == FFNWB_EPI_SWIGLU) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[0][j] = swiglu(p[0][j], p[1][j]);
+      for (int j = 0; j < 4; ++j) p[0][j] = swiglu_fast(p[0][j], p[1][j]);
     }
-    store4<T>(a.y + row * a.ys, n0 + g * 4, a.F, p[0], a.vec);
+    if constexpr (T::kHeld) {
+      *reinterpret_cast<u32x2*>(a.y + row * a.ys + (n0 + g * 4) * 2) = narrow4<T>(a, p[0], row, n0 + g * 4, true);
+    } else {
+      store4<typename T::Out>(a.y + row * a.ys, n0 + g * 4, a.F, p[0], a.vec);
+    }
   }
 }
 
@@ -100,8 +104,7 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
 //
 // Products split over K: whole-number sums [parts][R][N rounded up to 8], whose order does not
 // matter.  16 lanes take 128 outputs of a row; a workgroup takes 16 such blocks of a row tile, so
-// that rows of no expert stay as they were.  FP32 results on their way to INT8 go to the FP32 rows
-// that mm8_rows_kernel takes.
+// that rows of no expert stay as they were.
 
 constexpr int kJoin8Threads = 256;
 
@@ -135,62 +138,58 @@ __global__ __launch_bounds__(kJoin8Threads) void mm8_join_kernel(Mm8Args a, cons
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[h][j] = swiglu(f[h][j], up[h][j]);
+      for (int j = 0; j < 4; ++j) f[h][j] = swiglu_fast(f[h][j], up[h][j]);
   }
   char* y = a.y + row * a.ys;
-  store4<T>(y, f0, a.F, f[0], a.vec);
-  store4<T>(y, f0 + 4, a.F, f[1], a.vec);
+  if constexpr (T::kHeld) {
+    uint32_t m = 0;  // of the 16 columns of two lanes
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(f[h][j]) & 0x7fffffffu);
+    m = max(m, lane_dpp<0xb1>(m));
+    if (f0 % 16 == 0) a.held_max[row * (a.F / 16) + f0 / 16] = __uint_as_float(m);
+    const float per_unit = __builtin_amdgcn_rcpf(held_unit(__uint_as_float(m)));
+    *reinterpret_cast<u32x4*>(y + f0 * 2) = u32x4{held2(f[0][0], f[0][1], per_unit), held2(f[0][2], f[0][3], per_unit),
+                                                  held2(f[1][0], f[1][1], per_unit), held2(f[1][2], f[1][3], per_unit)};
+  } else {
+    store4<typename T::Out>(y, f0, a.F, f[0], a.vec);
+    store4<typename T::Out>(y, f0 + 4, a.F, f[1], a.vec);
+  }
 }
 
 // ------------------------------------------------------------------ INT8 results
 //
-// FP32 rows [R][F] to INT8, with the row's scale: a wave to a row, 4 rows of a row tile to a
-// workgroup.  C: runs of 8 elements that a lane holds; 0: the row is read twice instead.
+// Held rows [R][F] to INT8, with the row's scale: a wave to a row, 4 rows of a row tile to a workgroup.  The
+// row's largest value is that of its fragments, so its elements are read once, whatever the length.
 
-template <int C>
-__global__ __launch_bounds__(256) void mm8_rows_kernel(Mm8Args a, const float* h, int64_t pitch, int32_t bm) {
+constexpr int kRows8 = 4;
+
+__global__ __launch_bounds__(kRows8* kWave) void mm8_rows_kernel(Mm8Args a, const char* held, int32_t bm) {
   RowTile rt;
   int32_t group;
   if (!find_tile(a, bm, rt, group)) return;
-  const int32_t i = group * 4 + uniform(threadIdx.x / kWave), t = threadIdx.x % kWave;
+  const int32_t i = group * kRows8 + uniform(threadIdx.x / kWave), t = threadIdx.x % kWave;
   if (i >= rt.rows) return;
   const int64_t row = rt.row0 + i;
-  const char* from = reinterpret_cast<const char*>(h + row * pitch);
-  char* q = a.y + row * a.ys;
   const int32_t F = static_cast<int32_t>(a.F);
-  float v[C > 0 ? C : 1][8] = {}, none = 0.0f;
-  uint32_t m = 0, lo, hi;
-  auto gather = [&](int32_t h0, float (&f)[8]) {
-    Raw<TF32> raw;
-    load_raw<TF32, false>(from, h0, F, raw);  // F is a multiple of 16
-    widen_raw(raw, f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
-  };
-  if constexpr (C > 0) {
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if ((j * kWave + t) * 8 < F) gather((j * kWave + t) * 8, v[j]);
-  } else {
-    for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) gather(h0, v[0]);
-  }
-  row_reduce<64, false>(none, m, 0);
-  const float s = row_scale(__uint_as_float(m));
+  const float* largest = a.held_max + row * (F / 16);
+  uint32_t m = 0;
+  for (int32_t f = t; f < F / 16; f += kWave) m = max(m, __float_as_uint(largest[f]));
+  const float s = row_scale(__uint_as_float(lanes_max<64>(m)));
   if (t == 0) a.y_scale[row * a.yss] = s;
-  if constexpr (C > 0) {
+  const char* from = held + row * F * 2;
+  char* q = a.y + row * a.ys;
+#pragma unroll 2
+  for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) {
+    const u32x4 v = *reinterpret_cast<const u32x4*>(from + h0 * 2);
+    const float unit = held_unit(largest[h0 / 16]);
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int32_t h0 = (j * kWave + t) * 8;
-      if (h0 >= F) continue;
-      quant_int8(v[j], s, lo, hi);
-      store_bytes<false>(q, h0, F, lo, hi);
-    }
-  } else {
-    for (int32_t h0 = t * 8; h0 < F; h0 += kWave * 8) {
-      gather(h0, v[0]);
-      quant_int8(v[0], s, lo, hi);
-      store_bytes<false>(q, h0, F, lo, hi);
-    }
+    for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int32_t>(j % 2 ? v[j / 2] : v[j / 2] << 16) >> 16) * unit;
+    uint32_t lo, hi;
+    quant_int8(f, s, lo, hi);
+    *reinterpret_cast<u32x2_a1*>(q + h0) = u32x2{lo, hi};
   }
 }
 
@@ -278,7 +277,7 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
     p->join = p->parts > 1;
     p->join_groups = p->join ? (p->bm * ((p->F + 127) / 128) + kJoin8Threads / 16 - 1) / (kJoin8Threads / 16) : 0;
     int64_t most = p->join_groups > p->ntiles ? p->join_groups : p->ntiles;
-    if (quant && p->bm / 4 > most) most = p->bm / 4;
+    if (quant && p->bm / kRows8 > most) most = p->bm / kRows8;
     return p->mtiles * most;
   };
   // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  256 rows
@@ -315,7 +314,7 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
     c.take<int4>(static_cast<size_t>(p->mtiles));
   }
   if (p->join) c.take<int32_t>(static_cast<size_t>(p->parts * p->R * p->pitch));
-  if (p->quant) c.take<float>(static_cast<size_t>(p->R * p->F));
+  if (p->quant) c.take<uint16_t>(static_cast<size_t>(p->R * p->F)), c.take<float>(static_cast<size_t>(p->R * p->F / 16));
   p->ws_bytes = c.off;
   return FFNWB_OK;
 }
@@ -343,9 +342,9 @@ template <class T, int EPI>
 static bool launch_product8(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
   if constexpr (!T::kWhole) {
     if (!p.tile)
-      return p.bm == 16   ? launch_direct8_rows<typename T::Out, EPI, 1>(a, p, s, b, e)
-             : p.bm == 32 ? launch_direct8_rows<typename T::Out, EPI, 2>(a, p, s, b, e)
-                          : launch_direct8_rows<typename T::Out, EPI, 4>(a, p, s, b, e);
+      return p.bm == 16   ? launch_direct8_rows<T, EPI, 1>(a, p, s, b, e)
+             : p.bm == 32 ? launch_direct8_rows<T, EPI, 2>(a, p, s, b, e)
+                          : launch_direct8_rows<T, EPI, 4>(a, p, s, b, e);
   }
   return p.bm == 256   ? launch_tile8_shape<T, EPI, 2, 4, 8>(a, p, s, b, e)
          : p.bm == 128 ? launch_tile8_shape<T, EPI, 2, 4, 4>(a, p, s, b, e)
@@ -375,15 +374,14 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
     a.table = table, a.count = count;
   }
   int32_t* sums = p.join ? c.take<int32_t>(static_cast<size_t>(p.parts * p.R * p.pitch)) : nullptr;
-  float* rows = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
+  uint16_t* held = p.quant ? c.take<uint16_t>(static_cast<size_t>(p.R * p.F)) : nullptr;
+  a.held_max = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F / 16)) : nullptr;
   void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
-  // results in their own type, or FP32 rows on their way to INT8
+  // results in their own type, or rows held on their way to INT8
   Mm8Args out = a;
-  const int32_t dt = p.quant ? static_cast<int32_t>(FFNWB_DT_FP32) : d->out_dtype;
-  const uint64_t elt = static_cast<uint64_t>(out_size8(dt));
-  if (p.quant) out.y = reinterpret_cast<char*>(rows), out.ys = p.F * 4;
-  const uint64_t at = reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys);
-  out.vec = (at & (4 * elt - 1)) == 0;
+  const int32_t dt = d->out_dtype;
+  if (p.quant) out.y = reinterpret_cast<char*>(held), out.ys = p.F * 2;
+  out.vec = ((reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys)) & (4 * static_cast<uint64_t>(out_size8(dt)) - 1)) == 0;
   void* out_end = p.quant ? nullptr : e;
   // the product: results, or whole-number sums for the join
   Mm8Args m = out;
@@ -400,25 +398,25 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
       auto join = [&](auto kernel) {
         return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.join_groups)), dim3(kJoin8Threads), 0, s, nullptr, out_end, out, sums, pitch, parts, bm);
       };
-      ok = dt == FFNWB_DT_FP16   ? (p.swiglu ? join(mm8_join_kernel<TF16, true>) : join(mm8_join_kernel<TF16, false>))
-           : dt == FFNWB_DT_BF16 ? (p.swiglu ? join(mm8_join_kernel<TBF16, true>) : join(mm8_join_kernel<TBF16, false>))
-                                 : (p.swiglu ? join(mm8_join_kernel<TF32, true>) : join(mm8_join_kernel<TF32, false>));
+      ok = dt == FFNWB_DT_INT8   ? join(mm8_join_kernel<Held, true>)
+           : dt == FFNWB_DT_FP16 ? (p.swiglu ? join(mm8_join_kernel<Scaled<TF16>, true>) : join(mm8_join_kernel<Scaled<TF16>, false>))
+           : dt == FFNWB_DT_BF16 ? (p.swiglu ? join(mm8_join_kernel<Scaled<TBF16>, true>) : join(mm8_join_kernel<Scaled<TBF16>, false>))
+                                 : (p.swiglu ? join(mm8_join_kernel<Scaled<TF32>, true>) : join(mm8_join_kernel<Scaled<TF32>, false>));
     }
+  } else if (p.swiglu) {
+    ok = dt == FFNWB_DT_INT8   ? launch_product8<Held, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end)
+         : dt == FFNWB_DT_FP16 ? launch_product8<Scaled<TF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end)
+         : dt == FFNWB_DT_BF16 ? launch_product8<Scaled<TBF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end)
+                               : launch_product8<Scaled<TF32>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end);
   } else {
-    ok = dt == FFNWB_DT_FP16   ? (p.swiglu ? launch_product8<Scaled<TF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end) : launch_product8<Scaled<TF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end))
-         : dt == FFNWB_DT_BF16 ? (p.swiglu ? launch_product8<Scaled<TBF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end) : launch_product8<Scaled<TBF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end))
-                               : (p.swiglu ? launch_product8<Scaled<TF32>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end) : launch_product8<Scaled<TF32>, FFNWB_EPI_NONE>(m, p, s, b, out_end));
+    ok = dt == FFNWB_DT_FP16   ? launch_product8<Scaled<TF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end)
+         : dt == FFNWB_DT_BF16 ? launch_product8<Scaled<TBF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end)
+                               : launch_product8<Scaled<TF32>, FFNWB_EPI_NONE>(m, p, s, b, out_end);
   }
   if (ok && p.quant) {
-    a.ntiles = bm / 4;
-    const int64_t pitch = p.F;
-    auto quant = [&](auto kernel) {
-      return launch_bound(kernel, dim3(tile_grid(p.mtiles * a.ntiles)), dim3(256), 0, s, nullptr, e, a, static_cast<const float*>(rows), pitch, bm);
-    };
-    ok = p.F <= 512    ? quant(mm8_rows_kernel<1>)
-         : p.F <= 1024 ? quant(mm8_rows_kernel<2>)
-         : p.F <= 2048 ? quant(mm8_rows_kernel<4>)
-                       : quant(mm8_rows_kernel<0>);
+    a.ntiles = bm / kRows8;
+    ok = launch_bound(mm8_rows_kernel, dim3(tile_grid(p.mtiles * a.ntiles)), dim3(kRows8 * kWave), 0, s, nullptr, e, a,
+                      reinterpret_cast<const char*>(held), bm);
   }
   return ok ? FFNWB_OK : FFNWB_ERR_RUNTIME;
 }

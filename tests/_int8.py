@@ -5,7 +5,8 @@ the operators' own arithmetic.
   products with scales: 3 half-units of 2^-24 of the result, whatever cancels (``PRODUCT``).
 * SwiGLU, in half-units of 2^-24 relative: the exponential 2 and its correction 2 (at most as much in the
   sigmoid), its product with the sum 1, the reciprocal 2, two products 2: 9, and 1 for the rest of the
-  exponent (``SWIGLU``).
+  exponent (``SWIGLU``).  Results that are rounded to 16 or 8 bits add |gate| half-units and 1 % for the
+  exponent's own rounding, twice (the product with log2(e), and log2(e) itself).
 * The norm sums squares in FP32, all terms positive: each addition loses half a unit of the sum
   so far, so the sum is off by (additions one after another) * 2^-24 relative: a thread's own
   elements (at most 32, or H / 1024 of them in rows read twice), 6 steps of a wave, 16 waves.  Half of that
@@ -43,15 +44,16 @@ def matmul_inputs(seed, rows, k, n, experts=1):
                 ws=(rng.uniform(0.5, 1.5, (experts, n)) / (50 * np.sqrt(k))).astype(np.float32))
 
 
-def matmul_reference(c, groups=None, epilogue="none"):
-    """(values, how far 32-bit arithmetic may be off, rows written)."""
+def matmul_reference(c, groups=None, epilogue="none", dtype=torch.bfloat16):
+    """(values, how far 32-bit arithmetic may be off, rows written); dtype: of the result."""
     y, p, written = O.grouped_matmul(c["x"], c["xs"], c["w"], c["ws"], groups, epilogue)
     off = PRODUCT * np.abs(p)
     if epilogue == "none":
         return y, off, written
     f = p.shape[1] // 2
     gate, up, dg, du = p[:, :f], p[:, f:], off[:, :f], off[:, f:]
-    return y, 1.1 * dg * (np.abs(up) + du) + np.abs(expert_ffn.silu(gate)) * du + SWIGLU * np.abs(y), written
+    swiglu = SWIGLU + (0 if dtype == torch.float32 else 2.02 * np.abs(gate) * 2.0 ** -24)
+    return y, 1.1 * dg * (np.abs(up) + du) + np.abs(expert_ffn.silu(gate)) * du + swiglu * np.abs(y), written
 
 
 def close(got, want, off, dtype):

@@ -34,7 +34,7 @@ def check(c, groups=None, epilogue="none", out_dtype=BF16, pad=0, what=""):
     print(f"int8 product {c['x'].shape} x {c['w'].shape} {NAMES[out_dtype]} {epilogue} {what} {plan}", flush=True)
     call.run()
     torch.cuda.synchronize()
-    want, off, written = matmul_reference(c, groups, epilogue)
+    want, off, written = matmul_reference(c, groups, epilogue, out_dtype)
     w = dev(written)
     if out_dtype == I8:
         quantised_close(out["y"][w], out["y_scale"][w], want[written], off[written], held=True)
@@ -173,7 +173,7 @@ def test_quantised_rows_that_are_not_finite_or_zero():
     assert np.isnan(s[3]) and not np.isfinite(s[4]) and s[5] == 2.0 ** -126
     assert (q[3:6] == 0).all()
     keep = np.delete(np.arange(40), [3, 4])
-    want, off, _ = matmul_reference(dict(c, xs=np.nan_to_num(c["xs"], posinf=0)), None, "swiglu")
+    want, off, _ = matmul_reference(dict(c, xs=np.nan_to_num(c["xs"], posinf=0)), None, "swiglu", I8)
     quantised_close(out["y"][dev(keep)], out["y_scale"][dev(keep)], want[keep], off[keep], held=True)
 
 

@@ -85,18 +85,23 @@ __device__ __forceinline__ void join_columns(uint32_t& a, uint32_t& b) {
   a = q[0], b = q[1];
 }
 
-// silu(g) * u as swiglu (fp8_block.hpp), with the hardware's exponential and reciprocal (2^-23 each): 13
-// operations instead of about 45 (131072 rows by 1024 outputs over 4096: 1189 -> 1130 us).  The exponent of 2 is
-// -g log2(e) in two parts, so that its rounding does not grow with |g|.  exp overflows to infinity for
-// very negative g, which gives the limit -0; g = -inf is NaN.
+// silu(g) * u as swiglu (fp8_block.hpp), with the hardware's exponential and reciprocal (2^-23 each): 6
+// operations, or 11, instead of about 45 (131072 rows by 1024 outputs over 4096: 1189 -> 1130 us).  The
+// exponent of 2 is -g log2(e); its rounding is an error of |g| 2^-24 of the result, up to 6e-6, which is far
+// below the rounding to 16 bits or INT8 but not below that to FP32: there (kExact) the exponent is in two
+// parts.  exp overflows to infinity for very negative g, which gives the limit -0; g = -inf is NaN.
+template <bool kExact>
 __device__ __forceinline__ float swiglu_fast(float g, float u) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500011e-8f, kLn2 = 0.693147180559945f;
   const float x = -g * kLog2e;
-  const float rest = __builtin_fmaf(-g, kLog2eRest, __builtin_fmaf(-g, kLog2e, -x));
   const float e = __builtin_amdgcn_exp2f(x);
-  // at most 2^-16 where e matters; the bound is for g = inf, whose rest is NaN
-  const float more = __builtin_fmaf(fminf(fmaxf(rest, -0.001f), 0.001f), kLn2, 1.0f);
-  return g * __builtin_amdgcn_rcpf(__builtin_fmaf(e, more, 1.0f)) * u;
+  float sum = 1.0f + e;
+  if constexpr (kExact) {
+    const float rest = __builtin_fmaf(-g, kLog2eRest, __builtin_fmaf(-g, kLog2e, -x));
+    // at most 2^-16 where e matters; the bound is for g = inf, whose rest is NaN
+    sum = __builtin_fmaf(e, __builtin_fmaf(fminf(fmaxf(rest, -0.001f), 0.001f), kLn2, 1.0f), 1.0f);
+  }
+  return g * __builtin_amdgcn_rcpf(sum) * u;
 }
 
 // Rows on their way to INT8 are held in 16 bits, as whole numbers of units, 65534 of which are the span of a
@@ -124,9 +129,9 @@ __device__ __forceinline__ uint32_t fragment_max(const f32x4& v) {
 }
 
 // What a product writes: whole-number sums, results of a type, or held rows.
-struct Whole { static constexpr bool kWhole = true, kHeld = false; using Out = TF32; };
-template <class T> struct Scaled { static constexpr bool kWhole = false, kHeld = false; using Out = T; };
-struct Held { static constexpr bool kWhole = false, kHeld = true; using Out = TF16; };  // 2 bytes
+struct Whole { static constexpr bool kWhole = true, kHeld = false, kExact = true; using Out = TF32; };
+template <class T> struct Scaled { static constexpr bool kWhole = false, kHeld = false, kExact = T::kBytes == 4; using Out = T; };
+struct Held { static constexpr bool kWhole = false, kHeld = true, kExact = false; using Out = TF16; };  // 2 bytes
 
 // Four results as two registers; a held fragment's largest value is stored by its first lanes.
 template <class T>
@@ -215,13 +220,8 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
     if (left <= s * 64) v = u32x4{0, 0, 0, 0};
   };
 
-  fetch_x(0);
-  fetch_w(0);
-  if (kb > 1) {
-    fetch_x(1);
-    if constexpr (S::kAhead) fetch_w(1);
-  }
-  // The scales of the wave's rows and columns, loaded among the last products.
+  // The scales of the wave's rows and columns: loaded among the last products where registers are
+  // short, ahead of the first copies else.
   float xs[MF];
   f32x4 ws[NF];
   const int64_t n0 = c0 + wn * (kSwiglu ? NF * 8 : NF * 16) + g * 4;  // the lane's first column of fragment 0
@@ -234,6 +234,13 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
         ws[f] = channel_scales(a, rt.expert, kSwiglu && f >= NF / 2 ? a.F + n0 + (f - NF / 2) * 16 : n0 + f * 16);
     }
   };
+  if constexpr (!S::kAhead) scales();
+  fetch_x(0);
+  fetch_w(0);
+  if (kb > 1) {
+    fetch_x(1);
+    if constexpr (S::kAhead) fetch_w(1);
+  }
   i32x4 tot[MF][NF] = {};
   if constexpr (S::kAhead) {
     // A block's two halves are multiplied from fragments read before: w's in the half before, x's two
@@ -314,7 +321,6 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
       copies_done<S::kXCopies + S::kWCopies>(b + 2 < kb);
     }
   }
-  if constexpr (!S::kAhead) scales();
 
   // Results go from registers to memory: a lane holds 4 adjacent columns of a row, in 16-bit types 8 after
   // an exchange between two fragments, so that a store writes 64 adjacent bytes of 16 rows.
@@ -339,7 +345,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
         if constexpr (kSwiglu) {
           const f32x4 up = scaled(tot[i][OF + f], xs[i], ws[OF + f]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[f][j] = swiglu_fast(v[f][j], up[j]);
+          for (int j = 0; j < 4; ++j) v[f][j] = swiglu_fast<T::kExact>(v[f][j], up[j]);
         }
       }
       if constexpr (Out::kBytes == 4) {

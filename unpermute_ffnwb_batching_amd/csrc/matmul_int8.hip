@@ -33,6 +33,16 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
   const char* xp[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) xp[i] = a.x + static_cast<int64_t>(rt.row0 + min(i * 16 + r, rt.rows - 1)) * a.xs;
+  // The scales: ahead of the blocks, where there are registers (MT = 4 would lose a wave of three).
+  f32x4 ws[NF];
+  float xs[MT];
+  auto scales = [&] {
+#pragma unroll
+    for (int f = 0; f < NF; ++f) ws[f] = channel_scales(a, rt.expert, n0 + f * a.F + g * 4);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xs[i] = load_f32(a.x_scale + (rt.row0 + min(i * 16 + r, rt.rows - 1)) * a.xss);
+  };
+  if constexpr (MT < 4) scales();
   struct Block {
     u32x4 w[NF][2], x[MT][2];
   } blk[2];
@@ -76,21 +86,23 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
   for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int i = 0; i < MT; ++i) red8[(wave * NF * MT + f * MT + i) * kWave + lane] = tot[f][i];
+  if constexpr (MT >= 4) scales();
   __syncthreads();
-  for (int32_t i = wave; i < MT; i += waves) {
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    if (i % waves != wave) continue;
     i32x4 s[NF] = {};
     for (int32_t w = 0; w < waves; ++w)
 #pragma unroll
       for (int f = 0; f < NF; ++f) s[f] += red8[(w * NF * MT + f * MT + i) * kWave + lane];
     if (i * 16 + r >= rt.rows) continue;  // the four lanes of a row together
     const int64_t row = rt.row0 + i * 16 + r;
-    const float xs = a.x_scale[row * a.xss];
     f32x4 p[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) p[f] = scaled(s[f], xs, channel_scales(a, rt.expert, n0 + f * a.F + g * 4));
+    for (int f = 0; f < NF; ++f) p[f] = scaled(s[f], xs[i], ws[f]);
     if constexpr (EPI == FFNWB_EPI_SWIGLU) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[0][j] = swiglu_fast(p[0][j], p[1][j]);
+      for (int j = 0; j < 4; ++j) p[0][j] = swiglu_fast<T::kExact>(p[0][j], p[1][j]);
     }
     if constexpr (T::kHeld) {
       *reinterpret_cast<u32x2*>(a.y + row * a.ys + (n0 + g * 4) * 2) = narrow4<T>(a, p[0], row, n0 + g * 4, true);
@@ -138,7 +150,7 @@ __global__ __launch_bounds__(kJoin8Threads) void mm8_join_kernel(Mm8Args a, cons
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f[h][j] = swiglu_fast(f[h][j], up[h][j]);
+      for (int j = 0; j < 4; ++j) f[h][j] = swiglu_fast<T::kExact>(f[h][j], up[h][j]);
   }
   char* y = a.y + row * a.ys;
   if constexpr (T::kHeld) {

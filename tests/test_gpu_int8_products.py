@@ -124,9 +124,9 @@ def test_large(rows, k, n, dtype, epilogue, experts):
 
 
 # few tiles and a long K, which is split: parts that do not divide it, odd widths, rows behind
-SPLIT = [(128, 7168, 1000, BF16, "none", 0), (128, 7184, 1001, FP32, "none", 0), (300, 6160, 333, FP16, "none", 0),
-         (520, 4112, 1504, FP32, "swiglu", 0), (260, 8192, 1056, BF16, "swiglu", 0), (330, 8000, 800, I8, "swiglu", 0),
-         (1000, 8192, 1056, I8, "swiglu", 3), (260, 8000, 1000, BF16, "none", 2), (200, 12304, 600, FP32, "none", 2)]
+SPLIT = [(300, 6160, 1333, FP16, "none", 0), (256, 7184, 2048, BF16, "none", 0), (520, 4112, 1504, FP32, "swiglu", 0),
+         (260, 8192, 2080, BF16, "swiglu", 0), (330, 8000, 1600, I8, "swiglu", 0), (1000, 8192, 1056, I8, "swiglu", 3),
+         (400, 12304, 1201, FP32, "none", 2), (200, 12304, 600, FP32, "none", 2)]
 
 
 @pytest.mark.parametrize("rows,k,n,dtype,epilogue,experts", SPLIT)

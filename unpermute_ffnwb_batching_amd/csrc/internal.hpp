@@ -171,6 +171,7 @@ struct Int8MatmulPlan {
   int64_t xs = 0, xss = 0, ys = 0, yss = 0;    // row strides: bytes, elements, bytes, elements
   bool swiglu = false;
   bool quant = false;                          // INT8 rows out, by a second launch
+  bool fp32 = false;                           // FP32 rows out
   bool tile = false;                           // through LDS, else straight to registers
   int64_t bm = 0;                              // rows of a tile
   int64_t kb = 0;                              // 128-column blocks of K

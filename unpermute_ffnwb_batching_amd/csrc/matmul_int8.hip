@@ -213,6 +213,7 @@ static int64_t rows8_lanes(int64_t F) { return F <= 512 ? 16 : 64; }
 // ------------------------------------------------------------------ host side
 
 constexpr int64_t kCus8 = 256;
+constexpr int64_t kListedTiles8 = 16 * kCus8;  // more tiles of grouped rows are listed by a launch of their own
 
 static int64_t out_size8(int32_t dt) { return dt == FFNWB_DT_FP32 ? 4 : dt == FFNWB_DT_INT8 ? 1 : 2; }
 
@@ -225,30 +226,33 @@ static int direct_waves8(int64_t tiles, int64_t kb, int64_t bm) {
 }
 
 // Microseconds that a product takes with the given kernel and tile rows, as far as the choice
-// between them needs it.
-static double expected_us8(int64_t rows, int64_t N, int64_t K, int64_t F, int64_t groups, bool swiglu, bool tile, int64_t bm,
-                           int64_t parts) {
-  const int64_t kb = (K + 127) / 128, some = groups < rows ? groups : rows;
-  const double mt = groups > 0 ? static_cast<double>(rows) / bm + 0.58 * some : static_cast<double>((rows + bm - 1) / bm);
-  auto rounds = [](double wgs, int64_t together) { return wgs <= together ? 1.0 : __builtin_ceil(wgs / together); };
-  if (tile) {
-    const double tiles = parts > 1 ? mt * ((N + 255) / 256) * parts : mt * ((F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256));
-    const double join = parts > 1 ? 4.1 + parts * rows * N * 8 / 5430e3 : 0.0;  // a launch, sums written and read
-    double us = bm == 256 ? 1.53 : bm == 128 ? 0.98 : 0.79;
-    int64_t together = kCus8;
-    if (bm == 32) {  // two to a CU
-      us = tiles > kCus8 ? 1.2 : 0.65;
-      together = 2 * kCus8;
-    }
-    return 2.8 + rounds(tiles, together) * ((kb + parts - 1) / parts * us + 2.7) + join;
+// between them needs it: rounds of workgroups that fit the chip together times what one needs for
+// its blocks of K, or the time of the weights and results in memory if that is longer.  The figures
+// are fitted so that the least of them picks the fastest shape, and are not those of the parts.
+static double expected_us8(const Int8MatmulPlan& p, int64_t groups) {
+  const int64_t some = groups < p.R ? groups : p.R, elt = p.quant || p.fp32 ? 4 : 2;
+  const double mt = groups > 0 ? static_cast<double>(p.R) / p.bm + 0.7 * some : static_cast<double>((p.R + p.bm - 1) / p.bm);
+  const double results = static_cast<double>(p.R * p.F * elt) / 2.42e6, wgs = mt * p.ntiles;
+  auto rounds = [](double n, double together) { return n <= together ? 1.0 : __builtin_ceil(n / together); };
+  double us = 2.6;
+  if (groups > kWaveGroups || (groups > 0 && p.mtiles * p.ntiles > kListedTiles8)) us += 2.05;
+  if (p.quant) us += 3.84 + static_cast<double>(p.R * p.F) / 1.24e6;
+  if (p.tile) {
+    const bool two = p.bm < 128 && wgs > kCus8;  // two workgroups share a CU
+    const double block = p.bm == 256 ? 1.25 : p.bm == 128 ? 0.826 : p.bm == 64 ? (two ? 1.19 : 0.733) : (two ? 1.25 : 0.599);
+    const double once = p.bm == 256 ? 6.9 : p.bm == 128 ? 2.0 : two ? 2.3 : 1.6;
+    const double work = rounds(wgs, p.bm < 128 ? 2 * kCus8 : kCus8) * (p.part_blocks * block + once);
+    const double memory = (groups > 0 ? 1.09 * some : 1.0) * p.N * p.K / 6.79e6 + results;
+    if (p.parts > 1) us += 3.79 + static_cast<double>(p.parts * p.R * p.N) / 5.35e5;  // a launch, sums written and read
+    return us + (work > memory ? work : memory);
   }
-  const int64_t nt = (F + 15) / 16;
-  const int waves = direct_waves8(((rows + bm - 1) / bm + some) * nt, kb, bm);
-  const int fit = bm == 16 ? (swiglu ? 20 : 28) : bm == 32 ? (swiglu ? 12 : 20) : (swiglu ? 8 : 12);
-  const double wgs = mt * nt, us = (wgs * waves > 2048 ? 1.74 : 1.33) * (bm == 64 ? 1.63 : bm == 32 ? 1.27 : 1.0);
-  const double work = rounds(wgs, fit / waves > 0 ? fit / waves * kCus8 : kCus8) * ((kb + waves - 1) / waves * us + 0.7);
-  const double weights = mt * N * K / 5120e3;  // read again for every row tile, from L2
-  return 2.8 + (work > weights ? work : weights);
+  const int waves = direct_waves8(p.mtiles * p.ntiles, p.kb, p.bm);
+  const double fit = p.bm == 16 ? (p.swiglu ? 20 : 28) : p.bm == 32 ? (p.swiglu ? 12 : 20) : (p.swiglu ? 8 : 12);  // waves of a CU
+  const double busy = wgs * waves / kCus8 < fit ? wgs * waves / kCus8 : fit;
+  const double block = (p.bm == 64 ? 0.918 : p.bm == 32 ? 0.648 : 0.598) * (0.977 + 0.0956 * busy) * (p.swiglu ? 1.21 : 1.0);
+  const double work = rounds(wgs, (fit > waves ? fit / waves : 1.0) * kCus8) * ((p.kb + waves - 1) / waves * block + 0.22 * (1 + 1.15 * (p.bm / 16 - 1)));
+  const double memory = mt * p.N * p.K / 6.77e6 + results;  // the weights again for every row tile, from L2
+  return us + (work > memory ? work : memory);
 }
 
 int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPlan* p) {
@@ -272,6 +276,9 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
   p->N = d->out_features;
   p->F = swiglu ? d->out_features / 2 : d->out_features;
   p->kb = (p->K + 127) / 128;
+  p->swiglu = swiglu;
+  p->quant = quant;
+  p->fp32 = d->out_dtype == FFNWB_DT_FP32;
   const int64_t elt = out_size8(d->out_dtype);
   p->xs = d->x_row_stride ? d->x_row_stride : p->K;
   p->xss = d->x_scale_stride ? d->x_scale_stride : 1;
@@ -298,15 +305,19 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
     if (quant && quant_groups > most) most = quant_groups;
     return p->mtiles * most;
   };
-  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  256 rows
-  // of x, and the gate rows of w, have to be inside the 32-bit offsets of the tile kernel.
+  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  On 1500
+  // random sizes that the fit has not seen (1 to 65536 rows, K and N to 8192, 0 to 256 groups) the choice is
+  // 2.0% slower than the best of the shapes on average, more than 10% in 103 of them and 1.85 times at
+  // worst; on 700 with up to 4096 rows and K and N from 512 on, 2.6%, more than 10% in 62.  Parts are what fills the chip with a long K and few tiles: 256 rows by 2048 columns over 7168
+  // take 32 us in the best shape without and 18 us in 4 parts.
+  // 256 rows of x, and the gate rows of w, have to be inside the 32-bit offsets of the tile kernel.
   const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
   const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup
   double best = 0;
   int64_t best_bm = 0, best_parts = 1;
   auto consider = [&](int64_t bm, int64_t parts) {
     if (shape(bm, parts) > most) return;
-    const double t = expected_us8(p->R, p->N, p->K, p->F, d->num_groups, swiglu, p->tile, p->bm, p->parts);
+    const double t = expected_us8(*p, d->num_groups);
     if (best_bm == 0 || t < best) best = t, best_bm = bm, best_parts = p->parts;
   };
   for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {
@@ -321,12 +332,10 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
   }
   if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
   shape(best_bm, best_parts);
-  p->swiglu = swiglu;
-  p->quant = quant;
   p->pitch = (p->N + 7) / 8 * 8;
   p->ws_bytes = 0;
   Carve c;
-  p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > 16 * kCus8));
+  p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > kListedTiles8));
   if (p->table) {
     c.take<int32_t>(1);
     c.take<int4>(static_cast<size_t>(p->mtiles));

@@ -5,16 +5,13 @@ the operators' own arithmetic.
   products with scales: 3 half-units of 2^-24 of the result, whatever cancels (``PRODUCT``).
 * SwiGLU, in half-units of 2^-24 relative: the exponential 2 and its correction 2 (at most as much in the
   sigmoid), its product with the sum 1, the reciprocal 2, two products 2: 9, and 1 for the rest of the
-  exponent (``SWIGLU``).  Results that are rounded to 16 or 8 bits add |gate| half-units and 1 % for the
+  exponent (``SWIGLU``).  Results that are rounded to 16 bits add |gate| half-units and 1 % for the
   exponent's own rounding, twice (the product with log2(e), and log2(e) itself).
 * The norm sums squares in FP32, all terms positive: each addition loses half a unit of the sum
   so far, so the sum is off by (additions one after another) * 2^-24 relative: a thread's own
   elements (at most 32, or H / 1024 of them in rows read twice), 6 steps of a wave, 16 waves.  Half of that
   reaches the square root, then division by H, epsilon's addition, root, reciprocal (half of the
   first two reaches it), and the two products of n: ``norm_error(h)``.
-* INT8 results of a product are held in 16 bits first, in units of 1 / 32767 of the largest of 16
-  columns: off by half a unit of the row's largest at most, and 3 roundings (``HELD``); the scale
-  comes from the largest values themselves.
 * The scale of a row of n follows its largest value, whose error it shares, with one more
   rounding; a code is within half a step of its quotient, which has one rounding.
 """
@@ -52,7 +49,7 @@ def matmul_reference(c, groups=None, epilogue="none", dtype=torch.bfloat16):
         return y, off, written
     f = p.shape[1] // 2
     gate, up, dg, du = p[:, :f], p[:, f:], off[:, :f], off[:, f:]
-    swiglu = SWIGLU + (0 if dtype == torch.float32 else 2.02 * np.abs(gate) * 2.0 ** -24)
+    swiglu = SWIGLU + (0 if dtype in (torch.float32, torch.int8) else 2.02 * np.abs(gate) * 2.0 ** -24)
     return y, 1.1 * dg * (np.abs(up) + du) + np.abs(expert_ffn.silu(gate)) * du + swiglu * np.abs(y), written
 
 
@@ -63,19 +60,14 @@ def close(got, want, off, dtype):
     assert not bad.any(), (int(bad.sum()), got[bad][:3], want[bad][:3], room[bad][:3])
 
 
-HELD = 1 / 65534 + 3 * 2.0 ** -24
-
-
-def quantised_close(q, scale, want, off, held=False):
-    """INT8 rows and scales of finite values that are off by at most `off`; held: of a product."""
+def quantised_close(q, scale, want, off):
+    """INT8 rows and scales of finite values that are off by at most `off`."""
     assert q.dtype == torch.int8
     q, scale = host(q), host(scale)
     amax, far = np.abs(want).max(1), off.max(1)
     assert (np.abs(scale - np.maximum(amax / 127, 2.0 ** -126)) <= far / 127 + (amax + far) / 127 * 2.0 ** -24 + 2.0 ** -149).all()
     # half a step of the scale in use, the quotient's rounding (at most 127 * 2^-24 steps), and the value's error
     room = scale[:, None] * (0.5 + 127 * 2.0 ** -24) + off
-    if held:
-        room = room + (amax + far)[:, None] * HELD
     bad = ~(np.abs(q * scale[:, None] - want) <= room * (1 + 2.0 ** -40))
     assert not bad.any(), (int(bad.sum()), q[bad][:3], want[bad][:3])
     some = amax > 2.0 ** -100

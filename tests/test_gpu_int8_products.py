@@ -37,7 +37,7 @@ def check(c, groups=None, epilogue="none", out_dtype=BF16, pad=0, what=""):
     want, off, written = matmul_reference(c, groups, epilogue, out_dtype)
     w = dev(written)
     if out_dtype == I8:
-        quantised_close(out["y"][w], out["y_scale"][w], want[written], off[written], held=True)
+        quantised_close(out["y"][w], out["y_scale"][w], want[written], off[written])
         side = out["y_scale"]._base.view(FP32).reshape(rows, 3)
         assert untouched(side[~w]) and untouched(side[:, :1]) and untouched(side[:, 2:])
     else:
@@ -174,7 +174,7 @@ def test_quantised_rows_that_are_not_finite_or_zero():
     assert (q[3:6] == 0).all()
     keep = np.delete(np.arange(40), [3, 4])
     want, off, _ = matmul_reference(dict(c, xs=np.nan_to_num(c["xs"], posinf=0)), None, "swiglu", I8)
-    quantised_close(out["y"][dev(keep)], out["y_scale"][dev(keep)], want[keep], off[keep], held=True)
+    quantised_close(out["y"][dev(keep)], out["y_scale"][dev(keep)], want[keep], off[keep])
 
 
 def test_no_rows():

@@ -33,7 +33,7 @@ def _check_product(got, x, xs, w, ws, groups, epilogue, dtype):
     want, off, written = matmul_reference(c, groups, epilogue, dtype)
     assert written.all()
     if dtype == I8:
-        quantised_close(got["y"][:len(want)], got["y_scale"][:len(want)], want, off, held=True)
+        quantised_close(got["y"][:len(want)], got["y_scale"][:len(want)], want, off)
     else:
         close(got["y"][:len(want)], want, off, dtype)
 

@@ -44,7 +44,7 @@ def test_sizes_named_beside_the_rule():
 
 
 def test_workspaces():
-    # held rows of 2 bytes and a float for each 16 columns; nothing for a plain call
+    # FP32 rows and a float for each 16 columns; nothing for a plain call
     d = _matmul(num_rows=8, in_features=256, out_features=96, epilogue=1, out_dtype=F.FFNWB_DT_INT8)
-    assert _ws("moe_grouped_matmul_int8", d) == (0, 768 + 256)
+    assert _ws("moe_grouped_matmul_int8", d) == (0, 8 * 48 * 4 + 256)
     assert _ws("moe_grouped_matmul_int8", _matmul()) == (0, 0)

@@ -88,8 +88,8 @@ __device__ __forceinline__ void join_columns(uint32_t& a, uint32_t& b) {
 // silu(g) * u as swiglu (fp8_block.hpp), with the hardware's exponential and reciprocal (2^-23 each): 6
 // operations, or 11, instead of about 45 (131072 rows by 1024 outputs over 4096: 1189 -> 1130 us).  The
 // exponent of 2 is -g log2(e); its rounding is an error of |g| 2^-24 of the result, up to 6e-6, which is far
-// below the rounding to 16 bits or INT8 but not below that to FP32: there (kExact) the exponent is in two
-// parts.  exp overflows to infinity for very negative g, which gives the limit -0; g = -inf is NaN.
+// below the rounding to 16 bits but not below that to FP32: there (kExact), and for rows on their way to
+// INT8, the exponent is in two parts.  exp overflows to infinity for very negative g, which gives the limit -0; g = -inf is NaN.
 template <bool kExact>
 __device__ __forceinline__ float swiglu_fast(float g, float u) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500011e-8f, kLn2 = 0.693147180559945f;
@@ -104,19 +104,6 @@ __device__ __forceinline__ float swiglu_fast(float g, float u) {
   return g * __builtin_amdgcn_rcpf(sum) * u;
 }
 
-// Rows on their way to INT8 are held in 16 bits, as whole numbers of units, 65534 of which are the span of a
-// fragment's 16 columns: their largest |v| is kept beside them in FP32, and makes the unit here and
-// where they are read.  The row's scale comes from those largest values, exactly; a value is off by half a
-// unit at most, 1 / 516 of an INT8 step.  Held in FP32 instead, 16384 rows by 4096 outputs over 1024 took 335
-// us instead of 300.
-__device__ __forceinline__ float held_unit(float largest) {
-  const float u = largest * (1.0f / 32767.0f);
-  return u < 1.17549435e-38f ? 1.17549435e-38f : u;
-}
-// The low 16 bits of a + 1.5 * 2^23 are a rounded to a whole number (see quant_int8); a NaN leaves any.
-__device__ __forceinline__ uint32_t held2(float a, float b, float per_unit) {
-  return __builtin_amdgcn_perm(__float_as_uint(b * per_unit + 12582912.0f), __float_as_uint(a * per_unit + 12582912.0f), 0x05040100u);
-}
 // The largest |v| of the 16 columns that the four lanes r, r + 16, .. hold, as FP32 bits (NaN largest).
 __device__ __forceinline__ uint32_t fragment_max(const f32x4& v) {
   uint32_t m = 0;
@@ -131,19 +118,16 @@ __device__ __forceinline__ uint32_t fragment_max(const f32x4& v) {
 // What a product writes: whole-number sums, results of a type, or held rows.
 struct Whole { static constexpr bool kWhole = true, kHeld = false, kExact = true; using Out = TF32; };
 template <class T> struct Scaled { static constexpr bool kWhole = false, kHeld = false, kExact = T::kBytes == 4; using Out = T; };
-struct Held { static constexpr bool kWhole = false, kHeld = true, kExact = false; using Out = TF16; };  // 2 bytes
+struct Held { static constexpr bool kWhole = false, kHeld = true, kExact = true; using Out = TF32; };
 
-// Four results as two registers; a held fragment's largest value is stored by its first lanes.
-template <class T>
-__device__ __forceinline__ u32x2 narrow4(const Mm8Args& a, const f32x4& v, int64_t row, int64_t n, bool in) {
-  if constexpr (T::kHeld) {
-    const float m = __uint_as_float(fragment_max(v));
-    if (in && n % 16 == 0) a.held_max[row * (a.F / 16) + n / 16] = m;
-    const float per_unit = __builtin_amdgcn_rcpf(held_unit(m));
-    return u32x2{held2(v[0], v[1], per_unit), held2(v[2], v[3], per_unit)};
-  } else {
-    return u32x2{narrow2<typename T::Out>(v[0], v[1]), narrow2<typename T::Out>(v[2], v[3])};
-  }
+// Rows on their way to INT8 are held in FP32, with the largest |v| of each 16 columns beside them, so that
+// the kernel that makes them INT8 knows a row's scale without reading the row first.  Held in 16 bits
+// (whole numbers of 1 / 32767 of that largest value) they cost half the traffic, 16384 rows by 4096
+// outputs over 1024 300 us instead of 335, but one element in some hundreds then lies on the other
+// side of a rounding, 18 times the error of FP32 rows.
+__device__ __forceinline__ void store_largest(const Mm8Args& a, const f32x4& v, int64_t row, int64_t n, bool in) {
+  const uint32_t m = fragment_max(v);
+  if (in && n % 16 == 0) a.held_max[row * (a.F / 16) + n / 16] = __uint_as_float(m);
 }
 
 template <int WM, int WN, int MF>
@@ -353,6 +337,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
         for (int f = 0; f < OF; ++f) {
           const int64_t n = n0 + f * 16;
           char* to = y + n * 4;
+          if constexpr (T::kHeld) store_largest(a, v[f], rt.row0 + row, n, in && n < limit);
           if (in && n + 4 <= limit) {
             *reinterpret_cast<u32x4_a4*>(to) = __builtin_bit_cast(u32x4, v[f]);
           } else if (in) {
@@ -364,9 +349,8 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
       } else {
 #pragma unroll
         for (int f = 0; f < OF; f += 2) {
-          const u32x2 va = narrow4<T>(a, v[f], rt.row0 + row, n0 + f * 16, in && n0 + f * 16 < limit);
-          const u32x2 vb = narrow4<T>(a, v[f + 1], rt.row0 + row, n0 + (f + 1) * 16, in && n0 + (f + 1) * 16 < limit);
-          uint32_t p[2] = {va[0], va[1]}, q[2] = {vb[0], vb[1]};
+          uint32_t p[2] = {narrow2<Out>(v[f][0], v[f][1]), narrow2<Out>(v[f][2], v[f][3])};
+          uint32_t q[2] = {narrow2<Out>(v[f + 1][0], v[f + 1][1]), narrow2<Out>(v[f + 1][2], v[f + 1][3])};
           join_columns(p[0], q[0]);
           join_columns(p[1], q[1]);
           const int64_t n = n0 + f * 16 + g * 4;  // n0 holds 4 g, the lane's columns start at 8 g

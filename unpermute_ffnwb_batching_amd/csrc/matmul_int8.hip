@@ -104,11 +104,8 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
 #pragma unroll
       for (int j = 0; j < 4; ++j) p[0][j] = swiglu_fast<T::kExact>(p[0][j], p[1][j]);
     }
-    if constexpr (T::kHeld) {
-      *reinterpret_cast<u32x2*>(a.y + row * a.ys + (n0 + g * 4) * 2) = narrow4<T>(a, p[0], row, n0 + g * 4, true);
-    } else {
-      store4<typename T::Out>(a.y + row * a.ys, n0 + g * 4, a.F, p[0], a.vec);
-    }
+    if constexpr (T::kHeld) store_largest(a, p[0], row, n0 + g * 4, true);
+    store4<typename T::Out>(a.y + row * a.ys, n0 + g * 4, a.F, p[0], a.vec);
   }
 }
 
@@ -161,25 +158,21 @@ __global__ __launch_bounds__(kJoin8Threads) void mm8_join_kernel(Mm8Args a, cons
       for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(f[h][j]) & 0x7fffffffu);
     m = max(m, lane_dpp<0xb1>(m));
     if (f0 % 16 == 0) a.held_max[row * (a.F / 16) + f0 / 16] = __uint_as_float(m);
-    const float per_unit = __builtin_amdgcn_rcpf(held_unit(__uint_as_float(m)));
-    *reinterpret_cast<u32x4*>(y + f0 * 2) = u32x4{held2(f[0][0], f[0][1], per_unit), held2(f[0][2], f[0][3], per_unit),
-                                                  held2(f[1][0], f[1][1], per_unit), held2(f[1][2], f[1][3], per_unit)};
-  } else {
-    store4<typename T::Out>(y, f0, a.F, f[0], a.vec);
-    store4<typename T::Out>(y, f0 + 4, a.F, f[1], a.vec);
   }
+  store4<typename T::Out>(y, f0, a.F, f[0], a.vec);
+  store4<typename T::Out>(y, f0 + 4, a.F, f[1], a.vec);
 }
 
 // ------------------------------------------------------------------ INT8 results
 //
-// Held rows [R][F] to INT8, with the row's scale: kLanes lanes to a row, 256 / kLanes rows of a row tile to a
+// Held rows (FP32 [R][F]) to INT8, with the row's scale: kLanes lanes to a row, 256 / kLanes rows of a row tile to a
 // workgroup.  The row's largest value is that of its fragments, so its elements are read once,
-// whatever the length.  131072 rows of 1024 take 89 to 100 us, 420 MB at the rate of a copy.
+// whatever the length.  131072 rows of 1024 take 127 us, 706 MB at the rate of a copy.
 
 constexpr int kRows8Threads = 256;
 
 template <int kLanes>
-__global__ __launch_bounds__(kRows8Threads) void mm8_rows_kernel(Mm8Args a, const char* held, int32_t bm) {
+__global__ __launch_bounds__(kRows8Threads) void mm8_rows_kernel(Mm8Args a, const float* held, int32_t bm) {
   RowTile rt;
   int32_t group;
   if (!find_tile(a, bm, rt, group)) return;
@@ -192,15 +185,14 @@ __global__ __launch_bounds__(kRows8Threads) void mm8_rows_kernel(Mm8Args a, cons
   for (int32_t f = t; f < F / 16; f += kLanes) m = max(m, __float_as_uint(largest[f]));
   const float s = row_scale(__uint_as_float(lanes_max<kLanes>(m)));
   if (t == 0) a.y_scale[row * a.yss] = s;
-  const char* from = held + row * F * 2;
+  const char* from = reinterpret_cast<const char*>(held + row * F);
   char* q = a.y + row * a.ys;
 #pragma unroll 2
   for (int32_t h0 = t * 8; h0 < F; h0 += kLanes * 8) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(from + h0 * 2);
-    const float unit = held_unit(largest[h0 / 16]);
+    Raw<TF32> raw;
+    load_raw<TF32, false>(from, h0, F, raw);  // F is a multiple of 16
     float f[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = static_cast<float>(static_cast<int32_t>(j % 2 ? v[j / 2] : v[j / 2] << 16) >> 16) * unit;
+    widen_raw(raw, f);
     uint32_t lo, hi;
     quant_int8(f, s, lo, hi);
     *reinterpret_cast<u32x2_a1*>(q + h0) = u32x2{lo, hi};
@@ -341,7 +333,7 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
     c.take<int4>(static_cast<size_t>(p->mtiles));
   }
   if (p->join) c.take<int32_t>(static_cast<size_t>(p->parts * p->R * p->pitch));
-  if (p->quant) c.take<uint16_t>(static_cast<size_t>(p->R * p->F)), c.take<float>(static_cast<size_t>(p->R * p->F / 16));
+  if (p->quant) c.take<float>(static_cast<size_t>(p->R * p->F)), c.take<float>(static_cast<size_t>(p->R * p->F / 16));
   p->ws_bytes = c.off;
   return FFNWB_OK;
 }
@@ -401,14 +393,15 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
     a.table = table, a.count = count;
   }
   int32_t* sums = p.join ? c.take<int32_t>(static_cast<size_t>(p.parts * p.R * p.pitch)) : nullptr;
-  uint16_t* held = p.quant ? c.take<uint16_t>(static_cast<size_t>(p.R * p.F)) : nullptr;
+  float* held = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
   a.held_max = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F / 16)) : nullptr;
   void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
   // results in their own type, or rows held on their way to INT8
   Mm8Args out = a;
   const int32_t dt = d->out_dtype;
-  if (p.quant) out.y = reinterpret_cast<char*>(held), out.ys = p.F * 2;
-  out.vec = ((reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys)) & (4 * static_cast<uint64_t>(out_size8(dt)) - 1)) == 0;
+  const uint64_t elt = p.quant ? 4 : static_cast<uint64_t>(out_size8(dt));
+  if (p.quant) out.y = reinterpret_cast<char*>(held), out.ys = p.F * 4;
+  out.vec = ((reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys)) & (4 * elt - 1)) == 0;
   void* out_end = p.quant ? nullptr : e;
   // the product: results, or whole-number sums for the join
   Mm8Args m = out;
@@ -445,7 +438,7 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
     a.ntiles = static_cast<int32_t>((p.bm * lanes + kRows8Threads - 1) / kRows8Threads);
     auto quant = [&](auto kernel) {
       return launch_bound(kernel, dim3(tile_grid(p.mtiles * a.ntiles)), dim3(kRows8Threads), 0, s, nullptr, e, a,
-                          reinterpret_cast<const char*>(held), bm);
+                          static_cast<const float*>(held), bm);
     };
     ok = lanes == 16 ? quant(mm8_rows_kernel<16>) : quant(mm8_rows_kernel<64>);
   }

@@ -829,9 +829,10 @@ int moe_grouped_matmul_int8_workspace_size(const moe_grouped_matmul_int8_desc* d
 /* Which kernels a call of *d runs, for reports and tests (host only; the errors of
    moe_grouped_matmul_int8_workspace_size). */
 typedef struct moe_grouped_matmul_int8_plan_info {
-  int32_t lds_tiles;         /* 1: tiles of 256 columns through LDS; 0: 16 columns straight to registers */
+  int32_t lds_tiles;         /* 1: tiles whose waves share both operands; 0: small ones, K split over the waves */
   int32_t tile_rows;         /* 32, 64, 128 or 256; 16, 32 or 64 */
-  int32_t k_parts;           /* parts of K, added by a launch of their own when more than one */
+  int32_t tile_columns;      /* of results */
+  int32_t waves;             /* of a workgroup that splits K; 0 with lds_tiles */
   int32_t listed;            /* 1: the row tiles are listed by a launch of their own */
 } moe_grouped_matmul_int8_plan_info;
 

@@ -15,135 +15,174 @@ pytestmark = pytest.mark.gpu
 
 BF16, FP16, FP32, I8 = torch.bfloat16, torch.float16, torch.float32, torch.int8
 
-# (rows, K, N, groups), type of the results, epilogue, kernel and tile rows, and how: "split" over K; row
+# (rows, K, N, groups), type of the results, epilogue, kernel and its tile, and how: the "waves" that split K; row
 # tiles "listed" by a launch of their own; of 128 and 256 rows, whether the last round of tiles is "halved"
 FORMS = [
-    ((20, 304, 148, 0), BF16, "none", "direct16", ""),
-    ((20, 1136, 2033, 0), BF16, "none", "direct32", ""),
-    ((623, 400, 950, 3), BF16, "none", "direct64", ""),
-    ((131, 416, 3209, 3), BF16, "none", "tiles32", ""),
-    ((4327, 272, 276, 0), BF16, "none", "tiles64", ""),
-    ((1878, 272, 1839, 3), BF16, "none", "tiles128", "halved"),
-    ((8454, 288, 283, 3), BF16, "none", "tiles128", "whole"),
-    ((6340, 944, 2543, 0), BF16, "none", "tiles256", "halved"),
-    ((8873, 912, 841, 3), BF16, "none", "tiles256", "whole"),
-    ((20, 6768, 3134, 3), BF16, "none", "tiles32", "split"),
-    ((21, 7824, 3383, 3), BF16, "none", "tiles64", "split"),
-    ((88, 3728, 2032, 3), BF16, "none", "tiles128", "split halved"),
-    ((48, 5008, 2388, 3), BF16, "none", "tiles128", "split whole"),
-    ((22, 352, 145, 300), BF16, "none", "direct16", "listed"),
-    ((218, 400, 354, 300), BF16, "none", "direct32", "listed"),
-    ((52, 272, 930, 300), BF16, "none", "tiles32", "listed"),
-    ((117, 272, 685, 300), BF16, "none", "tiles64", "listed"),
-    ((40, 368, 2080, 300), BF16, "none", "tiles128", "listed"),
-    ((22, 288, 288, 0), BF16, "swiglu", "direct16", ""),
-    ((23, 992, 3360, 3), BF16, "swiglu", "direct32", ""),
-    ((276, 400, 2208, 3), BF16, "swiglu", "direct64", ""),
-    ((53, 1104, 3392, 3), BF16, "swiglu", "tiles32", ""),
-    ((2819, 272, 576, 3), BF16, "swiglu", "tiles64", ""),
-    ((6310, 272, 1152, 0), BF16, "swiglu", "tiles128", "halved"),
-    ((8870, 320, 288, 3), BF16, "swiglu", "tiles128", "whole"),
-    ((6957, 976, 2176, 0), BF16, "swiglu", "tiles256", "halved"),
-    ((8472, 912, 800, 3), BF16, "swiglu", "tiles256", "whole"),
-    ((54, 2096, 3424, 3), BF16, "swiglu", "tiles32", "split"),
-    ((65, 2352, 3296, 3), BF16, "swiglu", "tiles64", "split"),
-    ((94, 4896, 2400, 3), BF16, "swiglu", "tiles128", "split halved"),
-    ((64, 3648, 3072, 3), BF16, "swiglu", "tiles128", "split whole"),
-    ((20, 272, 352, 300), BF16, "swiglu", "direct16", "listed"),
-    ((42, 912, 640, 300), BF16, "swiglu", "direct32", "listed"),
-    ((39, 272, 1760, 300), BF16, "swiglu", "tiles32", "listed"),
-    ((49, 272, 2272, 300), BF16, "swiglu", "tiles64", "listed"),
-    ((179, 624, 384, 300), BF16, "swiglu", "tiles128", "listed"),
-    ((20, 320, 132, 0), FP16, "none", "direct16", ""),
-    ((20, 1216, 2154, 0), FP16, "none", "direct32", ""),
-    ((396, 416, 1356, 3), FP16, "none", "direct64", ""),
-    ((164, 272, 3532, 3), FP16, "none", "tiles32", ""),
-    ((8112, 288, 136, 3), FP16, "none", "tiles64", ""),
-    ((6078, 272, 1083, 3), FP16, "none", "tiles128", "halved"),
-    ((8096, 288, 269, 3), FP16, "none", "tiles128", "whole"),
-    ((4405, 1056, 3565, 0), FP16, "none", "tiles256", "halved"),
-    ((4003, 944, 1793, 3), FP16, "none", "tiles256", "whole"),
-    ((57, 3264, 2705, 3), FP16, "none", "tiles32", "split"),
-    ((27, 5952, 2837, 3), FP16, "none", "tiles64", "split"),
-    ((120, 3168, 1964, 3), FP16, "none", "tiles128", "split halved"),
-    ((56, 4208, 2515, 3), FP16, "none", "tiles128", "split whole"),
-    ((23, 304, 131, 300), FP16, "none", "direct16", "listed"),
-    ((186, 432, 283, 300), FP16, "none", "direct32", "listed"),
-    ((328, 272, 145, 300), FP16, "none", "tiles32", "listed"),
-    ((235, 272, 339, 300), FP16, "none", "tiles64", "listed"),
-    ((60, 272, 1404, 300), FP16, "none", "tiles128", "listed"),
-    ((21, 304, 288, 0), FP16, "swiglu", "direct16", ""),
-    ((22, 1072, 3008, 0), FP16, "swiglu", "direct32", ""),
-    ((187, 416, 2848, 3), FP16, "swiglu", "direct64", ""),
-    ((76, 1056, 2720, 3), FP16, "swiglu", "tiles32", ""),
-    ((5528, 288, 288, 0), FP16, "swiglu", "tiles64", ""),
-    ((1643, 464, 2112, 3), FP16, "swiglu", "tiles128", "halved"),
-    ((8397, 320, 288, 0), FP16, "swiglu", "tiles128", "whole"),
-    ((5205, 928, 2688, 3), FP16, "swiglu", "tiles256", "halved"),
-    ((8638, 912, 896, 3), FP16, "swiglu", "tiles256", "whole"),
-    ((55, 2208, 3328, 3), FP16, "swiglu", "tiles32", "split"),
-    ((68, 2384, 3424, 3), FP16, "swiglu", "tiles64", "split"),
-    ((123, 4432, 2528, 3), FP16, "swiglu", "tiles128", "split halved"),
-    ((64, 3088, 3488, 3), FP16, "swiglu", "tiles128", "split whole"),
-    ((21, 304, 288, 300), FP16, "swiglu", "direct16", "listed"),
-    ((24, 912, 1152, 300), FP16, "swiglu", "direct32", "listed"),
-    ((71, 288, 1024, 300), FP16, "swiglu", "tiles32", "listed"),
-    ((101, 272, 1120, 300), FP16, "swiglu", "tiles64", "listed"),
-    ((180, 544, 320, 300), FP16, "swiglu", "tiles128", "listed"),
-    ((20, 272, 148, 3), FP32, "none", "direct16", ""),
-    ((22, 608, 3469, 0), FP32, "none", "direct32", ""),
-    ((3697, 400, 162, 3), FP32, "none", "direct64", ""),
-    ((137, 400, 2958, 3), FP32, "none", "tiles32", ""),
-    ((8168, 288, 130, 3), FP32, "none", "tiles64", ""),
-    ((8633, 304, 792, 3), FP32, "none", "tiles128", "halved"),
-    ((8056, 272, 270, 3), FP32, "none", "tiles128", "whole"),
-    ((8115, 928, 788, 3), FP32, "none", "tiles256", "whole"),
-    ((68, 3104, 2139, 3), FP32, "none", "tiles32", "split"),
-    ((22, 7248, 3325, 3), FP32, "none", "tiles64", "split"),
-    ((121, 4304, 1574, 3), FP32, "none", "tiles128", "split halved"),
-    ((47, 4752, 2430, 3), FP32, "none", "tiles128", "split whole"),
-    ((20, 272, 139, 300), FP32, "none", "direct16", "listed"),
-    ((198, 400, 272, 300), FP32, "none", "direct32", "listed"),
-    ((62, 272, 771, 300), FP32, "none", "tiles32", "listed"),
-    ((231, 288, 322, 300), FP32, "none", "tiles64", "listed"),
-    ((45, 288, 1896, 300), FP32, "none", "tiles128", "listed"),
-    ((21, 272, 288, 0), FP32, "swiglu", "direct16", ""),
-    ((24, 1104, 3040, 0), FP32, "swiglu", "direct32", ""),
-    ((260, 400, 2336, 3), FP32, "swiglu", "direct64", ""),
-    ((67, 1072, 2976, 3), FP32, "swiglu", "tiles32", ""),
-    ((5066, 272, 320, 3), FP32, "swiglu", "tiles64", ""),
-    ((1872, 464, 1824, 3), FP32, "swiglu", "tiles128", "halved"),
-    ((8228, 336, 288, 3), FP32, "swiglu", "tiles128", "whole"),
-    ((5180, 912, 2592, 3), FP32, "swiglu", "tiles256", "halved"),
-    ((8042, 1008, 800, 3), FP32, "swiglu", "tiles256", "whole"),
-    ((76, 2208, 2880, 3), FP32, "swiglu", "tiles32", "split"),
-    ((127, 2080, 2048, 3), FP32, "swiglu", "tiles64", "split"),
-    ((96, 5568, 2272, 3), FP32, "swiglu", "tiles128", "split halved"),
-    ((58, 3104, 3456, 3), FP32, "swiglu", "tiles128", "split whole"),
-    ((21, 272, 352, 300), FP32, "swiglu", "direct16", "listed"),
-    ((225, 400, 288, 300), FP32, "swiglu", "direct32", "listed"),
-    ((49, 272, 1472, 300), FP32, "swiglu", "tiles32", "listed"),
-    ((176, 400, 384, 300), FP32, "swiglu", "tiles64", "listed"),
-    ((3252, 288, 416, 300), FP32, "swiglu", "tiles128", "listed"),
-    ((21, 272, 288, 3), I8, "swiglu", "direct16", ""),
-    ((20, 1104, 3296, 0), I8, "swiglu", "direct32", ""),
-    ((218, 400, 2624, 3), I8, "swiglu", "direct64", ""),
-    ((54, 1040, 3488, 3), I8, "swiglu", "tiles32", ""),
-    ((4960, 272, 320, 0), I8, "swiglu", "tiles64", ""),
-    ((1642, 320, 2080, 3), I8, "swiglu", "tiles128", "halved"),
-    ((8345, 272, 288, 3), I8, "swiglu", "tiles128", "whole"),
-    ((5162, 912, 2752, 3), I8, "swiglu", "tiles256", "halved"),
-    ((8472, 944, 832, 3), I8, "swiglu", "tiles256", "whole"),
-    ((54, 2256, 3424, 3), I8, "swiglu", "tiles32", "split"),
-    ((92, 2144, 2528, 3), I8, "swiglu", "tiles64", "split"),
-    ((94, 5088, 2400, 3), I8, "swiglu", "tiles128", "split halved"),
-    ((58, 3168, 3424, 3), I8, "swiglu", "tiles128", "split whole"),
-    ((20, 272, 288, 300), I8, "swiglu", "direct16", "listed"),
-    ((96, 912, 288, 300), I8, "swiglu", "direct32", "listed"),
-    ((36, 272, 1920, 300), I8, "swiglu", "tiles32", "listed"),
-    ((173, 272, 640, 300), I8, "swiglu", "tiles64", "listed"),
-    ((72, 608, 1120, 300), I8, "swiglu", "tiles128", "listed"),
-    ((5820, 1568, 2347, 3), FP32, "none", "tiles256", "halved"),
+    ((20, 48, 48, 0), BF16, "none", "direct16x16", ""),
+    ((8037, 48, 65, 3), BF16, "none", "direct32x16", ""),
+    ((545, 48, 1246, 3), BF16, "none", "direct32x32", ""),
+    ((8639, 48, 279, 3), BF16, "none", "direct64x32", ""),
+    ((8874, 320, 303, 3), BF16, "none", "direct64x64", ""),
+    ((229, 48, 3508, 3), BF16, "none", "tiles32", ""),
+    ((8754, 48, 141, 3), BF16, "none", "tiles64", ""),
+    ((6704, 400, 1085, 0), BF16, "none", "tiles128", "halved"),
+    ((4123, 416, 773, 3), BF16, "none", "tiles128", "whole"),
+    ((5168, 1472, 2914, 0), BF16, "none", "tiles256", "halved"),
+    ((3440, 1312, 2317, 3), BF16, "none", "tiles256", "whole"),
+    ((22, 48, 43, 300), BF16, "none", "direct16x16", "listed"),
+    ((6940, 160, 70, 300), BF16, "none", "direct32x16", "listed"),
+    ((49, 144, 2449, 300), BF16, "none", "direct32x32", "listed"),
+    ((37, 1440, 3456, 300), BF16, "none", "direct64x64", "listed"),
+    ((43, 48, 2245, 300), BF16, "none", "tiles32", "listed"),
+    ((66, 48, 3020, 300), BF16, "none", "tiles64", "listed"),
+    ((101, 1312, 969, 300), BF16, "none", "tiles128", "listed"),
+    ((20, 48, 48, 0), BF16, "none", "direct16x16", "waves 1"),
+    ((21, 144, 40, 3), BF16, "none", "direct16x16", "waves 2"),
+    ((21, 432, 40, 3), BF16, "none", "direct16x16", "waves 4"),
+    ((20, 1744, 41, 3), BF16, "none", "direct16x16", "waves 8"),
+    ((21, 7888, 42, 0), BF16, "none", "direct16x16", "waves 16"),
+    ((8037, 48, 65, 3), BF16, "none", "direct32x16", "waves 1"),
+    ((3075, 400, 69, 3), BF16, "none", "direct32x16", "waves 2"),
+    ((1959, 1008, 49, 0), BF16, "none", "direct32x16", "waves 4"),
+    ((21, 2608, 1147, 3), BF16, "none", "direct32x16", "waves 8"),
+    ((545, 48, 1246, 3), BF16, "none", "direct32x32", "waves 1"),
+    ((56, 400, 3859, 3), BF16, "none", "direct32x32", "waves 2"),
+    ((24, 1984, 2187, 3), BF16, "none", "direct32x32", "waves 4"),
+    ((22, 4816, 1851, 3), BF16, "none", "direct32x32", "waves 8"),
+    ((8639, 48, 279, 3), BF16, "none", "direct64x32", "waves 1"),
+    ((3580, 928, 233, 3), BF16, "none", "direct64x32", "waves 2"),
+    ((7547, 2032, 42, 3), BF16, "none", "direct64x32", "waves 4"),
+    ((8874, 320, 303, 3), BF16, "none", "direct64x64", "waves 1"),
+    ((369, 2256, 1941, 3), BF16, "none", "direct64x64", "waves 2"),
+    ((119, 2496, 3573, 3), BF16, "none", "direct64x64", "waves 4"),
+    ((20, 48, 64, 3), BF16, "swiglu", "direct16x16", ""),
+    ((301, 48, 1984, 3), BF16, "swiglu", "direct32x16", ""),
+    ((8392, 48, 288, 3), BF16, "swiglu", "direct64x16", ""),
+    ((8506, 288, 320, 3), BF16, "swiglu", "direct64x32", ""),
+    ((251, 48, 3616, 3), BF16, "swiglu", "tiles32", ""),
+    ((4517, 48, 288, 3), BF16, "swiglu", "tiles64", ""),
+    ((3946, 816, 800, 3), BF16, "swiglu", "tiles128", "halved"),
+    ((8972, 400, 352, 0), BF16, "swiglu", "tiles128", "whole"),
+    ((4722, 1376, 2880, 3), BF16, "swiglu", "tiles256", "halved"),
+    ((8428, 1296, 896, 3), BF16, "swiglu", "tiles256", "whole"),
+    ((20, 48, 64, 300), BF16, "swiglu", "direct16x16", "listed"),
+    ((131, 784, 96, 300), BF16, "swiglu", "direct32x16", "listed"),
+    ((4135, 3408, 64, 300), BF16, "swiglu", "direct64x32", "listed"),
+    ((131, 64, 736, 300), BF16, "swiglu", "tiles32", "listed"),
+    ((53, 48, 3680, 300), BF16, "swiglu", "tiles64", "listed"),
+    ((5989, 848, 192, 300), BF16, "swiglu", "tiles128", "listed"),
+    ((20, 48, 64, 3), BF16, "swiglu", "direct16x16", "waves 1"),
+    ((20, 144, 64, 0), BF16, "swiglu", "direct16x16", "waves 2"),
+    ((20, 800, 64, 3), BF16, "swiglu", "direct16x16", "waves 4"),
+    ((20, 2592, 64, 3), BF16, "swiglu", "direct16x16", "waves 8"),
+    ((301, 48, 1984, 3), BF16, "swiglu", "direct32x16", "waves 1"),
+    ((148, 400, 2304, 3), BF16, "swiglu", "direct32x16", "waves 2"),
+    ((21, 832, 2208, 3), BF16, "swiglu", "direct32x16", "waves 4"),
+    ((21, 4016, 2176, 3), BF16, "swiglu", "direct32x16", "waves 8"),
+    ((8392, 48, 288, 3), BF16, "swiglu", "direct64x16", "waves 1"),
+    ((291, 672, 3232, 0), BF16, "swiglu", "direct64x16", "waves 2"),
+    ((1004, 1424, 512, 0), BF16, "swiglu", "direct64x16", "waves 4"),
+    ((8506, 288, 320, 3), BF16, "swiglu", "direct64x32", "waves 1"),
+    ((2039, 1200, 800, 3), BF16, "swiglu", "direct64x32", "waves 2"),
+    ((86, 2960, 3936, 3), BF16, "swiglu", "direct64x32", "waves 4"),
+    ((20, 48, 41, 0), FP16, "none", "direct16x16", ""),
+    ((7367, 48, 66, 3), FP16, "none", "direct32x16", ""),
+    ((5831, 48, 116, 3), FP16, "none", "direct32x32", ""),
+    ((8356, 48, 271, 3), FP16, "none", "direct64x32", ""),
+    ((8612, 368, 289, 3), FP16, "none", "direct64x64", ""),
+    ((310, 48, 2761, 3), FP16, "none", "tiles32", ""),
+    ((8773, 48, 130, 0), FP16, "none", "tiles64", ""),
+    ((5432, 400, 1307, 3), FP16, "none", "tiles128", "halved"),
+    ((8915, 400, 337, 0), FP16, "none", "tiles128", "whole"),
+    ((5268, 1360, 2656, 3), FP16, "none", "tiles256", "halved"),
+    ((8690, 1360, 770, 3), FP16, "none", "tiles256", "whole"),
+    ((23, 48, 40, 300), FP16, "none", "direct16x16", "listed"),
+    ((6527, 160, 66, 300), FP16, "none", "direct32x16", "listed"),
+    ((43, 144, 2900, 300), FP16, "none", "direct32x32", "listed"),
+    ((36, 4064, 1402, 300), FP16, "none", "direct64x64", "listed"),
+    ((63, 48, 1532, 300), FP16, "none", "tiles32", "listed"),
+    ((265, 64, 578, 300), FP16, "none", "tiles64", "listed"),
+    ((34, 1168, 2970, 300), FP16, "none", "tiles128", "listed"),
+    ((20, 48, 64, 0), FP16, "swiglu", "direct16x16", ""),
+    ((220, 48, 2560, 3), FP16, "swiglu", "direct32x16", ""),
+    ((8722, 48, 288, 0), FP16, "swiglu", "direct64x16", ""),
+    ((8801, 352, 320, 0), FP16, "swiglu", "direct64x32", ""),
+    ((241, 48, 3936, 3), FP16, "swiglu", "tiles32", ""),
+    ((4567, 48, 288, 3), FP16, "swiglu", "tiles64", ""),
+    ((2646, 400, 2688, 3), FP16, "swiglu", "tiles128", "halved"),
+    ((5928, 448, 544, 0), FP16, "swiglu", "tiles128", "whole"),
+    ((8681, 1328, 1600, 3), FP16, "swiglu", "tiles256", "halved"),
+    ((5379, 1328, 1376, 3), FP16, "swiglu", "tiles256", "whole"),
+    ((20, 48, 64, 300), FP16, "swiglu", "direct16x16", "listed"),
+    ((126, 816, 96, 300), FP16, "swiglu", "direct32x16", "listed"),
+    ((4131, 1712, 128, 300), FP16, "swiglu", "direct64x32", "listed"),
+    ((49, 64, 1984, 300), FP16, "swiglu", "tiles32", "listed"),
+    ((199, 48, 864, 300), FP16, "swiglu", "tiles64", "listed"),
+    ((4789, 944, 224, 300), FP16, "swiglu", "tiles128", "listed"),
+    ((21, 48, 41, 3), FP32, "none", "direct16x16", ""),
+    ((8056, 48, 65, 3), FP32, "none", "direct32x16", ""),
+    ((7767, 48, 85, 0), FP32, "none", "direct32x32", ""),
+    ((8983, 48, 258, 0), FP32, "none", "direct64x32", ""),
+    ((8950, 336, 312, 3), FP32, "none", "direct64x64", ""),
+    ((353, 48, 2451, 3), FP32, "none", "tiles32", ""),
+    ((8390, 48, 130, 3), FP32, "none", "tiles64", ""),
+    ((7970, 448, 841, 0), FP32, "none", "tiles128", "halved"),
+    ((6143, 432, 519, 3), FP32, "none", "tiles128", "whole"),
+    ((5757, 1344, 2387, 3), FP32, "none", "tiles256", "halved"),
+    ((1900, 1296, 3912, 3), FP32, "none", "tiles256", "whole"),
+    ((20, 48, 44, 300), FP32, "none", "direct16x16", "listed"),
+    ((8883, 48, 104, 300), FP32, "none", "direct32x16", "listed"),
+    ((43, 144, 2841, 300), FP32, "none", "direct32x32", "listed"),
+    ((177, 1840, 569, 300), FP32, "none", "direct64x64", "listed"),
+    ((30, 48, 3251, 300), FP32, "none", "tiles32", "listed"),
+    ((201, 48, 787, 300), FP32, "none", "tiles64", "listed"),
+    ((4710, 816, 199, 300), FP32, "none", "tiles128", "listed"),
+    ((20, 48, 64, 3), FP32, "swiglu", "direct16x16", ""),
+    ((186, 48, 2912, 3), FP32, "swiglu", "direct32x16", ""),
+    ((8909, 48, 288, 0), FP32, "swiglu", "direct64x16", ""),
+    ((8156, 288, 320, 3), FP32, "swiglu", "direct64x32", ""),
+    ((267, 48, 3520, 3), FP32, "swiglu", "tiles32", ""),
+    ((4027, 48, 320, 3), FP32, "swiglu", "tiles64", ""),
+    ((8214, 416, 800, 3), FP32, "swiglu", "tiles128", "halved"),
+    ((5669, 416, 544, 3), FP32, "swiglu", "tiles128", "whole"),
+    ((5812, 1296, 2336, 3), FP32, "swiglu", "tiles256", "halved"),
+    ((6553, 1296, 1056, 0), FP32, "swiglu", "tiles256", "whole"),
+    ((21, 48, 64, 300), FP32, "swiglu", "direct16x16", "listed"),
+    ((129, 784, 96, 300), FP32, "swiglu", "direct32x16", "listed"),
+    ((4288, 2976, 64, 300), FP32, "swiglu", "direct64x32", "listed"),
+    ((188, 64, 512, 300), FP32, "swiglu", "tiles32", "listed"),
+    ((268, 48, 672, 300), FP32, "swiglu", "tiles64", "listed"),
+    ((5756, 784, 192, 300), FP32, "swiglu", "tiles128", "listed"),
+    ((20, 48, 64, 0), I8, "swiglu", "direct16x16", ""),
+    ((208, 48, 2688, 3), I8, "swiglu", "direct32x16", ""),
+    ((8187, 48, 288, 3), I8, "swiglu", "direct64x16", ""),
+    ((8148, 288, 320, 3), I8, "swiglu", "direct64x32", ""),
+    ((271, 48, 3456, 3), I8, "swiglu", "tiles32", ""),
+    ((4503, 48, 288, 3), I8, "swiglu", "tiles64", ""),
+    ((4301, 400, 1664, 3), I8, "swiglu", "tiles128", "halved"),
+    ((5665, 416, 544, 3), I8, "swiglu", "tiles128", "whole"),
+    ((6556, 1344, 2112, 3), I8, "swiglu", "tiles256", "halved"),
+    ((5538, 1328, 1312, 3), I8, "swiglu", "tiles256", "whole"),
+    ((20, 48, 64, 300), I8, "swiglu", "direct16x16", "listed"),
+    ((39, 784, 320, 300), I8, "swiglu", "direct32x16", "listed"),
+    ((4418, 1696, 128, 300), I8, "swiglu", "direct64x32", "listed"),
+    ((35, 48, 2752, 300), I8, "swiglu", "tiles32", "listed"),
+    ((88, 48, 2208, 300), I8, "swiglu", "tiles64", "listed"),
+    ((4537, 848, 256, 300), I8, "swiglu", "tiles128", "listed"),
+    ((20, 48, 64, 0), I8, "swiglu", "direct16x16", "waves 1"),
+    ((20, 144, 64, 0), I8, "swiglu", "direct16x16", "waves 2"),
+    ((21, 784, 64, 0), I8, "swiglu", "direct16x16", "waves 4"),
+    ((21, 2656, 64, 3), I8, "swiglu", "direct16x16", "waves 8"),
+    ((208, 48, 2688, 3), I8, "swiglu", "direct32x16", "waves 1"),
+    ((102, 400, 2816, 3), I8, "swiglu", "direct32x16", "waves 2"),
+    ((20, 816, 2208, 3), I8, "swiglu", "direct32x16", "waves 4"),
+    ((20, 3904, 2272, 3), I8, "swiglu", "direct32x16", "waves 8"),
+    ((8187, 48, 288, 3), I8, "swiglu", "direct64x16", "waves 1"),
+    ((2480, 720, 416, 0), I8, "swiglu", "direct64x16", "waves 2"),
+    ((97, 2224, 3904, 0), I8, "swiglu", "direct64x16", "waves 4"),
+    ((8148, 288, 320, 3), I8, "swiglu", "direct64x32", "waves 1"),
+    ((2671, 1200, 576, 3), I8, "swiglu", "direct64x32", "waves 2"),
+    ((126, 2416, 3648, 3), I8, "swiglu", "direct64x32", "waves 4"),
 ]
 
 
@@ -158,18 +197,19 @@ def _groups(rows, groups):
 
 def _last_round_halved(plan, groups, rows, n, epilogue):
     """Whether the last tiles of each of the 8 XCDs, 32 at a time, are at most half a round."""
-    bm, parts = plan["tile_rows"], plan["k_parts"]
-    mt = sum(-(-m // bm) for key, m in groups if key < 3) if groups else -(-rows // bm)
-    nt = -(-n // 256) * parts
+    mt = sum(-(-m // plan["tile_rows"]) for key, m in groups if key < 3) if groups else -(-rows // plan["tile_rows"])
+    nt = -(-(n // 2 if epilogue == "swiglu" else n) // plan["tile_columns"])
     return 2 * (-(-mt * nt // 8) % 32) <= 32
 
 
 def check_form(plan, size, epilogue, kernel, how):
     rows, _, n, groups = size
-    assert ("tiles" if plan["lds_tiles"] else "direct") + str(plan["tile_rows"]) == kernel
-    assert (plan["k_parts"] > 1) == ("split" in how) and bool(plan["listed"]) == ("listed" in how)
-    if plan["tile_rows"] >= 128 and plan["lds_tiles"] and "listed" not in how:
-        assert _last_round_halved(plan, _groups(rows, groups), rows, n, epilogue) == ("halved" in how)
+    assert (f"tiles{plan['tile_rows']}" if plan["lds_tiles"] else f"direct{plan['tile_rows']}x{plan['tile_columns']}") == kernel
+    assert bool(plan["listed"]) == (how == "listed") and (plan["waves"] == 0) == bool(plan["lds_tiles"])
+    if how.startswith("waves"):
+        assert how == f"waves {plan['waves']}"
+    if plan["tile_rows"] >= 128 and plan["lds_tiles"] and how != "listed":
+        assert _last_round_halved(plan, _groups(rows, groups), rows, n, epilogue) == (how == "halved")
 
 
 @pytest.mark.parametrize("size,dtype,epilogue,kernel,how", FORMS,

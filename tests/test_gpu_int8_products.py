@@ -123,7 +123,7 @@ def test_large(rows, k, n, dtype, epilogue, experts):
     check(matmul_inputs(rows + k, rows, k, n, max(experts, 1)), groups, epilogue, dtype, pad=7 if dtype != I8 else 0)
 
 
-# few tiles and a long K, which is split: parts that do not divide it, odd widths, rows behind
+# few tiles and a long K, which the waves of a workgroup split: blocks that they do not divide, odd widths, rows behind
 SPLIT = [(300, 6160, 1333, FP16, "none", 0), (256, 7184, 2048, BF16, "none", 0), (520, 4112, 1504, FP32, "swiglu", 0),
          (260, 8192, 2080, BF16, "swiglu", 0), (330, 8000, 1600, I8, "swiglu", 0), (1000, 8192, 1056, I8, "swiglu", 3),
          (400, 12304, 1201, FP32, "none", 2), (200, 12304, 600, FP32, "none", 2)]
@@ -133,7 +133,7 @@ SPLIT = [(300, 6160, 1333, FP16, "none", 0), (256, 7184, 2048, BF16, "none", 0),
 def test_split_over_k(rows, k, n, dtype, epilogue, experts):
     groups = None if experts == 0 else [(e, (rows - 9) // experts) for e in range(experts)] + [(experts, 4)]
     plan = check(matmul_inputs(rows + k + n, rows, k, n, max(experts, 1)), groups, epilogue, dtype, pad=5)
-    assert plan["k_parts"] > 1, "this size is not split"
+    assert plan["waves"] > 1, "this size is not split"
 
 
 def test_strided_scales_and_packed_rows():

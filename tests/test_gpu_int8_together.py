@@ -131,7 +131,7 @@ def _calls(seed):
     gamma = dev(rng.normal(size=700).astype(np.float32), BF16)
     actual = torch.tensor([90], device="cuda")
     args = [dev(m[k]) for k in ("x", "xs", "w", "ws")]
-    lm = matmul_inputs(seed + 1, 256, 7168, 2048)     # split over K
+    lm = matmul_inputs(seed + 1, 256, 7168, 2048)     # K split over waves
     long = [dev(lm[k]) for k in ("x", "xs", "w", "ws")]
     many = matmul_inputs(seed + 2, 900, 64, 64, 6)    # listed by a launch of its own
     groups = dev(np.stack([np.arange(300) % 6, np.full(300, 3)], 1).astype(np.int64))
@@ -164,7 +164,7 @@ def _same(a, b):
 
 def test_the_calls_cover_the_workspaces():
     plans = [F.moe_grouped_matmul_int8_plan(c.desc) for c in _calls(7)[3:]]
-    assert plans[2]["k_parts"] > 1 and plans[3]["listed"] and all(c.ws_bytes > 0 for c in _calls(7)[5:])
+    assert plans[2]["waves"] > 1 and plans[3]["listed"] and all(_calls(7)[i].ws_bytes > 0 for i in (3, 6))
 
 
 def test_calls_on_streams_at_once():

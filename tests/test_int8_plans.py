@@ -25,22 +25,19 @@ def test_the_gpu_tests_reach_their_forms(size, dtype, epilogue, kernel, how):
 
 
 def test_every_kernel_is_among_the_forms():
-    kinds = {(d, e, k) for _, d, e, k, h in FORMS if "split" not in h}
-    for kernel in ("direct16", "direct32", "direct64", "tiles32", "tiles64", "tiles128", "tiles256"):
-        for dtype in (BF16, FP16, FP32):
-            assert (dtype, "none", kernel) in kinds and (dtype, "swiglu", kernel) in kinds, (dtype, kernel)
-        assert (I8, "swiglu", kernel) in kinds
-    split = {(d, e, k) for _, d, e, k, h in FORMS if "split" in h}
-    for kernel in ("tiles32", "tiles64", "tiles128"):
-        for dtype in (BF16, FP16, FP32):
-            assert (dtype, "none", kernel) in split and (dtype, "swiglu", kernel) in split, (dtype, kernel)
-        assert (I8, "swiglu", kernel) in split
+    kinds = {(d, e, k) for _, d, e, k, h in FORMS}
+    tiles = ("tiles32", "tiles64", "tiles128", "tiles256")
+    plain = ("direct16x16", "direct32x16", "direct32x32", "direct64x32", "direct64x64") + tiles
+    swiglu = ("direct16x16", "direct32x16", "direct64x16", "direct64x32") + tiles
+    assert kinds >= {(d, "none", k) for d in (BF16, FP16, FP32) for k in plain}
+    assert kinds >= {(d, "swiglu", k) for d in (BF16, FP16, FP32, I8) for k in swiglu}
+    assert {f"waves {w}" for w in (1, 2, 4, 8, 16)} <= {h for _, d, e, k, h in FORMS}
 
 
 def test_sizes_named_beside_the_rule():
-    assert _plan((256, 7168, 2048, 0))["k_parts"] > 1
     assert not _plan((1, 7168, 4096, 0))["lds_tiles"]
-    assert _plan((8191, 5120, 7168, 0)) == dict(lds_tiles=1, tile_rows=256, k_parts=1, listed=0)
+    assert not _plan((64, 7168, 4096, 0))["lds_tiles"]
+    assert _plan((8191, 5120, 7168, 0)) == dict(lds_tiles=1, tile_rows=256, tile_columns=256, waves=0, listed=0)
 
 
 def test_workspaces():

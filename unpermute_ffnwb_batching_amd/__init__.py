@@ -1119,7 +1119,7 @@ def moe_grouped_matmul_int8_workspace_size(desc):
 
 
 def moe_grouped_matmul_int8_plan(desc):
-    """Which kernels a call runs: dict(lds_tiles, tile_rows, k_parts, listed)."""
+    """Which kernels a call runs: dict(lds_tiles, tile_rows, tile_columns, waves, listed)."""
     return _plan("moe_grouped_matmul_int8_plan", desc, GroupedMatmulInt8PlanInfo())
 
 

@@ -180,4 +180,4 @@ class GroupedMatmulInt8Desc(ctypes.Structure):
 
 
 class GroupedMatmulInt8PlanInfo(ctypes.Structure):
-    _fields_ = [("lds_tiles", _i32), ("tile_rows", _i32), ("k_parts", _i32), ("listed", _i32)]
+    _fields_ = [("lds_tiles", _i32), ("tile_rows", _i32), ("tile_columns", _i32), ("waves", _i32), ("listed", _i32)]

@@ -275,8 +275,8 @@ int moe_grouped_matmul_int8_plan(const moe_grouped_matmul_int8_desc* d, moe_grou
   Int8MatmulPlan p;
   const int st = plan_grouped_matmul_int8(d, &p);
   if (st != FFNWB_OK) return st;
-  *info = moe_grouped_matmul_int8_plan_info{p.tile ? 1 : 0, static_cast<int32_t>(p.bm), static_cast<int32_t>(p.parts),
-                                            p.table ? 1 : 0};
+  *info = moe_grouped_matmul_int8_plan_info{p.tile ? 1 : 0, static_cast<int32_t>(p.bm), static_cast<int32_t>(p.cols),
+                                            static_cast<int32_t>(p.waves), p.table ? 1 : 0};
   return FFNWB_OK;
 }
 

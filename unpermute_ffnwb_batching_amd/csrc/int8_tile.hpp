@@ -7,6 +7,11 @@
 // at position c ^ (r % 8), which spreads the 16 rows that a matrix operand reads at once over all
 // banks.  The lanes of a copy write adjacent LDS addresses, so the permutation is applied to the
 // addresses they read.
+//
+// Many rows are bound by the power that the matrix cores draw: 8191 rows by 7168 columns over 5120 take 255 us (2.36 POP/s;
+// zeros in place of random codes 204), 4096 by 4096 over 8192 105 us (2.62), and by about 12 us a round of tiles to fill the
+// buffers and store, which do not overlap the next one.  Few rows of many experts are bound by memory: 4377 rows of
+// 256 experts, 2048 columns over 7168, 636 us (5.8 TB/s).
 #pragma once
 
 #include <type_traits>
@@ -27,8 +32,6 @@ struct Mm8Args {
   int32_t rows;
   int32_t kb;                  // 128-column blocks of K
   int32_t ntiles;              // column tiles
-  int32_t parts, part_blocks;  // parts of K, each a workgroup's, and blocks of a part
-  int64_t part_bytes;          // between the results of two parts
   int32_t ngroups, nexperts;
   bool vec;                    // four adjacent outputs are one aligned store
   const char* x;
@@ -115,10 +118,9 @@ __device__ __forceinline__ uint32_t fragment_max(const f32x4& v) {
   return max(b[0], b[1]);
 }
 
-// What a product writes: whole-number sums, results of a type, or held rows.
-struct Whole { static constexpr bool kWhole = true, kHeld = false, kExact = true; using Out = TF32; };
-template <class T> struct Scaled { static constexpr bool kWhole = false, kHeld = false, kExact = T::kBytes == 4; using Out = T; };
-struct Held { static constexpr bool kWhole = false, kHeld = true, kExact = true; using Out = TF32; };
+// What a product writes: results of a type, or held rows.
+template <class T> struct Scaled { static constexpr bool kHeld = false, kExact = T::kBytes == 4; using Out = T; };
+struct Held { static constexpr bool kHeld = true, kExact = true; using Out = TF32; };
 
 // Rows on their way to INT8 are held in FP32, with the largest |v| of each 16 columns beside them, so that
 // the kernel that makes them INT8 knows a row's scale without reading the row first.  Held in 16 bits
@@ -147,10 +149,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
   using S = Tile8Shape<WM, WN, MF>;
   constexpr bool kSwiglu = EPI == FFNWB_EPI_SWIGLU;
   constexpr int NF = S::kNF, kWaves = WM * WN;
-  // this workgroup's part of K: kb blocks, `columns` columns
-  const int32_t part = c % a.parts, k0 = part * a.part_blocks * kBlk;
-  const int32_t columns = min(static_cast<int32_t>(a.K) - k0, a.part_blocks * kBlk), kb = (columns + kBlk - 1) / kBlk;
-  c /= a.parts;
+  const int32_t kb = a.kb;
   const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), r = lane % 16, g = lane / 16;
   const int32_t wm = wave / WN, wn = wave % WN;
   const int64_t c0 = static_cast<int64_t>(c) * (kSwiglu ? 128 : 256);  // first output column
@@ -167,8 +166,8 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
   // Copy j of a wave takes 8 rows, one chunk per lane: 32-bit offsets from the tile's first rows
   // (256 rows of x, and of w as far as the up columns, are below 2^32 bytes in this kernel).
   const int64_t w0 = weight_row(0);
-  const Buffer xbuf = make_buffer(a.x + rt.row0 * a.xs + k0, (rt.rows - 1) * a.xs + a.K - k0);
-  const Buffer wbuf = make_buffer(a.w + (static_cast<int64_t>(rt.expert) * a.N + w0) * a.K + k0, (a.N - w0) * a.K - k0);
+  const Buffer xbuf = make_buffer(a.x + rt.row0 * a.xs, (rt.rows - 1) * a.xs + a.K);
+  const Buffer wbuf = make_buffer(a.w + (static_cast<int64_t>(rt.expert) * a.N + w0) * a.K, (a.N - w0) * a.K);
   const uint32_t chunk = ((lane % 8) ^ (lane / 8)) * 16;
   uint32_t xsrc[S::kXCopies], wsrc[S::kWCopies];
 #pragma unroll
@@ -199,7 +198,7 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
   };
   // In the last block the columns past K (of the next row, or not there) count as zeros: clearing
   // them in x is enough.
-  const int32_t left = columns - (kb - 1) * kBlk - g * 16;
+  const int32_t left = static_cast<int32_t>(a.K) - (kb - 1) * kBlk - g * 16;
   auto clear_past = [&](int s, u32x4& v) {
     if (left <= s * 64) v = u32x4{0, 0, 0, 0};
   };
@@ -210,13 +209,11 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
   f32x4 ws[NF];
   const int64_t n0 = c0 + wn * (kSwiglu ? NF * 8 : NF * 16) + g * 4;  // the lane's first column of fragment 0
   auto scales = [&] {
-    if constexpr (!T::kWhole) {
 #pragma unroll
-      for (int i = 0; i < MF; ++i) xs[i] = a.x_scale[(rt.row0 + min((wm * MF + i) * 16 + r, rt.rows - 1)) * a.xss];
+    for (int i = 0; i < MF; ++i) xs[i] = a.x_scale[(rt.row0 + min((wm * MF + i) * 16 + r, rt.rows - 1)) * a.xss];
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
-        ws[f] = channel_scales(a, rt.expert, kSwiglu && f >= NF / 2 ? a.F + n0 + (f - NF / 2) * 16 : n0 + f * 16);
-    }
+    for (int f = 0; f < NF; ++f)
+      ws[f] = channel_scales(a, rt.expert, kSwiglu && f >= NF / 2 ? a.F + n0 + (f - NF / 2) * 16 : n0 + f * 16);
   };
   if constexpr (!S::kAhead) scales();
   fetch_x(0);
@@ -314,55 +311,49 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
   for (int i = 0; i < MF; ++i) {
     __builtin_amdgcn_sched_barrier(0);  // one row fragment after another: few registers
     const int32_t row = (wm * MF + i) * 16 + r;
-    char* y = a.y + part * a.part_bytes + (rt.row0 + min(row, rt.rows - 1)) * a.ys;
+    char* y = a.y + (rt.row0 + min(row, rt.rows - 1)) * a.ys;
     const bool in = row < rt.rows;
-    if constexpr (T::kWhole) {
+    using Out = typename T::Out;
+    f32x4 v[OF];
 #pragma unroll
-      for (int f = 0; f < OF; ++f)  // the ends of a row may run into the rest of its pitch
-        if (in && n0 + f * 16 < limit) *reinterpret_cast<i32x4*>(y + (n0 + f * 16) * 4) = tot[i][f];
-    } else {
-      using Out = typename T::Out;
-      f32x4 v[OF];
+    for (int f = 0; f < OF; ++f) {
+      v[f] = scaled(tot[i][f], xs[i], ws[f]);
+      if constexpr (kSwiglu) {
+        const f32x4 up = scaled(tot[i][OF + f], xs[i], ws[OF + f]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[f][j] = swiglu_fast<T::kExact>(v[f][j], up[j]);
+      }
+    }
+    if constexpr (Out::kBytes == 4) {
 #pragma unroll
       for (int f = 0; f < OF; ++f) {
-        v[f] = scaled(tot[i][f], xs[i], ws[f]);
-        if constexpr (kSwiglu) {
-          const f32x4 up = scaled(tot[i][OF + f], xs[i], ws[OF + f]);
+        const int64_t n = n0 + f * 16;
+        char* to = y + n * 4;
+        if constexpr (T::kHeld) store_largest(a, v[f], rt.row0 + row, n, in && n < limit);
+        if (in && n + 4 <= limit) {
+          *reinterpret_cast<u32x4_a4*>(to) = __builtin_bit_cast(u32x4, v[f]);
+        } else if (in) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[f][j] = swiglu_fast<T::kExact>(v[f][j], up[j]);
+          for (int j = 0; j < 3; ++j)
+            if (n + j < limit) reinterpret_cast<float*>(to)[j] = v[f][j];
         }
       }
-      if constexpr (Out::kBytes == 4) {
+    } else {
 #pragma unroll
-        for (int f = 0; f < OF; ++f) {
-          const int64_t n = n0 + f * 16;
-          char* to = y + n * 4;
-          if constexpr (T::kHeld) store_largest(a, v[f], rt.row0 + row, n, in && n < limit);
-          if (in && n + 4 <= limit) {
-            *reinterpret_cast<u32x4_a4*>(to) = __builtin_bit_cast(u32x4, v[f]);
-          } else if (in) {
+      for (int f = 0; f < OF; f += 2) {
+        uint32_t p[2] = {narrow2<Out>(v[f][0], v[f][1]), narrow2<Out>(v[f][2], v[f][3])};
+        uint32_t q[2] = {narrow2<Out>(v[f + 1][0], v[f + 1][1]), narrow2<Out>(v[f + 1][2], v[f + 1][3])};
+        join_columns(p[0], q[0]);
+        join_columns(p[1], q[1]);
+        const int64_t n = n0 + f * 16 + g * 4;  // n0 holds 4 g, the lane's columns start at 8 g
+        char* to = y + n * 2;
+        if (in && n + 8 <= limit) {
+          *reinterpret_cast<u32x4_a1*>(to) = u32x4{p[0], p[1], q[0], q[1]};
+        } else if (in) {
+          const uint32_t w[4] = {p[0], p[1], q[0], q[1]};
 #pragma unroll
-            for (int j = 0; j < 3; ++j)
-              if (n + j < limit) reinterpret_cast<float*>(to)[j] = v[f][j];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int f = 0; f < OF; f += 2) {
-          uint32_t p[2] = {narrow2<Out>(v[f][0], v[f][1]), narrow2<Out>(v[f][2], v[f][3])};
-          uint32_t q[2] = {narrow2<Out>(v[f + 1][0], v[f + 1][1]), narrow2<Out>(v[f + 1][2], v[f + 1][3])};
-          join_columns(p[0], q[0]);
-          join_columns(p[1], q[1]);
-          const int64_t n = n0 + f * 16 + g * 4;  // n0 holds 4 g, the lane's columns start at 8 g
-          char* to = y + n * 2;
-          if (in && n + 8 <= limit) {
-            *reinterpret_cast<u32x4_a1*>(to) = u32x4{p[0], p[1], q[0], q[1]};
-          } else if (in) {
-            const uint32_t w[4] = {p[0], p[1], q[0], q[1]};
-#pragma unroll
-            for (int j = 0; j < 7; ++j)
-              if (n + j < limit) reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
-          }
+          for (int j = 0; j < 7; ++j)
+            if (n + j < limit) reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j % 2)));
         }
       }
     }

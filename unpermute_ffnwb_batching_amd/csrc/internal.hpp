@@ -172,14 +172,11 @@ struct Int8MatmulPlan {
   bool swiglu = false;
   bool quant = false;                          // INT8 rows out, by a second launch
   bool fp32 = false;                           // FP32 rows out
-  bool tile = false;                           // through LDS, else straight to registers
-  int64_t bm = 0;                              // rows of a tile
+  bool tile = false;                           // tiles of 256 columns, else of 16 to 64 (direct)
+  int64_t bm = 0, cols = 0;                    // rows and result columns of a tile
+  int64_t waves = 0;                           // of a direct workgroup
   int64_t kb = 0;                              // 128-column blocks of K
-  int64_t parts = 1, part_blocks = 0;          // parts of K, and blocks of each
-  int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles (times the parts)
-  bool join = false;                           // sums or FP32 rows, finished by a launch of its own
-  int64_t pitch = 0;                           // elements of a row of them
-  int64_t join_groups = 0;                     // workgroups that finish a row tile
+  int64_t mtiles = 0, ntiles = 0;              // most row tiles, column tiles
   bool table = false;                          // row tiles listed by a launch of their own
   size_t ws_bytes = 0;
 };

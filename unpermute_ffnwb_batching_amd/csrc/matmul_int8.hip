@@ -1,71 +1,99 @@
 // The experts' products on INT8 rows, with a scale for each row of x and each row of w.
 //
-// As for e4m3 rows there are two kernels: few rows go straight from memory to registers
-// (mm8_direct_kernel), more rows in tiles through LDS (mm8_tile_kernel).  The scales belong to whole
-// rows, so the matrix cores carry the 32-bit totals over all of K, and the scaling is done once, at
-// the end.  What a workgroup cannot finish by itself, mm8_join_kernel (parts of K) or mm8_rows_kernel
-// (INT8 results, whose scale spans the row) does.
+// As for e4m3 rows there are two kernels: few rows take small tiles whose waves split K
+// (mm8_direct_kernel), more rows large ones whose waves share both operands (mm8_tile_kernel).  The scales
+// belong to whole rows, so the matrix cores carry the 32-bit totals over all of K, and the scaling is
+// done once, at the end.  INT8 results, whose scale spans the row, are finished by mm8_rows_kernel.
 #include "int8_tile.hpp"
 
 namespace ffnwb {
 
 // ------------------------------------------------------------------ direct kernel
 //
-// For few rows, where the weights are read once and latency counts.  A workgroup takes MT * 16
-// rows by 16 columns (SwiGLU: 16 gate and the 16 up columns that go with them); its waves take
-// the 128-column blocks of K in turn, straight from memory to registers, a wave's next block
-// ahead of its present one, and their totals are added in wave order.
+// For few rows, or few of each expert, where latency and the reading of the weights count.  A workgroup
+// takes 16 MT rows by 16 NF columns (SwiGLU: half of them gate columns, half the up columns that go with
+// them); its waves take the 128-column blocks of K in turn, each through two LDS buffers of its own, without
+// barriers, and their totals are added at the end.
+//
+// Why through LDS although no wave shares its blocks: a matrix operand has 16 rows in adjacent lanes,
+// and loads in that order move 38 GB/s per CU, a lane each cycle; copies of whole lines to LDS move 125 to
+// 150.  More buffers gained nothing.  Over 7168: 1 row by 4096 columns 6.7 us (7.6 with loads to registers), which is
+// 4.4 TB/s with the launch, 16 rows 7.1 us (9.3), 64 rows 8.5 us (18.7); 256 rows by 2048 11.3 us (33.8): there the copies, from L2,
+// and the reads of the fragments keep LDS busy.
 
-template <class T, int EPI, int MT>
-__global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Args a) {
-  constexpr int NF = EPI == FFNWB_EPI_SWIGLU ? 2 : 1;
-  extern __shared__ __align__(16) i32x4 red8[];  // [waves][NF * MT][lanes]
+// Bytes of LDS of a wave, and the most waves of a workgroup.
+constexpr int direct_lds(int mt, int nf) { return 2 * (mt + nf) * 2048; }
+constexpr int direct_waves(int mt, int nf) { return mt + nf <= 2 ? 16 : mt + nf <= 4 ? 8 : 4; }
+
+// This wave's copies have landed, all or (`some`, uniform) all but the last kLeft.
+template <int kLeft>
+__device__ __forceinline__ void own_copies_done(bool some) {
+  asm volatile("s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lown%=\n\ts_waitcnt vmcnt(0)\n.Lown%=:\n\ts_waitcnt vmcnt(%1)"
+               ::"s"(uniform(static_cast<int32_t>(some))), "n"(kLeft) : "memory", "scc");
+}
+template <class T, int EPI, int MT, int NF>
+__global__ __launch_bounds__(direct_waves(MT, NF) * kWave) void mm8_direct_kernel(Mm8Args a) {
+  constexpr bool kSwiglu = EPI == FFNWB_EPI_SWIGLU;
+  constexpr int CF = kSwiglu ? NF / 2 : NF;  // fragments of results; SwiGLU: gate, then up
+  constexpr int kFrags = NF + MT, kRegion = direct_lds(MT, NF);
+  extern __shared__ __align__(16) char lds8[];
   RowTile rt;
   int32_t c;
   if (!find_tile(a, MT * 16, rt, c)) return;
   const int32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), waves = blockDim.x / kWave;
   const int32_t r = lane % 16, g = lane / 16;
-  const int64_t n0 = int64_t{c} * 16;
-  const char* wp[NF];
+  const int64_t n0 = int64_t{c} * 16 * CF;
+  auto column = [&](int f) -> int64_t { return n0 + f % CF * 16 + f / CF * a.F; };
+  const char* src[kFrags][2];
 #pragma unroll
-  for (int f = 0; f < NF; ++f)
-    wp[f] = a.w + (static_cast<int64_t>(rt.expert) * a.N + min(n0 + f * a.F + r, a.N - 1)) * a.K;
-  const char* xp[MT];
+  for (int j = 0; j < 2; ++j) {
+    const int32_t q = j * 8 + lane / 8;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) xp[i] = a.x + static_cast<int64_t>(rt.row0 + min(i * 16 + r, rt.rows - 1)) * a.xs;
-  // The scales: ahead of the blocks, where there are registers (MT = 4 would lose a wave of three).
+    for (int f = 0; f < NF; ++f) src[f][j] = a.w + (static_cast<int64_t>(rt.expert) * a.N + min(column(f) + q, a.N - 1)) * a.K;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) src[NF + i][j] = a.x + static_cast<int64_t>(rt.row0 + min(i * 16 + q, rt.rows - 1)) * a.xs;
+  }
   f32x4 ws[NF];
   float xs[MT];
-  auto scales = [&] {
 #pragma unroll
-    for (int f = 0; f < NF; ++f) ws[f] = channel_scales(a, rt.expert, n0 + f * a.F + g * 4);
+  for (int f = 0; f < NF; ++f) ws[f] = channel_scales(a, rt.expert, column(f) + g * 4);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) xs[i] = load_f32(a.x_scale + (rt.row0 + min(i * 16 + r, rt.rows - 1)) * a.xss);
+  for (int i = 0; i < MT; ++i) xs[i] = load_f32(a.x_scale + (rt.row0 + min(i * 16 + r, rt.rows - 1)) * a.xss);
+  // A block of a fragment: two copies of 8 rows, chunks permuted as in the tile kernel.  Chunks past the
+  // end of K take the row's last one, which counts as zeros: clearing it in x is enough.
+  char* const own = lds8 + wave * kRegion;
+  const int32_t last = static_cast<int32_t>(a.K) - 16, chunk = ((lane % 8) ^ (lane / 8)) * 16;
+  auto fetch = [&](int32_t b, int32_t stage) {
+    const int32_t k = min(b * kBlk + chunk, last);
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src[f][j] + k),
+                                         reinterpret_cast<__attribute__((address_space(3))) void*>(reinterpret_cast<uintptr_t>(own + (stage * kFrags + f) * 2048 + j * 1024)), 16, 0, 0);
   };
-  if constexpr (MT < 4) scales();
-  struct Block {
-    u32x4 w[NF][2], x[MT][2];
-  } blk[2];
-  // A block's columns; past the end of K the row's last ones (no branch in the way of the loads),
-  // which `multiply` clears in x.
-  const int32_t last = static_cast<int32_t>(a.K) - 16;
-  auto load = [&](Block& v, int32_t b) {
-    if (b >= a.kb) return;
-    const int32_t k0 = min(b * kBlk + g * 16, last), k1 = min(b * kBlk + 64 + g * 16, last);
-#pragma unroll
-    for (int f = 0; f < NF; ++f) v.w[f][0] = load16(wp[f] + k0), v.w[f][1] = load16(wp[f] + k1);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) v.x[i][0] = load16(xp[i] + k0), v.x[i][1] = load16(xp[i] + k1);
-  };
+  const int32_t at = r * kBlk + (g ^ (r & 7)) * 16;
   i32x4 tot[NF][MT] = {};
-  auto multiply = [&](Block& v, int32_t b) {
-    if (b >= a.kb) return;
+#pragma unroll
+  for (int st = 0; st < 2; ++st)
+    if (wave + st * waves < a.kb) fetch(wave + st * waves, st);
+  int32_t stage = 0;
+  for (int32_t b = wave; b < a.kb; b += waves) {
+    own_copies_done<kFrags * 2>(b + waves < a.kb);
+    const char* p = own + stage * kFrags * 2048;
+    u32x4 v[kFrags][2];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) v[f][h] = *reinterpret_cast<const u32x4*>(p + f * 2048 + (at ^ (h * 64)));
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the fragments are in registers: their buffer is free
+    if (b + 2 * waves < a.kb) fetch(b + 2 * waves, stage);
     if ((b + 1) * kBlk > a.K) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (b * kBlk + h * 64 + g * 16 > last) {
 #pragma unroll
-          for (int i = 0; i < MT; ++i) v.x[i][h] = u32x4{0, 0, 0, 0};
+          for (int i = 0; i < MT; ++i) v[NF + i][h] = u32x4{0, 0, 0, 0};
         }
     }
 #pragma unroll
@@ -73,94 +101,37 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void mm8_direct_kernel(Mm8Arg
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) tot[f][i] = mul_int8(v.w[f][h], v.x[i][h], tot[f][i]);
-  };
-  load(blk[0], wave);
-  for (int32_t b = wave; b < a.kb; b += 2 * waves) {
-    load(blk[1], b + waves);
-    multiply(blk[0], b);
-    load(blk[0], b + 2 * waves);
-    multiply(blk[1], b + waves);
+        for (int f = 0; f < NF; ++f) tot[f][i] = mul_int8(v[f][h], v[NF + i][h], tot[f][i]);
+    stage ^= 1;
   }
+  // Each wave's totals take the place of its own blocks, whose copies have all landed.
+  auto red = [&](int32_t w, int k) -> i32x4& { return reinterpret_cast<i32x4*>(lds8 + w * kRegion)[k * kWave + lane]; };
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) red8[(wave * NF * MT + f * MT + i) * kWave + lane] = tot[f][i];
-  if constexpr (MT >= 4) scales();
+    for (int i = 0; i < MT; ++i) red(wave, f * MT + i) = tot[f][i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    if (i % waves != wave) continue;
-    i32x4 s[NF] = {};
+  for (int o = 0; o < MT * CF; ++o) {
+    if (o % waves != wave) continue;
+    constexpr int kParts = kSwiglu ? 2 : 1;
+    const int i = o % MT, f = o / MT;
+    i32x4 s[kParts] = {};
     for (int32_t w = 0; w < waves; ++w)
 #pragma unroll
-      for (int f = 0; f < NF; ++f) s[f] += red8[(w * NF * MT + f * MT + i) * kWave + lane];
+      for (int u = 0; u < kParts; ++u) s[u] += red(w, (f + u * CF) * MT + i);
     if (i * 16 + r >= rt.rows) continue;  // the four lanes of a row together
-    const int64_t row = rt.row0 + i * 16 + r;
-    f32x4 p[NF];
+    const int64_t row = rt.row0 + i * 16 + r, n = n0 + f * 16 + g * 4;
+    f32x4 p[kParts];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) p[f] = scaled(s[f], xs[i], ws[f]);
-    if constexpr (EPI == FFNWB_EPI_SWIGLU) {
+    for (int u = 0; u < kParts; ++u) p[u] = scaled(s[u], xs[i], ws[f + u * CF]);
+    if constexpr (kSwiglu) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) p[0][j] = swiglu_fast<T::kExact>(p[0][j], p[1][j]);
     }
-    if constexpr (T::kHeld) store_largest(a, p[0], row, n0 + g * 4, true);
-    store4<typename T::Out>(a.y + row * a.ys, n0 + g * 4, a.F, p[0], a.vec);
+    if constexpr (T::kHeld) store_largest(a, p[0], row, n, n < a.F);
+    store4<typename T::Out>(a.y + row * a.ys, n, a.F, p[0], a.vec);
   }
-}
-
-// ------------------------------------------------------------------ joining a product
-//
-// Products split over K: whole-number sums [parts][R][N rounded up to 8], whose order does not
-// matter.  16 lanes take 128 outputs of a row; a workgroup takes 16 such blocks of a row tile, so
-// that rows of no expert stay as they were.
-
-constexpr int kJoin8Threads = 256;
-
-template <class T, bool kSwiglu>
-__global__ __launch_bounds__(kJoin8Threads) void mm8_join_kernel(Mm8Args a, const int32_t* sums, int64_t pitch, int32_t parts, int32_t bm) {
-  const int32_t fb = static_cast<int32_t>((a.F + kBlk - 1) / kBlk);
-  RowTile rt;
-  int32_t group;
-  if (!find_tile(a, bm, rt, group)) return;
-  const int32_t u = group * (kJoin8Threads / 16) + threadIdx.x / 16;
-  const int32_t i = u / fb, b = u - i * fb;
-  const int64_t row = rt.row0 + i, f0 = static_cast<int64_t>(b) * kBlk + threadIdx.x % 16 * 8;
-  if (i >= rt.rows || f0 >= a.F) return;
-  const float xs = a.x_scale[row * a.xss];
-  auto sum = [&](int64_t n, f32x4 (&f)[2]) {  // columns n .. n + 7
-    const int32_t* p = sums + row * pitch + n;
-    i32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int32_t s = 0; s < parts; ++s, p += a.rows * pitch) {
-      v0 += reinterpret_cast<const i32x4*>(p)[0];
-      v1 += reinterpret_cast<const i32x4*>(p)[1];
-    }
-    f[0] = scaled(v0, xs, channel_scales(a, rt.expert, n));
-    f[1] = scaled(v1, xs, channel_scales(a, rt.expert, n + 4));
-  };
-  f32x4 f[2];
-  sum(f0, f);
-  if constexpr (kSwiglu) {
-    f32x4 up[2];
-    sum(a.F + f0, up);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[h][j] = swiglu_fast<T::kExact>(f[h][j], up[h][j]);
-  }
-  char* y = a.y + row * a.ys;
-  if constexpr (T::kHeld) {
-    uint32_t m = 0;  // of the 16 columns of two lanes
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m = max(m, __float_as_uint(f[h][j]) & 0x7fffffffu);
-    m = max(m, lane_dpp<0xb1>(m));
-    if (f0 % 16 == 0) a.held_max[row * (a.F / 16) + f0 / 16] = __uint_as_float(m);
-  }
-  store4<typename T::Out>(y, f0, a.F, f[0], a.vec);
-  store4<typename T::Out>(y, f0 + 4, a.F, f[1], a.vec);
 }
 
 // ------------------------------------------------------------------ INT8 results
@@ -199,7 +170,7 @@ __global__ __launch_bounds__(kRows8Threads) void mm8_rows_kernel(Mm8Args a, cons
   }
 }
 
-// 16 lanes to a row of up to 512 elements (58010 rows of 208, the whole call: 37 us, 62 with a wave to a row).
+// 16 lanes to a row of up to 512 elements (58010 rows of 208, the whole call: 38 us, 62 with a wave to a row).
 static int64_t rows8_lanes(int64_t F) { return F <= 512 ? 16 : 64; }
 
 // ------------------------------------------------------------------ host side
@@ -209,42 +180,41 @@ constexpr int64_t kListedTiles8 = 16 * kCus8;  // more tiles of grouped rows are
 
 static int64_t out_size8(int32_t dt) { return dt == FFNWB_DT_FP32 ? 4 : dt == FFNWB_DT_INT8 ? 1 : 2; }
 
-// Waves of a direct workgroup: a block of K for each, four at most where there are enough
-// workgroups to fill the chip.
-static int direct_waves8(int64_t tiles, int64_t kb, int64_t bm) {
-  int waves = 1;
-  while (waves < (bm == 16 ? 16 : 8) && waves * 2 <= kb && (waves < 4 || tiles * waves < kCus8 * 16)) waves *= 2;
-  return waves;
-}
+// The direct kernel's tiles: MT row and NF column fragments (of w: SwiGLU has half of them as results).
+struct Direct8 { int mt, nf; };
+constexpr Direct8 kDirect8[] = {{1, 1}, {2, 1}, {2, 2}, {4, 2}, {4, 4}};
+constexpr Direct8 kDirect8Swiglu[] = {{1, 2}, {2, 2}, {4, 2}, {4, 4}};
 
-// Microseconds that a product takes with the given kernel and tile rows, as far as the choice
+// Microseconds that a product takes with the given kernel and tile, as far as the choice
 // between them needs it: rounds of workgroups that fit the chip together times what one needs for
-// its blocks of K, or the time of the weights and results in memory if that is longer.  The figures
-// are fitted so that the least of them picks the fastest shape, and are not those of the parts.
+// its blocks of K, and the time of the weights and results in memory; the longer one, and a part of
+// the first, as they overlap in part.  The figures are fitted so that the least of them picks the fastest shape,
+// and are not those of the parts.
 static double expected_us8(const Int8MatmulPlan& p, int64_t groups) {
   const int64_t some = groups < p.R ? groups : p.R, elt = p.quant || p.fp32 ? 4 : 2;
-  const double mt = groups > 0 ? static_cast<double>(p.R) / p.bm + 0.7 * some : static_cast<double>((p.R + p.bm - 1) / p.bm);
-  const double results = static_cast<double>(p.R * p.F * elt) / 2.42e6, wgs = mt * p.ntiles;
+  const double mt = groups > 0 ? static_cast<double>(p.R) / p.bm + 0.619 * some : static_cast<double>((p.R + p.bm - 1) / p.bm);
+  const double weights = (groups > 0 ? 0.621 * some : 1.0) * p.N * p.K;
+  const double results = static_cast<double>(p.R * p.F * elt) / 4.0e6, wgs = mt * p.ntiles;
   auto rounds = [](double n, double together) { return n <= together ? 1.0 : __builtin_ceil(n / together); };
-  double us = 2.6;
-  if (groups > kWaveGroups || (groups > 0 && p.mtiles * p.ntiles > kListedTiles8)) us += 2.05;
-  if (p.quant) us += 3.84 + static_cast<double>(p.R * p.F) / 1.24e6;
+  auto larger = [](double a, double b) { return a > b ? a : b; };
+  auto lesser = [](double a, double b) { return a < b ? a : b; };
+  double us = 2.46;
+  if (p.table) us += 2.29;
+  if (p.quant) us += 3.73 + static_cast<double>(p.R * p.F) / 6.74e5;
   if (p.tile) {
     const bool two = p.bm < 128 && wgs > kCus8;  // two workgroups share a CU
-    const double block = p.bm == 256 ? 1.25 : p.bm == 128 ? 0.826 : p.bm == 64 ? (two ? 1.19 : 0.733) : (two ? 1.25 : 0.599);
-    const double once = p.bm == 256 ? 6.9 : p.bm == 128 ? 2.0 : two ? 2.3 : 1.6;
-    const double work = rounds(wgs, p.bm < 128 ? 2 * kCus8 : kCus8) * (p.part_blocks * block + once);
-    const double memory = (groups > 0 ? 1.09 * some : 1.0) * p.N * p.K / 6.79e6 + results;
-    if (p.parts > 1) us += 3.79 + static_cast<double>(p.parts * p.R * p.N) / 5.35e5;  // a launch, sums written and read
-    return us + (work > memory ? work : memory);
+    const double block = p.bm == 256 ? 0.782 : p.bm == 128 ? 0.942 : p.bm == 64 ? (two ? 1.17 : 0.733) : (two ? 1.08 : 0.6);
+    const double once = p.bm == 256 ? 17.0 : p.bm == 128 ? 2.91 : two ? 2.04 : 1.37;
+    const double work = rounds(wgs, p.bm < 128 ? 2 * kCus8 : kCus8) * (p.kb * block + once);
+    return us + larger(work, weights / 5.8e6 + results) + 0.43 * work;
   }
-  const int waves = direct_waves8(p.mtiles * p.ntiles, p.kb, p.bm);
-  const double fit = p.bm == 16 ? (p.swiglu ? 20 : 28) : p.bm == 32 ? (p.swiglu ? 12 : 20) : (p.swiglu ? 8 : 12);  // waves of a CU
-  const double busy = wgs * waves / kCus8 < fit ? wgs * waves / kCus8 : fit;
-  const double block = (p.bm == 64 ? 0.918 : p.bm == 32 ? 0.648 : 0.598) * (0.977 + 0.0956 * busy) * (p.swiglu ? 1.21 : 1.0);
-  const double work = rounds(wgs, (fit > waves ? fit / waves : 1.0) * kCus8) * ((p.kb + waves - 1) / waves * block + 0.22 * (1 + 1.15 * (p.bm / 16 - 1)));
-  const double memory = mt * p.N * p.K / 6.77e6 + results;  // the weights again for every row tile, from L2
-  return us + (work > memory ? work : memory);
+  const double m = p.bm / 16, n = p.cols / 16 * (p.swiglu ? 2 : 1);  // fragments
+  const double fit = larger(1.0, __builtin_floor(lesser(160.0 * 1024 / (4096 * (m + n) * p.waves), 20.0 / p.waves)));  // workgroups of a CU
+  const double busy = lesser(__builtin_ceil(wgs / kCus8), fit) * p.waves;                                              // waves of one
+  const double block = 0.0481 * (m + n) + 0.00982 * busy * (m + n) + 0.00496 * busy * m * n;
+  const double copies = wgs * p.kb * (m + n) / 6890 + 0.65;  // 2 KB each, mostly from L2
+  const double work = larger(rounds(wgs, fit * kCus8) * ((p.kb + p.waves - 1) / p.waves * block + 0.798 + 0.0406 * busy * m * n), copies);
+  return us + larger(work, weights / 8.07e6 + results) + 0.43 * work;
 }
 
 int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPlan* p) {
@@ -284,67 +254,56 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
       (quant && reinterpret_cast<uintptr_t>(d->y_scale) % 4 != 0))
     return FFNWB_ERR_PARAM_INVALID;
   const int64_t groups = d->group_list != nullptr ? d->num_groups : 1;
-  auto shape = [&](int64_t bm, int64_t parts) {  // negative bm: direct; the result: workgroups, of the larger launch
-    p->tile = bm > 0, p->bm = bm > 0 ? bm : -bm;
-    p->part_blocks = (p->kb + parts - 1) / parts;
-    p->parts = (p->kb + p->part_blocks - 1) / p->part_blocks;
-    p->mtiles = (p->R + p->bm - 1) / p->bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
-    p->ntiles = !p->tile ? (p->F + 15) / 16 : p->parts > 1 ? (p->N + 255) / 256 * p->parts : (p->F + (swiglu ? 127 : 255)) / (swiglu ? 128 : 256);
-    p->join = p->parts > 1;
-    p->join_groups = p->join ? (p->bm * ((p->F + 127) / 128) + kJoin8Threads / 16 - 1) / (kJoin8Threads / 16) : 0;
-    int64_t most = p->join_groups > p->ntiles ? p->join_groups : p->ntiles;
-    const int64_t quant_groups = (p->bm * rows8_lanes(p->F) + kRows8Threads - 1) / kRows8Threads;
-    if (quant && quant_groups > most) most = quant_groups;
-    return p->mtiles * most;
+  auto shape = [&](bool tile, int64_t bm, int64_t cols, int64_t waves) {  // the result: workgroups, of the larger launch
+    p->tile = tile, p->bm = bm, p->cols = cols, p->waves = waves;
+    p->mtiles = (p->R + bm - 1) / bm + (d->group_list != nullptr ? (groups < p->R ? groups : p->R) : 0);
+    p->ntiles = (p->F + cols - 1) / cols;
+    p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > kListedTiles8));
+    const int64_t quant_groups = (bm * rows8_lanes(p->F) + kRows8Threads - 1) / kRows8Threads;
+    return p->mtiles * (quant && quant_groups > p->ntiles ? quant_groups : p->ntiles);
   };
-  // The kernel, the rows of its tiles and the parts of K: the least of the times expected.  On 1500
-  // random sizes that the fit has not seen (1 to 65536 rows, K and N to 8192, 0 to 256 groups) the choice is
-  // 2.0% slower than the best of the shapes on average, more than 10% in 103 of them and 1.85 times at
-  // worst; on 700 with up to 4096 rows and K and N from 512 on, 2.6%, more than 10% in 62.  Parts are what fills the chip with a long K and few tiles: 256 rows by 2048 columns over 7168
-  // take 32 us in the best shape without and 18 us in 4 parts.
+  // The kernel, its tiles and the waves of a direct workgroup: the least of the times expected.  On 9000
+  // random sizes that the fit has not seen (up to 65536 rows, K and N to 8192, 0 to 256 groups; every other one
+  // with K and N from 512 on) the choice is 2.1% slower than the best of all shapes on average, more than 10% in
+  // 482 of them and 1.57 times at worst.  Either kernel alone would cost: 64 rows by 4096 columns over 7168 32 us in
+  // tiles and 8.6 direct, 8191 rows by 7168 over 5120 256 us in tiles and more than twice that direct.
   // 256 rows of x, and the gate rows of w, have to be inside the 32-bit offsets of the tile kernel.
   const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
   const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup
   double best = 0;
-  int64_t best_bm = 0, best_parts = 1;
-  auto consider = [&](int64_t bm, int64_t parts) {
-    if (shape(bm, parts) > most) return;
+  Int8MatmulPlan chosen;
+  auto consider = [&](bool tile, int64_t bm, int64_t cols, int64_t waves) {
+    if (shape(tile, bm, cols, waves) > most) return;
     const double t = expected_us8(*p, d->num_groups);
-    if (best_bm == 0 || t < best) best = t, best_bm = bm, best_parts = p->parts;
+    if (best == 0 || t < best) best = t, chosen = *p;
   };
-  for (const int64_t bm : {-16, -32, -64, 32, 64, 128, 256}) {
-    if (bm > 0 && !near) continue;
-    consider(bm, 1);
-    if (bm < 0 || bm == 256) continue;
-    // parts that fill the chip once, or half of it
-    const int64_t last = d->num_groups < p->R ? d->num_groups : p->R, tiles = ((p->R + bm - 1) / bm + last * 6 / 10) * ((p->N + 255) / 256);
-    const int64_t fill = (bm == 32 ? 2 : 1) * kCus8 / (tiles > 0 ? tiles : 1);
-    for (const int64_t parts : {fill, fill / 2})
-      if (parts > 1) consider(bm, parts < p->kb / 2 ? parts : p->kb / 2 > 1 ? p->kb / 2 : 1);
-  }
-  if (best_bm == 0) return FFNWB_ERR_PARAM_INVALID;
-  shape(best_bm, best_parts);
-  p->pitch = (p->N + 7) / 8 * 8;
+  auto direct = [&](const Direct8& s) {
+    for (int64_t waves = 1; waves <= direct_waves(s.mt, s.nf) && (waves == 1 || waves <= p->kb); waves *= 2)
+      consider(false, s.mt * 16, (swiglu ? s.nf / 2 : s.nf) * 16, waves);
+  };
+  if (swiglu) for (const Direct8& s : kDirect8Swiglu) direct(s);
+  else for (const Direct8& s : kDirect8) direct(s);
+  if (near)
+    for (const int64_t bm : {32, 64, 128, 256}) consider(true, bm, swiglu ? 128 : 256, 0);
+  if (best == 0) return FFNWB_ERR_PARAM_INVALID;
+  *p = chosen;
   p->ws_bytes = 0;
   Carve c;
-  p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > kListedTiles8));
   if (p->table) {
     c.take<int32_t>(1);
     c.take<int4>(static_cast<size_t>(p->mtiles));
   }
-  if (p->join) c.take<int32_t>(static_cast<size_t>(p->parts * p->R * p->pitch));
   if (p->quant) c.take<float>(static_cast<size_t>(p->R * p->F)), c.take<float>(static_cast<size_t>(p->R * p->F / 16));
   p->ws_bytes = c.off;
   return FFNWB_OK;
 }
 
-template <class T, int EPI, int MT>
-static bool launch_direct8_rows(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
-  const int waves = direct_waves8(p.mtiles * p.ntiles, p.kb, p.bm);
-  const size_t lds = static_cast<size_t>(waves) * (EPI == FFNWB_EPI_SWIGLU ? 2 : 1) * MT * kWave * 16;
-  auto kernel = mm8_direct_kernel<T, EPI, MT>;
+template <class T, int EPI, int MT, int NF>
+static bool launch_direct8(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
+  const size_t lds = static_cast<size_t>(p.waves) * direct_lds(MT, NF);
+  auto kernel = mm8_direct_kernel<T, EPI, MT, NF>;
   allow_large_lds(reinterpret_cast<const void*>(kernel), lds);
-  return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles)), dim3(static_cast<uint32_t>(waves * kWave)), lds, s, b, e, a);
+  return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.ntiles)), dim3(static_cast<uint32_t>(p.waves * kWave)), lds, s, b, e, a);
 }
 
 template <class T, int EPI, int WM, int WN, int MF>
@@ -359,11 +318,18 @@ static bool launch_tile8_shape(const Mm8Args& a, const Int8MatmulPlan& p, hipStr
 
 template <class T, int EPI>
 static bool launch_product8(const Mm8Args& a, const Int8MatmulPlan& p, hipStream_t s, void* b, void* e) {
-  if constexpr (!T::kWhole) {
+  if constexpr (EPI == FFNWB_EPI_SWIGLU) {
     if (!p.tile)
-      return p.bm == 16   ? launch_direct8_rows<T, EPI, 1>(a, p, s, b, e)
-             : p.bm == 32 ? launch_direct8_rows<T, EPI, 2>(a, p, s, b, e)
-                          : launch_direct8_rows<T, EPI, 4>(a, p, s, b, e);
+      return p.bm == 16     ? launch_direct8<T, EPI, 1, 2>(a, p, s, b, e)
+             : p.bm == 32   ? launch_direct8<T, EPI, 2, 2>(a, p, s, b, e)
+             : p.cols == 16 ? launch_direct8<T, EPI, 4, 2>(a, p, s, b, e)
+                            : launch_direct8<T, EPI, 4, 4>(a, p, s, b, e);
+  } else {
+    if (!p.tile)
+      return p.bm == 16     ? launch_direct8<T, EPI, 1, 1>(a, p, s, b, e)
+             : p.bm == 32   ? (p.cols == 16 ? launch_direct8<T, EPI, 2, 1>(a, p, s, b, e) : launch_direct8<T, EPI, 2, 2>(a, p, s, b, e))
+             : p.cols == 32 ? launch_direct8<T, EPI, 4, 2>(a, p, s, b, e)
+                            : launch_direct8<T, EPI, 4, 4>(a, p, s, b, e);
   }
   return p.bm == 256   ? launch_tile8_shape<T, EPI, 2, 4, 8>(a, p, s, b, e)
          : p.bm == 128 ? launch_tile8_shape<T, EPI, 2, 4, 4>(a, p, s, b, e)
@@ -392,47 +358,24 @@ int launch_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, const Int8
     if (hipGetLastError() != hipSuccess) return FFNWB_ERR_RUNTIME;
     a.table = table, a.count = count;
   }
-  int32_t* sums = p.join ? c.take<int32_t>(static_cast<size_t>(p.parts * p.R * p.pitch)) : nullptr;
   float* held = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F)) : nullptr;
   a.held_max = p.quant ? c.take<float>(static_cast<size_t>(p.R * p.F / 16)) : nullptr;
   void *b = d->ev_matmul_begin, *e = d->ev_matmul_end;
   // results in their own type, or rows held on their way to INT8
-  Mm8Args out = a;
+  Mm8Args m = a;
+  m.ntiles = static_cast<int32_t>(p.ntiles);
   const int32_t dt = d->out_dtype;
   const uint64_t elt = p.quant ? 4 : static_cast<uint64_t>(out_size8(dt));
-  if (p.quant) out.y = reinterpret_cast<char*>(held), out.ys = p.F * 4;
-  out.vec = ((reinterpret_cast<uintptr_t>(out.y) | static_cast<uint64_t>(out.ys)) & (4 * elt - 1)) == 0;
-  void* out_end = p.quant ? nullptr : e;
-  // the product: results, or whole-number sums for the join
-  Mm8Args m = out;
-  m.ntiles = static_cast<int32_t>(p.ntiles);
-  m.parts = static_cast<int32_t>(p.parts), m.part_blocks = static_cast<int32_t>(p.part_blocks), m.part_bytes = p.R * p.pitch * 4;
-  bool ok;
-  if (p.join) {
-    m.y = reinterpret_cast<char*>(sums), m.ys = p.pitch * 4, m.F = p.N;
-    ok = launch_product8<Whole, FFNWB_EPI_NONE>(m, p, s, b, nullptr);
-    if (ok) {
-      out.ntiles = static_cast<int32_t>(p.join_groups);
-      const int32_t parts = m.parts;
-      const int64_t pitch = p.pitch;
-      auto join = [&](auto kernel) {
-        return launch_bound(kernel, dim3(tile_grid(p.mtiles * p.join_groups)), dim3(kJoin8Threads), 0, s, nullptr, out_end, out, sums, pitch, parts, bm);
-      };
-      ok = dt == FFNWB_DT_INT8   ? join(mm8_join_kernel<Held, true>)
-           : dt == FFNWB_DT_FP16 ? (p.swiglu ? join(mm8_join_kernel<Scaled<TF16>, true>) : join(mm8_join_kernel<Scaled<TF16>, false>))
-           : dt == FFNWB_DT_BF16 ? (p.swiglu ? join(mm8_join_kernel<Scaled<TBF16>, true>) : join(mm8_join_kernel<Scaled<TBF16>, false>))
-                                 : (p.swiglu ? join(mm8_join_kernel<Scaled<TF32>, true>) : join(mm8_join_kernel<Scaled<TF32>, false>));
-    }
-  } else if (p.swiglu) {
-    ok = dt == FFNWB_DT_INT8   ? launch_product8<Held, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end)
-         : dt == FFNWB_DT_FP16 ? launch_product8<Scaled<TF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end)
-         : dt == FFNWB_DT_BF16 ? launch_product8<Scaled<TBF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end)
-                               : launch_product8<Scaled<TF32>, FFNWB_EPI_SWIGLU>(m, p, s, b, out_end);
-  } else {
-    ok = dt == FFNWB_DT_FP16   ? launch_product8<Scaled<TF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end)
-         : dt == FFNWB_DT_BF16 ? launch_product8<Scaled<TBF16>, FFNWB_EPI_NONE>(m, p, s, b, out_end)
-                               : launch_product8<Scaled<TF32>, FFNWB_EPI_NONE>(m, p, s, b, out_end);
-  }
+  if (p.quant) m.y = reinterpret_cast<char*>(held), m.ys = p.F * 4;
+  m.vec = ((reinterpret_cast<uintptr_t>(m.y) | static_cast<uint64_t>(m.ys)) & (4 * elt - 1)) == 0;
+  void* end = p.quant ? nullptr : e;
+  bool ok = p.swiglu ? (dt == FFNWB_DT_INT8   ? launch_product8<Held, FFNWB_EPI_SWIGLU>(m, p, s, b, end)
+                        : dt == FFNWB_DT_FP16 ? launch_product8<Scaled<TF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, end)
+                        : dt == FFNWB_DT_BF16 ? launch_product8<Scaled<TBF16>, FFNWB_EPI_SWIGLU>(m, p, s, b, end)
+                                              : launch_product8<Scaled<TF32>, FFNWB_EPI_SWIGLU>(m, p, s, b, end))
+                     : (dt == FFNWB_DT_FP16   ? launch_product8<Scaled<TF16>, FFNWB_EPI_NONE>(m, p, s, b, end)
+                        : dt == FFNWB_DT_BF16 ? launch_product8<Scaled<TBF16>, FFNWB_EPI_NONE>(m, p, s, b, end)
+                                              : launch_product8<Scaled<TF32>, FFNWB_EPI_NONE>(m, p, s, b, end));
   if (ok && p.quant) {
     const int64_t lanes = rows8_lanes(p.F);
     a.ntiles = static_cast<int32_t>((p.bm * lanes + kRows8Threads - 1) / kRows8Threads);

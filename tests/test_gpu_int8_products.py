@@ -91,6 +91,16 @@ def test_many_groups(epilogue, out_dtype):
     check(matmul_inputs(9, 1600, 128, 64, 8), groups, epilogue, out_dtype, what="2000 groups")
 
 
+@pytest.mark.parametrize("epilogue,out_dtype", [("none", FP32), ("swiglu", I8)])
+def test_the_most_groups_and_experts(epilogue, out_dtype):
+    rng = np.random.default_rng(8192)
+    m = rng.integers(0, 3, 8192)
+    m[rng.integers(0, 8192, 4)] = 300
+    keys = rng.permutation(8192)
+    keys[::7] = 9000  # no expert
+    check(matmul_inputs(3, int(m.sum()) + 5, 32, 64, 8192), list(zip(keys.tolist(), m.tolist())), epilogue, out_dtype)
+
+
 @pytest.mark.parametrize("rows,n,epilogue,dtype", [(1, 64, "none", FP32), (40, 64, "swiglu", FP32), (300, 512, "none", FP32), (300, 512, "swiglu", I8)])
 def test_the_longest_k_of_the_largest_codes(rows, n, epilogue, dtype):
     # -128 * -128 * 131056 is 2^31 - 262144: sums that reach the end of 32 bits on either side

@@ -353,7 +353,7 @@ int plan_grouped_matmul(const moe_grouped_matmul_fp8_desc* d, MatmulPlan* p) {
   p->ws_bytes = 0;
   Carve c;
   // The list in every workgroup costs each about 1 us, two to a CU at a time; the launch 3 to 5 us with
-  // 128 or 256 groups.  A thread writes the tiles of a group one after another, though: 13119 rows of two groups by 78 columns over 80 take 22 us, in 820 row tiles of 16, where 64-row
+  // 128 or 256 groups: 13119 rows of two groups by 78 columns over 80 take 9.1 us, in 820 row tiles of 16, where 64-row
   // tiles without the launch would take 6.4.
   p->table = p->R > 0 && (d->num_groups > kWaveGroups || (d->num_groups > 0 && p->mtiles * p->ntiles > 16 * kCus));
   if (p->table) {

@@ -8,8 +8,8 @@
 // banks.  The lanes of a copy write adjacent LDS addresses, so the permutation is applied to the
 // addresses they read.
 //
-// Many rows are bound by the power that the matrix cores draw: 8191 rows by 7168 columns over 5120 take 255 us (2.36 POP/s;
-// zeros in place of random codes 204), 4096 by 4096 over 8192 105 us (2.62), and by about 12 us a round of tiles to fill the
+// Many rows are bound by the power that the matrix cores draw: 8191 rows by 7168 columns over 5120 take 249 us (2.41 POP/s;
+// zeros in place of random codes 204), 4096 by 4096 over 8192 103 us (2.66), and by some us a round of tiles to fill the
 // buffers and store, which do not overlap the next one.  Few rows of many experts are bound by memory: 4377 rows of
 // 256 experts, 2048 columns over 7168, 636 us (5.8 TB/s).
 #pragma once
@@ -203,8 +203,9 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
     if (left <= s * 64) v = u32x4{0, 0, 0, 0};
   };
 
-  // The scales of the wave's rows and columns: loaded among the last products where registers are
-  // short, ahead of the first copies else.
+  // The scales of the wave's rows and columns: ahead of the first copies, among the last products where
+  // registers are short, or behind them in tiles of 256 rows, which have none left (24 scales ahead of the last block took
+  // 35 registers' way through memory: 131072 rows of 128 experts to INT8 1338 -> 1235 us, 40000 rows by 4096 columns over 512 184 -> 138).
   float xs[MF];
   f32x4 ws[NF];
   const int64_t n0 = c0 + wn * (kSwiglu ? NF * 8 : NF * 16) + g * 4;  // the lane's first column of fragment 0
@@ -267,8 +268,9 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
       }
     };
     for (int32_t b = 0; b + 1 < kb; ++b) block(b, std::false_type{});
-    scales();
+    if constexpr (MF < 8) scales();
     block(kb - 1, std::true_type{});
+    if constexpr (MF >= 8) scales();
   } else {
     // w of the next block is on its way since the step before, x since the start of this one, and the
     // fragments of w go to registers first, which frees their buffer for the block after next.

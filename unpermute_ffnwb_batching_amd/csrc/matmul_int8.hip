@@ -203,8 +203,8 @@ static double expected_us8(const Int8MatmulPlan& p, int64_t groups) {
   if (p.quant) us += 3.73 + static_cast<double>(p.R * p.F) / 6.74e5;
   if (p.tile) {
     const bool two = p.bm < 128 && wgs > kCus8;  // two workgroups share a CU
-    const double block = p.bm == 256 ? 0.782 : p.bm == 128 ? 0.942 : p.bm == 64 ? (two ? 1.17 : 0.733) : (two ? 1.08 : 0.6);
-    const double once = p.bm == 256 ? 17.0 : p.bm == 128 ? 2.91 : two ? 2.04 : 1.37;
+    const double block = p.bm == 256 ? 1.0 : p.bm == 128 ? 0.942 : p.bm == 64 ? (two ? 1.17 : 0.733) : (two ? 1.08 : 0.6);
+    const double once = p.bm == 256 ? 4.0 : p.bm == 128 ? 2.91 : two ? 2.04 : 1.37;
     const double work = rounds(wgs, p.bm < 128 ? 2 * kCus8 : kCus8) * (p.kb * block + once);
     return us + larger(work, weights / 5.8e6 + results) + 0.43 * work;
   }
@@ -262,11 +262,11 @@ int plan_grouped_matmul_int8(const moe_grouped_matmul_int8_desc* d, Int8MatmulPl
     const int64_t quant_groups = (bm * rows8_lanes(p->F) + kRows8Threads - 1) / kRows8Threads;
     return p->mtiles * (quant && quant_groups > p->ntiles ? quant_groups : p->ntiles);
   };
-  // The kernel, its tiles and the waves of a direct workgroup: the least of the times expected.  On 9000
+  // The kernel, its tiles and the waves of a direct workgroup: the least of the times expected.  On 1500
   // random sizes that the fit has not seen (up to 65536 rows, K and N to 8192, 0 to 256 groups; every other one
-  // with K and N from 512 on) the choice is 2.1% slower than the best of all shapes on average, more than 10% in
-  // 482 of them and 1.57 times at worst.  Either kernel alone would cost: 64 rows by 4096 columns over 7168 32 us in
-  // tiles and 8.6 direct, 8191 rows by 7168 over 5120 256 us in tiles and more than twice that direct.
+  // with K and N from 512 on) the choice is 2.2% slower than the best of all shapes on average, more than 10% in
+  // 85 of them and 1.42 times at worst.  Either kernel alone would cost: 64 rows by 4096 columns over 7168 32 us in
+  // tiles and 8.5 direct, 8191 rows by 7168 over 5120 249 us in tiles and more than twice that direct.
   // 256 rows of x, and the gate rows of w, have to be inside the 32-bit offsets of the tile kernel.
   const bool near = p->xs <= (1 << 22) && (!swiglu || (p->F + 128) * p->K < (int64_t{1} << 32));
   const int64_t most = (int64_t{1} << 22) - 8;  // workgroups of a launch: fewer than 2^32 threads of at most 1024 a workgroup

@@ -781,6 +781,7 @@ int moe_rmsnorm_quant(const moe_rmsnorm_quant_desc* d, void* workspace, size_t w
  * FFNWB_EPI_NONE:   y[i, n] = p[i, n], n < N.
  * FFNWB_EPI_SWIGLU: N = 2 F (gate rows of w, then up rows),
  *   y[i, f] = g * sigmoid(g) * u, g = p[i, f], u = p[i, F + f], f < F.
+ *   sigmoid(g) = 1 / (1 + exp(-g)) in FP32: 0 for g < -88.73, where exp(-g) passes its range.
  * y is rounded once to out_dtype; with out_dtype FFNWB_DT_INT8 (SwiGLU only) y and y_scale are
  * the FP32 rows quantised as moe_quant_int8 does.
  *

@@ -88,23 +88,28 @@ __device__ __forceinline__ void join_columns(uint32_t& a, uint32_t& b) {
   a = q[0], b = q[1];
 }
 
-// silu(g) * u as swiglu (fp8_block.hpp), with the hardware's exponential and reciprocal (2^-23 each): 6
-// operations, or 11, instead of about 45 (131072 rows by 1024 outputs over 4096: 1189 -> 1130 us).  The
+// silu(g) * u as swiglu (fp8_block.hpp), with the hardware's exponential and reciprocal (2^-23 each): 7
+// operations, or 12, instead of about 45 (131072 rows by 1024 outputs over 4096: 1189 -> 1130 us with 6).  The
 // exponent of 2 is -g log2(e); its rounding is an error of |g| 2^-24 of the result, up to 6e-6, which is far
 // below the rounding to 16 bits but not below that to FP32: there (kExact), and for rows on their way to
-// INT8, the exponent is in two parts.  exp overflows to infinity for very negative g, which gives the limit -0; g = -inf is NaN.
+// INT8, the exponent is in two parts.  The hardware's reciprocal is 0 where it would be subnormal, for sums past
+// 2^126 (g < -87.3): so it is taken of a 16th of the sum, and a 16th of it is rounded once there, 2^-22 of the
+// result at most (the one operation more is within the noise at those rows).  exp overflows to infinity for g < -88.7, which gives the limit -0; g = -inf is NaN.
 template <bool kExact>
 __device__ __forceinline__ float swiglu_fast(float g, float u) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eRest = 1.925963033500011e-8f, kLn2 = 0.693147180559945f;
+  constexpr float kPart = 0.0625f;
   const float x = -g * kLog2e;
   const float e = __builtin_amdgcn_exp2f(x);
-  float sum = 1.0f + e;
+  float part;  // (1 + exp(-g)) / 16
   if constexpr (kExact) {
     const float rest = __builtin_fmaf(-g, kLog2eRest, __builtin_fmaf(-g, kLog2e, -x));
     // at most 2^-16 where e matters; the bound is for g = inf, whose rest is NaN
-    sum = __builtin_fmaf(e, __builtin_fmaf(fminf(fmaxf(rest, -0.001f), 0.001f), kLn2, 1.0f), 1.0f);
+    part = __builtin_fmaf(e, __builtin_fmaf(fminf(fmaxf(rest, -0.001f), 0.001f), kLn2 * kPart, kPart), kPart);
+  } else {
+    part = __builtin_fmaf(e, kPart, kPart);
   }
-  return g * __builtin_amdgcn_rcpf(sum) * u;
+  return g * (__builtin_amdgcn_rcpf(part) * kPart) * u;
 }
 
 // The largest |v| of the 16 columns that the four lanes r, r + 16, .. hold, as FP32 bits (NaN largest).

@@ -161,9 +161,9 @@ __global__ __launch_bounds__(kRows8Threads) void mm8_rows_kernel(Mm8Args a, cons
 #pragma unroll 2
   for (int32_t h0 = t * 8; h0 < F; h0 += kLanes * 8) {
     Raw<TF32> raw;
-    load_raw<TF32, false>(from, h0, F, raw);  // F is a multiple of 16
+    load_raw<TF32, false, false>(from, h0, F, raw);  // F is a multiple of 16
     float f[8];
-    widen_raw(raw, f);
+    widen_raw<TF32, false, false>(raw, h0, F, f);
     uint32_t lo, hi;
     quant_int8(f, s, lo, hi);
     *reinterpret_cast<u32x2_a1*>(q + h0) = u32x2{lo, hi};

@@ -10,8 +10,12 @@
 // rows of 4096 with their residual 81 us (470 MB).  One row of 7168: 3.6 us, without a norm 2.4, most of
 // it the launch.  What was worth it: all loads of a thread ahead of the first use, and registers few
 // enough for 7 waves (gamma's type and rows of whole runs known to the compiler: 67 -> 46 us); reductions
-// through the data path instead of LDS.  Rows that are not whole runs of 8 elements: 4608 of 7167 in 64 us,
-// without a norm 25.
+// through the data path instead of LDS.
+//
+// Rows that are not whole runs of 8 elements start at any address: 4608 of 7167 BF16 take 62 us to INT8 and 63 to
+// e4m3, of 7164 (addresses of 8 bytes) 51, without a norm 18.  The row's end is read where the run before it
+// ends, without a branch: with one, the loads of a thread's runs waited for each other (64, 72 and 57 us; 16384 rows of
+// 4095 129 instead of 108).
 #include <type_traits>
 
 #include "internal.hpp"
@@ -49,6 +53,7 @@ __global__ __launch_bounds__(kLanes > 0 ? 256 : 1024) void row_quant_kernel(RowA
   }
   const int32_t t = kLanes > 0 ? threadIdx.x % kLanes : threadIdx.x, tr = kLanes > 0 ? kLanes : blockDim.x;
   constexpr int kRows = kLanes > 0 ? 256 / kLanes : 1;  // of a workgroup
+  constexpr bool kShort = kTail && kLanes == 16;        // rows below 8 elements take this shape only
   int32_t turn = 0;
   for (int64_t row = int64_t{blockIdx.x} * kRows + (kLanes == 64 ? uniform(threadIdx.x / kLanes) : kLanes > 0 ? threadIdx.x / kLanes : 0); row < rows;
        row += int64_t{gridDim.x} * kRows, turn ^= 1) {
@@ -62,27 +67,27 @@ __global__ __launch_bounds__(kLanes > 0 ? 256 : 1024) void row_quant_kernel(RowA
     };
     auto load = [&](int32_t h0, Run& v) {
       if constexpr (kNorm) {
-        load_raw<Gamma, kTail>(a.gamma, h0, a.hidden, v.gamma);
-        if (a.residual != nullptr) load_raw<T, kTail>(a.residual + row * a.rs, h0, a.hidden, v.res);
+        load_raw<Gamma, kTail, kShort>(a.gamma, h0, a.hidden, v.gamma);
+        if (a.residual != nullptr) load_raw<T, kTail, kShort>(a.residual + row * a.rs, h0, a.hidden, v.res);
       }
-      load_raw<T, kTail>(x, h0, a.hidden, v.x);
+      load_raw<T, kTail, kShort>(x, h0, a.hidden, v.x);
     };
     // The values that r and the scale apply to, s gamma or x, with their part of the reductions.
     float ss = 0.0f;
     uint32_t m = 0;
     auto gather = [&](int32_t h0, const Run& v, float (&f)[8], bool store_sum) {
-      widen_raw(v.x, f);
+      widen_raw<T, kTail, kShort>(v.x, h0, a.hidden, f);
       if constexpr (kNorm) {
         float g[8];
         if (a.residual != nullptr) {
-          widen_raw(v.res, g);
+          widen_raw<T, kTail, kShort>(v.res, h0, a.hidden, g);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] += g[i];
           if (store_sum) store_run<T, kTail>(a.residual_out + row * a.ros, h0, a.hidden, f);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(f[i], f[i], ss);
-        widen_raw(v.gamma, g);
+        widen_raw<Gamma, kTail, kShort>(v.gamma, h0, a.hidden, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= g[i];
       }

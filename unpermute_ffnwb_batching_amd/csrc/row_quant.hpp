@@ -18,37 +18,39 @@ typedef uint16_t u16_a1 __attribute__((aligned(1)));
 // The bytes of 8 elements: one 16-byte register group, or two of FP32.
 template <class T> struct Raw { u32x4 v[T::kBytes / 2]; };
 
-// Elements h0 .. h0 + 7 of a row (h0 a multiple of 8, below hidden), zeros past its end.  kTail: hidden
-// may be no multiple of 8.
-template <class T, bool kTail>
+// Elements h0 .. h0 + 7 of a row (h0 a multiple of 8, below hidden).  kTail: hidden may be no multiple of 8;
+// the run that passes the row's end holds its last 8 elements instead, for widen_raw to shift.  kShort: hidden
+// may be below 8; such rows are read one by one, zeros behind them.
+template <class T, bool kTail, bool kShort>
 __device__ __forceinline__ void load_raw(const char* row, int32_t h0, int32_t hidden, Raw<T>& out) {
   constexpr int W = T::kBytes * 2;  // registers of 8 elements
-  const char* p = row + static_cast<int64_t>(h0) * T::kBytes;
-  if (!kTail || h0 + 8 <= hidden) {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i) out.v[i] = reinterpret_cast<const u32x4_a1*>(p)[i];
-    return;
-  }
-  const int32_t left = hidden % 8;  // = hidden - h0, the same for every row
-  uint32_t w[W];
-  if (hidden < 8) {  // a row of fewer than 8 elements: one by one
-#pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = 0;
+  if (kShort && hidden < 8) {
+    uint32_t w[W] = {};
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-      if (i < left) {
-        if constexpr (T::kBytes == 2) w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i % 2));
-        else w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      if (i < hidden) {
+        if constexpr (T::kBytes == 2) w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[i]) << (16 * (i % 2));
+        else w[i] = reinterpret_cast<const uint32_t*>(row)[i];
       }
-  } else {  // the row's last 8, shifted down by those that the runs before hold
-    const int32_t down = 8 - left;  // elements
-    const char* e = p - down * T::kBytes;
 #pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const u32x4 v = reinterpret_cast<const u32x4_a1*>(e)[i];
+    for (int i = 0; i < W / 4; ++i) out.v[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    return;
+  }
+  const char* p = row + static_cast<int64_t>(kTail ? min(h0, hidden - 8) : h0) * T::kBytes;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
-    }
+  for (int i = 0; i < W / 4; ++i) out.v[i] = reinterpret_cast<const u32x4_a1*>(p)[i];
+}
+
+// The elements that load_raw read, zeros past the row's end.
+template <class T, bool kTail, bool kShort>
+__device__ __forceinline__ void widen_raw(const Raw<T>& r, int32_t h0, int32_t hidden, float (&f)[8]) {
+  constexpr int W = T::kBytes * 2;
+  uint32_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = r.v[i / 4][i % 4];
+  if (kTail && h0 + 8 > hidden && (!kShort || hidden >= 8)) {
+    // the row's last 8, shifted down by those that the runs before hold: as many in every row
+    const int32_t down = 8 - hidden % 8;
 #pragma unroll
     for (int s = W / 2; s > 0; s >>= 1)  // by whole registers: s, s / 2, ... 1
       if (down * T::kBytes / 4 & s) {
@@ -62,17 +64,11 @@ __device__ __forceinline__ void load_raw(const char* row, int32_t h0, int32_t hi
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < W / 4; ++i) out.v[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
-}
-
-template <class T>
-__device__ __forceinline__ void widen_raw(const Raw<T>& r, float (&f)[8]) {
   if constexpr (T::kBytes == 2) {
-    Chunk<T>::widen(r.v[0], f);
+    Chunk<T>::widen(u32x4{w[0], w[1], w[2], w[3]}, f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.v[i / 4][i % 4]);
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
   }
 }
 

@@ -368,8 +368,9 @@ __device__ __forceinline__ void mm8_tile(const Mm8Args& a, const RowTile& rt, in
 }
 
 // Tiles of at most half the rows (the last one of a group, the halves of find_tile) take half the
-// fragments.  Two workgroups of 64 rows share a CU: 4 waves to a SIMD, 128 registers (16189 rows by 7922
-// columns over 1216, FP32: 319 us, 380 with 135 registers).
+// fragments.  Two workgroups of 64 rows share a CU: 4 waves to a SIMD, 128 registers, for which 5 of the kernel
+// with FP32 results pass through memory (24 bytes a lane; 16189 rows by 7922 columns over 1216, FP32: 319 us,
+// 380 with 135 registers and none in memory).
 template <class T, int EPI, int WM, int WN, int MF>
 __global__ __launch_bounds__(WM* WN* kWave, MF == 2 && WM == 2 ? 4 : 2) void mm8_tile_kernel(Mm8Args a) {
   extern __shared__ __align__(16) char lds8[];

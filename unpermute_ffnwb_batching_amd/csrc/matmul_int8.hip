@@ -18,8 +18,9 @@ namespace ffnwb {
 // Why through LDS although no wave shares its blocks: a matrix operand has 16 rows in adjacent lanes,
 // and loads in that order move 38 GB/s per CU, a lane each cycle; copies of whole lines to LDS move 125 to
 // 150.  More buffers gained nothing.  Over 7168: 1 row by 4096 columns 6.7 us (7.6 with loads to registers), which is
-// 4.4 TB/s with the launch, 16 rows 7.1 us (9.3), 64 rows 8.5 us (18.7); 256 rows by 2048 11.3 us (33.8): there the copies, from L2,
-// and the reads of the fragments keep LDS busy.
+// 4.4 TB/s with the launch, 16 rows 7.1 us (9.3), 64 rows 8.5 us (21.4); 256 rows by 2048 11.3 us (33.8); 1024 rows 28.1 us,
+// 61 GB/s of copies per CU.  What bounds the last two is not known: LDS reads are 11% to 18% of a CU's busy cycles, without
+// bank conflicts, and waits for them few.
 
 // Bytes of LDS of a wave, and the most waves of a workgroup.
 constexpr int direct_lds(int mt, int nf) { return 2 * (mt + nf) * 2048; }

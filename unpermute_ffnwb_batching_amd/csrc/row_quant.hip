@@ -6,14 +6,15 @@
 // |s gamma| times r (rounding is monotonic), and the sum of squares and that maximum travel together.
 //
 // Bound by memory, at the rate of a copy (4.9 TB/s read and written) or over it: 4608 rows of 7168 BF16
-// with their residual take 46 us to INT8 and 49 us to e4m3 (231 MB), without a norm 19 us (99 MB); 16384
-// rows of 4096 with their residual 81 us (470 MB).  One row of 7168: 3.6 us, without a norm 2.4, most of
-// it the launch.  What was worth it: all loads of a thread ahead of the first use, and registers few
+// with their residual take 46 us to INT8 and 49 us to e4m3 (231 MB), without a norm 21 us (99 MB; 17 with two
+// sets of rows in turn, which the Infinity Cache holds in part); 16384 rows of 4096 with their residual 81 us
+// (470 MB).  One row of 7168: 3.6 us, without a norm 2.4, most of it the launch.  What was worth it: all loads of a thread ahead of the first use, and registers few
 // enough for 7 waves (gamma's type and rows of whole runs known to the compiler: 67 -> 46 us); reductions
 // through the data path instead of LDS.
 //
-// Rows that are not whole runs of 8 elements start at any address: 4608 of 7167 BF16 take 62 us to INT8 and 63 to
-// e4m3, of 7164 (addresses of 8 bytes) 51, without a norm 18.  The row's end is read where the run before it
+// Rows that are not whole runs of 8 elements start at any address: 4608 of 7167 BF16 take 63 us to INT8 and to
+// e4m3, of 7164 (rows at multiples of 8 bytes) 51, without a norm both 18: the rest over 46 is the norm's six
+// accesses a run that straddle lines.  The row's end is read where the run before it
 // ends, without a branch: with one, the loads of a thread's runs waited for each other (64, 72 and 57 us; 16384 rows of
 // 4095 129 instead of 108).
 #include <type_traits>

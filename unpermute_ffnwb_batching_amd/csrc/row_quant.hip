@@ -217,7 +217,9 @@ static bool launch_shape(const RowArgs& a, hipStream_t s, void* b, void* e) {
   auto threads = [&](int64_t c) { return ((runs + c - 1) / c + kWave - 1) / kWave * kWave; };
   if (runs <= 16) return launch_rows<T, G, kInt8, kTail, 1, 16>(a, 256, s, b, e);
   if (runs <= 64) return launch_rows<T, G, kInt8, kTail, 1, 64>(a, 256, s, b, e);
-  if (!std::is_void<G>::value && runs <= 512) return launch_rows<T, G, kInt8, kTail, 1, 0>(a, threads(1), s, b, e);
+  if constexpr (!std::is_void<G>::value) {
+    if (runs <= 512) return launch_rows<T, G, kInt8, kTail, 1, 0>(a, threads(1), s, b, e);
+  }
   if (runs <= 2048) return launch_rows<T, G, kInt8, kTail, 2, 0>(a, threads(2), s, b, e);
   return launch_rows<T, G, kInt8, kTail, 0, 0>(a, 1024, s, b, e);
 }
